@@ -1,8 +1,10 @@
 /*
  * ln.h -- C ABI of the GB300 (sm_103a) fused residual-add + LayerNorm library (libln.so),
  * with the bias + dropout + residual prologue (ln_fwd_bias_dropout_*, ln_dropout_bwd_*), the
- * fused residual-add + RMSNorm (ln_rms_*), the fused row softmax (ln_softmax_*) and the fused
- * cross-entropy (ln_xent_*) alongside.
+ * fused residual-add + RMSNorm (ln_rms_*), the fused row softmax (ln_softmax_*), the fused
+ * cross-entropy (ln_xent_*) and the operators over rows of logits -- token log probabilities with
+ * their gradient (ln_logprobs_*) and distillation from a teacher's top logits (ln_distill_*) --
+ * alongside.
  *
  * The library computes, for a row-major [rows, cols] problem:
  *
@@ -298,6 +300,114 @@ ln_status ln_xent_f32(const float* logits, const int32_t* targets, int64_t rows,
 ln_status ln_xent_bf16(const ln_bf16* logits, const int32_t* targets, int64_t rows, int64_t V,
                        float alpha, float dloss, float* losses, ln_bf16* dlogits,
                        ln_stream_t stream);
+
+/*
+ * Log probabilities of given tokens over rows of logits, with the entropy, the token's rank and
+ * the top alternatives, in one read of the logits.  For each row r of V logits x with token t:
+ *
+ *   z = scale * x,  L = log sum_j exp z_j,  q = exp(z - L)
+ *   logp[r] = z_t - L,  entropy[r] = -sum_j q_j log q_j,  lse[r] = L
+ *   ranks[r] = 1 + the number of logits greater than x_t
+ *   top_ids[r], top_logp[r]: the columns of the `top` largest logits, the largest first, equal
+ *     ones by the lowest column, and their z - L.  A logit of -inf (a word that a mask has
+ *     removed) or NaN is no alternative: places beyond the others hold id -1 and -inf.
+ *
+ *   logits    [rows, V], row r at logits + r * ld (ld >= V; rows of a padded vocabulary, say)
+ *   tokens    [rows] int32, or NULL (then logp and ranks must be NULL).  A negative token is no
+ *             token (a padded position): logp 0, rank 0.  One of V or more: logp NaN, rank 0.
+ *   scale     1 / temperature, finite and > 0
+ *   top       0 <= top <= LN_MAX_TOP; more than V is allowed
+ *   logp      [rows] fp32        may be NULL
+ *   entropy   [rows] fp32        may be NULL
+ *   lse       [rows] fp32        may be NULL
+ *   ranks     [rows] int32       may be NULL
+ *   top_ids   [rows, top] int32  required when top > 0
+ *   top_logp  [rows, top] fp32   required when top > 0
+ *
+ * At least one output must be given.  A logit of -inf has probability 0 and adds nothing to the
+ * entropy.  A row that holds NaN or +inf has no distribution, nor has one whose logits are all
+ * -inf: its logp and entropy are NaN (lse is -inf for the latter).  Outputs must not overlap the
+ * inputs.  Limits: 1 <= V <= LN_XENT_MAX_V, 0 <= rows <= LN_MAX_ROWS.  Other conventions and
+ * errors as for ln_fwd_*; nothing is allocated, and results are bitwise repeatable.
+ */
+#define LN_MAX_TOP 256
+
+ln_status ln_logprobs_f32(const float* logits, int64_t ld, const int32_t* tokens, int64_t rows,
+                          int64_t V, float scale, int64_t top, float* logp, float* entropy,
+                          float* lse, int32_t* ranks, int32_t* top_ids, float* top_logp,
+                          ln_stream_t stream);
+
+ln_status ln_logprobs_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tokens, int64_t rows,
+                           int64_t V, float scale, int64_t top, float* logp, float* entropy,
+                           float* lse, int32_t* ranks, int32_t* top_ids, float* top_logp,
+                           ln_stream_t stream);
+
+/*
+ * Gradient of the log probabilities and the entropies with respect to the logits:
+ *
+ *   dx_j = scale * (dlogp[r] (1[j = t] - q_j) - dentropy[r] q_j (log q_j + entropy[r]))
+ *
+ *   logits, ld, tokens, scale   as the forward had them
+ *   lse        [rows] fp32  as written by the forward
+ *   entropy    [rows] fp32  as written by the forward; may be NULL when dentropy is
+ *   dlogp      [rows] fp32  upstream gradient of logp; may be NULL (tokens may then be NULL)
+ *   dentropy   [rows] fp32  upstream gradient of entropy; may be NULL (not both)
+ *   dlogits    [rows, V], row r at dlogits + r * ldd (ldd >= V); written (columns V .. ldd of a
+ *              row are left as they are); may be the logits themselves, with ldd = ld
+ *
+ * A row without a token has no gradient of logp.  A row whose upstream gradients are both 0
+ * has gradient 0 whatever its logits hold (they are not used); a token of V or more gives a row
+ * of NaN.  Conventions, limits and errors as for ln_logprobs_*; nothing is allocated.
+ */
+ln_status ln_logprobs_bwd_f32(const float* logits, int64_t ld, const int32_t* tokens,
+                              const float* lse, const float* entropy, const float* dlogp,
+                              const float* dentropy, int64_t rows, int64_t V, float scale,
+                              float* dlogits, int64_t ldd, ln_stream_t stream);
+
+ln_status ln_logprobs_bwd_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tokens,
+                               const float* lse, const float* entropy, const float* dlogp,
+                               const float* dentropy, int64_t rows, int64_t V, float scale,
+                               ln_bf16* dlogits, int64_t ldd, ln_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits, loss and gradient in one kernel.  For each row r of V
+ * student logits x with the teacher's logits t_k of columns ids_k (k < K):
+ *
+ *   p_k = exp(scale t_k) / sum_k' exp(scale t_k')          over the row's entries
+ *   q = softmax(scale x)                                    over the whole row
+ *   losses[r] = w_r sum_k p_k (log p_k - log q_{ids_k})     (the Kullback-Leibler divergence)
+ *   dlogits_j = dloss * w_r * scale * (q_j - sum_{k: ids_k = j} p_k)
+ *
+ *   logits   [rows, V], row r at logits + r * ld (ld >= V)
+ *   ids      [rows, K] int32  columns of the teacher's entries, in any order; a negative one is no
+ *            entry (lists may be shorter than K); one named twice has both weights.  One of V or
+ *            more gives the row a NaN loss and gradient.
+ *   teacher  [rows, K] fp32   the teacher's logits there, or log probabilities: a constant per row
+ *            does not matter, so ln_logprobs_*'s top_ids and top_logp (at scale 1) fit as they are
+ *   weights  [rows] fp32      or NULL (all 1); rows of weight 0 are left out of the loss
+ *   scale                     1 / temperature of both sides, finite and > 0 (the customary factor
+ *                             temperature^2 of the loss belongs into dloss)
+ *   dloss                     factor of the gradient (1 / rows for a mean over rows), finite
+ *   losses   [rows] fp32      written; may be NULL
+ *   dlogits  [rows, V], row r at dlogits + r * ldd (ldd >= V); written (columns V .. ldd of a row
+ *            are left as they are); may be NULL; may be the logits themselves, with ldd = ld
+ *
+ * At least one of losses and dlogits must be given.  A row without entries (or with teacher logits
+ * of -inf only), or of weight 0, has loss 0 and gradient 0 whatever its logits hold (they are not
+ * read).  An entry of weight p_k = 0 adds nothing, even where the student has -inf; elsewhere a
+ * student's -inf gives an infinite loss.  Limits: 1 <= K <= LN_MAX_TOP, 1 <= V <= LN_XENT_MAX_V,
+ * 0 <= rows <= LN_MAX_ROWS.  Other conventions and errors as for ln_fwd_*; nothing is allocated,
+ * and results are bitwise repeatable.
+ */
+ln_status ln_distill_f32(const float* logits, int64_t ld, const int32_t* ids, const float* teacher,
+                         const float* weights, int64_t rows, int64_t V, int64_t K, float scale,
+                         float dloss, float* losses, float* dlogits, int64_t ldd,
+                         ln_stream_t stream);
+
+ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
+                          const float* teacher, const float* weights, int64_t rows, int64_t V,
+                          int64_t K, float scale, float dloss, float* losses, ln_bf16* dlogits,
+                          int64_t ldd, ln_stream_t stream);
 
 /*
  * LayerNorm forward with the bias + dropout + residual prologue fused in ("Accelerating

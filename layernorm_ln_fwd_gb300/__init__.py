@@ -10,12 +10,15 @@ Forward (``fwd``): s = x + res is written as ``res_out``; out = gamma * (s - mu)
 with per-row fp32 ``mean`` and ``rstd``.  Backward (``bwd``): dx with respect to s (hence to
 both x and res), dgamma and dbeta, the latter bitwise reproducible.  ``rms_fwd`` and
 ``rms_bwd`` do the same for the fused residual-add + RMSNorm ("GPU Performance from First
-Principles", section 6.1).  Definitions:
+Principles", section 6.1).  Over rows of logits, beside ``xent``: ``logprobs`` (token log
+probabilities, entropy, rank, top alternatives), its gradient ``logprobs_bwd`` and ``distill``
+(loss and gradient against a teacher's top logits).  Definitions:
 "Accelerating Transformer on GPU (II): Training with LightSeq2", sections 2.1, 2.2 and 2.4;
 residual fusion as in "llm.c: the llmc/ CUDA kernel layer", section 3.2.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -26,6 +29,7 @@ LIB_PATH = os.path.join(_HERE, "libln.so")
 STATUS = {0: "LN_OK", 1: "LN_EINVAL", 2: "LN_EALIGN", 3: "LN_EUNSUPPORTED", 4: "LN_ECUDA",
           5: "LN_ETIMEOUT", 6: "LN_ENOSPACE"}
 MAX_COLS = 16384
+MAX_TOP = 256
 PATH_AUTO, PATH_WARP, PATH_BLOCK, PATH_SCALAR = 0, 1, 2, 3
 
 # Every symbol include/ln.h declares, with its ctypes signature.
@@ -64,6 +68,12 @@ SIGNATURES = {
     "ln_softmax_bwd_bf16": (_INT, [_P, _P, _F, _I64, _I64, _P, _P]),
     "ln_xent_f32": (_INT, [_P, _P, _I64, _I64, _F, _F, _P, _P, _P]),
     "ln_xent_bf16": (_INT, [_P, _P, _I64, _I64, _F, _F, _P, _P, _P]),
+    "ln_logprobs_f32": (_INT, [_P, _I64, _P, _I64, _I64, _F, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "ln_logprobs_bf16": (_INT, [_P, _I64, _P, _I64, _I64, _F, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "ln_logprobs_bwd_f32": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, _I64, _P]),
+    "ln_logprobs_bwd_bf16": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, _I64, _P]),
+    "ln_distill_f32": (_INT, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _F, _P, _P, _I64, _P]),
+    "ln_distill_bf16": (_INT, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _F, _P, _P, _I64, _P]),
     "ln_fwd_bias_dropout_f32": (_INT, [_P, _P, _P, _P, _P, _F, _F, _U64, _U64, _I64, _I64, _P, _P,
                                        _P, _P, _P]),
     "ln_fwd_bias_dropout_bf16": (_INT, [_P, _P, _P, _P, _P, _F, _F, _U64, _U64, _I64, _I64, _P,
@@ -373,6 +383,181 @@ def xent(logits, targets, alpha: float = 0.0, dloss: float = 1.0, losses=None, d
     name = f"ln_xent_{sfx}"
     _check(name, getattr(lib(), name)(_ptr(logits), _ptr(targets), rows, V, float(alpha),
                                       float(dloss), _ptr(losses), _ptr(dlogits), _stream(stream)))
+    return losses, dlogits
+
+
+def _rows_of(t, name, device=None):
+    """(rows, V, ld) of a 2-D tensor whose rows are contiguous, ld >= V elements apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [rows, V]")
+    rows, V = t.shape
+    ld, step = t.stride()
+    if step != 1 and V > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows < 2:
+        ld = V
+    if ld < V:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return rows, V, ld
+
+
+def _gradient_of(logits, dlogits, in_place):
+    """The gradient's tensor: the logits, the caller's, or a new one whose rows are as far apart
+    as those of the logits (so a padded vocabulary's gradient has the padding too)."""
+    import torch
+    if in_place:
+        if dlogits is not None and dlogits is not logits:
+            raise ValueError("in_place and dlogits exclude each other")
+        return logits
+    if dlogits is None:
+        rows, V, ld = _rows_of(logits, "logits")
+        if ld == V:
+            return torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
+        return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :V]
+    if dlogits.device != logits.device:
+        raise ValueError(f"dlogits is on {dlogits.device}, expected {logits.device}")
+    if dlogits.dtype != logits.dtype:
+        raise TypeError(f"dlogits has dtype {dlogits.dtype}, expected {logits.dtype}")
+    if dlogits.shape != logits.shape:
+        raise ValueError(f"dlogits has shape {tuple(dlogits.shape)}, expected {tuple(logits.shape)}")
+    return dlogits
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """A context in which ``device`` is current, and ``stream`` if one is given (so that what a
+    call allocates belongs to the stream that writes it)."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _HERE_ALREADY
+
+
+def _new(shape, dtype, device, given, name, wanted=True):
+    import torch
+    if given is not None:
+        return _need(given, name, shape, dtype, device)
+    return torch.empty(shape, dtype=dtype, device=device) if wanted else None
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy: bool = True,
+             want_ranks: bool = False, logp=None, entropy=None, lse=None, ranks=None, top_ids=None,
+             top_logp=None, stream=None):
+    """Log probabilities of given tokens over rows of logits.  logits: [rows, V], rows contiguous
+    (a view into a padded vocabulary is fine); tokens: int32 [rows] (negative: no token), or None;
+    scale: 1 / temperature; top: number of alternatives, at most ``MAX_TOP``.
+
+    Returns (logp, entropy, lse, ranks, top_ids, top_logp): with L = logsumexp(scale * logits) per
+    row, logp = scale * logits[token] - L, entropy = -sum q log q with q = softmax(scale * logits),
+    lse = L, ranks = 1 + the number of larger logits, top_ids and top_logp ([rows, top]) the
+    largest logits' columns (ties by the lowest; -1 past the last logit above -inf) and log
+    probabilities.  What is not asked for is None: logp without tokens, entropy without
+    ``want_entropy``, ranks without ``want_ranks``, the alternatives with top = 0."""
+    import torch
+    rows, V, ld = _rows_of(logits, "logits")
+    sfx = _suffix(logits.dtype)
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    if tokens is not None:
+        _need(tokens, "tokens", (rows,), i32, dev)
+    elif want_ranks or logp is not None or ranks is not None:
+        raise ValueError("tokens are required for logp and ranks")
+    if not top and (top_ids is not None or top_logp is not None):
+        raise ValueError("top_ids and top_logp need top > 0")
+    if top < 0:
+        raise ValueError("top must be at least 0")
+    with _on(dev, stream):
+        logp = _new((rows,), f32, dev, logp, "logp", tokens is not None)
+        entropy = _new((rows,), f32, dev, entropy, "entropy", want_entropy)
+        lse = _new((rows,), f32, dev, lse, "lse")
+        ranks = _new((rows,), i32, dev, ranks, "ranks", want_ranks)
+        top_ids = _new((rows, top), i32, dev, top_ids, "top_ids", top > 0)
+        top_logp = _new((rows, top), f32, dev, top_logp, "top_logp", top > 0)
+        name = "ln_logprobs_" + sfx
+        _check(name, getattr(lib(), name)(
+            logits.data_ptr(), ld, _addr(tokens), rows, V, float(scale), int(top), _addr(logp), _addr(entropy),
+            lse.data_ptr(), _addr(ranks), _addr(top_ids), _addr(top_logp),
+            torch.cuda.current_stream(dev).cuda_stream))
+    return logp, entropy, lse, ranks, top_ids, top_logp
+
+
+def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, scale: float = 1.0,
+                 dlogits=None, in_place: bool = False, stream=None):
+    """Gradient of :func:`logprobs`: scale * (dlogp (onehot(token) - q) - dentropy q (log q +
+    entropy)) with q = softmax(scale * logits).  lse and entropy (needed with dentropy): the
+    forward's; dlogp, dentropy: fp32 [rows], at least one of them.  Rows whose upstream gradients
+    are 0 get 0 whatever they hold.  Returns dlogits; ``in_place`` writes it over the logits."""
+    import torch
+    rows, V, ld = _rows_of(logits, "logits")
+    sfx = _suffix(logits.dtype)
+    dev = logits.device
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        if t is not None:
+            _need(t, name, (rows,), torch.float32, dev)
+    if lse is None:
+        raise ValueError("lse is required")
+    if dlogp is None and dentropy is None:
+        raise ValueError("dlogp or dentropy is required")
+    if dentropy is not None and entropy is None:
+        raise ValueError("entropy is required with dentropy")
+    if tokens is not None:
+        _need(tokens, "tokens", (rows,), torch.int32, dev)
+    elif dlogp is not None:
+        raise ValueError("tokens are required with dlogp")
+    with _on(dev, stream):
+        dlogits = _gradient_of(logits, dlogits, in_place)
+        name = "ln_logprobs_bwd_" + sfx
+        _check(name, getattr(lib(), name)(
+            logits.data_ptr(), ld, _addr(tokens), lse.data_ptr(), _addr(entropy), _addr(dlogp),
+            _addr(dentropy), rows, V, float(scale), dlogits.data_ptr(), _rows_of(dlogits, "dlogits")[2],
+            torch.cuda.current_stream(dev).cuda_stream))
+    return dlogits
+
+
+def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float = 1.0, losses=None,
+            dlogits=None, want_losses: bool = True, want_grad: bool = True, in_place: bool = False,
+            stream=None):
+    """Distillation from a teacher's top logits.  logits: the student's, [rows, V], rows
+    contiguous; ids: int32 [rows, K], the columns of the teacher's entries (negative: no entry);
+    teacher: fp32 [rows, K], its logits there or log probabilities (:func:`logprobs`'s top_ids and
+    top_logp fit); weights: fp32 [rows] or None; scale: 1 / temperature of both sides.
+
+    Returns (losses, dlogits): with p = softmax(scale * teacher) over a row's entries and q =
+    softmax(scale * logits), losses = weights * sum p (log p - log q[ids]) and dlogits = dloss *
+    weights * scale * (q - p at the ids).  ``in_place`` writes the gradient over the logits."""
+    import torch
+    rows, V, ld = _rows_of(logits, "logits")
+    sfx = _suffix(logits.dtype)
+    dev = logits.device
+    if ids is None or ids.dim() != 2:
+        raise ValueError("ids must be 2-D [rows, K]")
+    K = ids.shape[1]
+    _need(ids, "ids", (rows, K), torch.int32, dev)
+    _need(teacher, "teacher", (rows, K), torch.float32, dev)
+    if weights is not None:
+        _need(weights, "weights", (rows,), torch.float32, dev)
+    with _on(dev, stream):
+        losses = _new((rows,), torch.float32, dev, losses, "losses", want_losses)
+        if want_grad or in_place or dlogits is not None:
+            dlogits = _gradient_of(logits, dlogits, in_place)
+        name = "ln_distill_" + sfx
+        _check(name, getattr(lib(), name)(
+            logits.data_ptr(), ld, ids.data_ptr(), teacher.data_ptr(), _addr(weights), rows, V, K,
+            float(scale), float(dloss), _addr(losses), _addr(dlogits),
+            V if dlogits is None else _rows_of(dlogits, "dlogits")[2],
+            torch.cuda.current_stream(dev).cuda_stream))
     return losses, dlogits
 
 

@@ -384,6 +384,126 @@ ln_status xent_impl(Dtype dt, const T* logits, const int32_t* targets, int64_t r
 
 namespace lnk {
 namespace {
+// Sizes shared by the operators over rows of logits.
+ln_status check_logits(int64_t ld, int64_t rows, int64_t V, float scale) {
+    if (!std::isfinite(scale) || scale <= 0.f) return LN_EINVAL;
+    if (rows < 0 || V <= 0 || ld < V) return LN_EINVAL;
+    if (rows > LN_MAX_ROWS || V > LN_XENT_MAX_V) return LN_EUNSUPPORTED;
+    // A row's address must stay within 63 bits of byte offset.
+    if (rows > 1 && ld > INT64_MAX / 4 / rows) return LN_EINVAL;
+    return LN_OK;
+}
+
+template <typename T>
+ln_status logprobs_impl(Dtype dt, const T* logits, int64_t ld, const int32_t* tokens, int64_t rows,
+                        int64_t V, float scale, int64_t top, float* logp, float* entropy,
+                        float* lse, int32_t* ranks, int32_t* top_ids, float* top_logp,
+                        ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_logits(ld, rows, V, scale);
+    if (st != LN_OK) return st;
+    if (top < 0) return LN_EINVAL;
+    if (top > LN_MAX_TOP) return LN_EUNSUPPORTED;
+    if (rows == 0) return LN_OK;
+    if (!logits || (!tokens && (logp || ranks))) return LN_EINVAL;
+    if (top > 0 ? !top_ids || !top_logp : top_ids || top_logp) return LN_EINVAL;
+    if (!logp && !entropy && !lse && !ranks && !top_ids) return LN_EINVAL;
+    st = check_device();
+    if (st != LN_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    LogprobsArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.rows = (int)rows;
+    a.V = (int)V;
+    a.scale = scale;
+    a.top = (int)top;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.ranks = ranks;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    int launches = 0;
+    cudaError_t e = launch_logprobs(dt, a, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+
+template <typename T>
+ln_status logprobs_bwd_impl(Dtype dt, const T* logits, int64_t ld, const int32_t* tokens,
+                            const float* lse, const float* entropy, const float* dlogp,
+                            const float* dentropy, int64_t rows, int64_t V, float scale,
+                            T* dlogits, int64_t ldd, ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_logits(ld, rows, V, scale);
+    if (st == LN_OK) st = check_logits(ldd, rows, V, scale);
+    if (st != LN_OK) return st;
+    if (rows == 0) return LN_OK;
+    if (!logits || !lse || !dlogits || (!dlogp && !dentropy)) return LN_EINVAL;
+    if ((dlogp && !tokens) || (dentropy && !entropy)) return LN_EINVAL;
+    if (logits == dlogits && ld != ldd && rows > 1) return LN_EINVAL;
+    st = check_device();
+    if (st != LN_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    LogprobsBwdArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.tokens = tokens;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.dlogp = dlogp;
+    a.dentropy = dentropy;
+    a.rows = (int)rows;
+    a.V = (int)V;
+    a.scale = scale;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    int launches = 0;
+    cudaError_t e = launch_logprobs_bwd(dt, a, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+
+template <typename T>
+ln_status distill_impl(Dtype dt, const T* logits, int64_t ld, const int32_t* ids,
+                       const float* teacher, const float* weights, int64_t rows, int64_t V,
+                       int64_t K, float scale, float dloss, float* losses, T* dlogits, int64_t ldd,
+                       ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_logits(ld, rows, V, scale);
+    if (st == LN_OK && dlogits) st = check_logits(ldd, rows, V, scale);
+    if (st != LN_OK) return st;
+    if (!std::isfinite(dloss) || K <= 0) return LN_EINVAL;
+    if (K > LN_MAX_TOP) return LN_EUNSUPPORTED;
+    if (rows == 0) return LN_OK;
+    if (!logits || !ids || !teacher || (!losses && !dlogits)) return LN_EINVAL;
+    if (logits == dlogits && ld != ldd && rows > 1) return LN_EINVAL;
+    st = check_device();
+    if (st != LN_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    DistillArgs a;
+    a.logits = logits;
+    a.ld = ld;
+    a.ids = ids;
+    a.teacher = teacher;
+    a.weights = weights;
+    a.rows = (int)rows;
+    a.V = (int)V;
+    a.K = (int)K;
+    a.scale = scale;
+    a.dloss = dloss;
+    a.losses = losses;
+    a.dlogits = dlogits;
+    a.ldd = ldd;
+    int launches = 0;
+    cudaError_t e = launch_distill(dt, a, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+}  // namespace
+}  // namespace lnk
+
+namespace lnk {
+namespace {
 template <typename T>
 ln_status dropout_bwd_impl(Dtype dt, const T* ds, float p, uint64_t seed, uint64_t offset,
                            int64_t rows, int64_t cols, T* dh, T* dbias, void* ws, size_t ws_bytes,
@@ -598,6 +718,57 @@ ln_status ln_xent_bf16(const ln_bf16* logits, const int32_t* targets, int64_t ro
     using B = __nv_bfloat16;
     return lnk::xent_impl<B>(Dtype::BF16, reinterpret_cast<const B*>(logits), targets, rows, V,
                              alpha, dloss, losses, reinterpret_cast<B*>(dlogits), stream);
+}
+
+ln_status ln_logprobs_f32(const float* logits, int64_t ld, const int32_t* tokens, int64_t rows,
+                          int64_t V, float scale, int64_t top, float* logp, float* entropy,
+                          float* lse, int32_t* ranks, int32_t* top_ids, float* top_logp,
+                          ln_stream_t stream) {
+    return lnk::logprobs_impl<float>(Dtype::F32, logits, ld, tokens, rows, V, scale, top,
+                                  logp, entropy, lse, ranks, top_ids, top_logp, stream);
+}
+
+ln_status ln_logprobs_bwd_f32(const float* logits, int64_t ld, const int32_t* tokens,
+                              const float* lse, const float* entropy, const float* dlogp,
+                              const float* dentropy, int64_t rows, int64_t V, float scale,
+                              float* dlogits, int64_t ldd, ln_stream_t stream) {
+    return lnk::logprobs_bwd_impl<float>(Dtype::F32, logits, ld, tokens, lse, entropy, dlogp,
+                                      dentropy, rows, V, scale, dlogits, ldd, stream);
+}
+
+ln_status ln_distill_f32(const float* logits, int64_t ld, const int32_t* ids, const float* teacher,
+                         const float* weights, int64_t rows, int64_t V, int64_t K, float scale,
+                         float dloss, float* losses, float* dlogits, int64_t ldd,
+                         ln_stream_t stream) {
+    return lnk::distill_impl<float>(Dtype::F32, logits, ld, ids, teacher, weights, rows, V, K,
+                                 scale, dloss, losses, dlogits, ldd, stream);
+}
+
+ln_status ln_logprobs_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tokens, int64_t rows,
+                          int64_t V, float scale, int64_t top, float* logp, float* entropy,
+                          float* lse, int32_t* ranks, int32_t* top_ids, float* top_logp,
+                          ln_stream_t stream) {
+    using B = __nv_bfloat16;
+    return lnk::logprobs_impl<B>(Dtype::BF16, reinterpret_cast<const B*>(logits), ld, tokens, rows, V, scale, top,
+                                  logp, entropy, lse, ranks, top_ids, top_logp, stream);
+}
+
+ln_status ln_logprobs_bwd_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tokens,
+                              const float* lse, const float* entropy, const float* dlogp,
+                              const float* dentropy, int64_t rows, int64_t V, float scale,
+                              ln_bf16* dlogits, int64_t ldd, ln_stream_t stream) {
+    using B = __nv_bfloat16;
+    return lnk::logprobs_bwd_impl<B>(Dtype::BF16, reinterpret_cast<const B*>(logits), ld, tokens, lse, entropy, dlogp,
+                                      dentropy, rows, V, scale, reinterpret_cast<B*>(dlogits), ldd, stream);
+}
+
+ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids, const float* teacher,
+                         const float* weights, int64_t rows, int64_t V, int64_t K, float scale,
+                         float dloss, float* losses, ln_bf16* dlogits, int64_t ldd,
+                         ln_stream_t stream) {
+    using B = __nv_bfloat16;
+    return lnk::distill_impl<B>(Dtype::BF16, reinterpret_cast<const B*>(logits), ld, ids, teacher, weights, rows, V, K,
+                                 scale, dloss, losses, reinterpret_cast<B*>(dlogits), ldd, stream);
 }
 
 ln_status ln_fwd_bias_dropout_f32(const float* h, const float* bias, const float* res,

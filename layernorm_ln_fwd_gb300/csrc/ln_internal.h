@@ -180,6 +180,69 @@ struct XentArgs {
 cudaError_t launch_xent(Dtype dt, const XentArgs& a, bool aligned, cudaStream_t stream,
                         int* launches);
 
+// Token log probabilities with entropy, rank and top alternatives (null outputs are left out;
+// `tokens` null: no logp and no ranks; `top` 0: no alternatives).
+struct LogprobsArgs {
+    const void* logits;
+    int64_t ld;
+    const int* tokens;
+    int rows;
+    int V;
+    float scale;
+    int top;
+    float* logp;
+    float* entropy;
+    float* lse;
+    int* ranks;
+    int* top_ids;
+    float* top_logp;
+};
+
+cudaError_t launch_logprobs(Dtype dt, const LogprobsArgs& a, cudaStream_t stream, int* launches);
+
+// Their gradient (dlogp or dentropy may be null; dlogits may alias logits).
+struct LogprobsBwdArgs {
+    const void* logits;
+    int64_t ld;
+    const int* tokens;
+    const float* lse;
+    const float* entropy;
+    const float* dlogp;
+    const float* dentropy;
+    int rows;
+    int V;
+    float scale;
+    void* dlogits;
+    int64_t ldd;
+};
+
+cudaError_t launch_logprobs_bwd(Dtype dt, const LogprobsBwdArgs& a, cudaStream_t stream,
+                                int* launches);
+
+// Distillation from a teacher's top logits: losses (optional) and dlogits (optional; may alias
+// logits).
+struct DistillArgs {
+    const void* logits;
+    int64_t ld;
+    const int* ids;
+    const float* teacher;
+    const float* weights;
+    int rows;
+    int V;
+    int K;
+    float scale;
+    float dloss;
+    float* losses;
+    void* dlogits;
+    int64_t ldd;
+};
+
+cudaError_t launch_distill(Dtype dt, const DistillArgs& a, cudaStream_t stream, int* launches);
+
+// Whether rows of `lda` elements at a and of `ldb` at b start at the same place of a 16-byte vector,
+// every row of them.
+bool rows_congruent(const void* a, int64_t lda, const void* b, int64_t ldb, size_t esize, int rows);
+
 // Backward of the bias + dropout + residual prologue: dh = ds * keep * scale (keep from the
 // generator, or from the bits the forward stored) and the deterministic column sums dbias (partials: [segs][cols] (hi, lo) fp32 pairs that announce
 // themselves, left zero), in one cooperative launch.

@@ -14,7 +14,8 @@ same definitions live here:
 * ``ln_oracle.c`` (float64 C, OpenMP over rows; built into ``libln_oracle.so`` by
   :func:`build`) -- the oracle proper, fast enough for the full-size configurations;
 * ``numpy_ref.py`` (float64 NumPy, vectorised) -- a twin for small shapes, used to
-  cross-check the C code.
+  cross-check the C code, and the only oracle of the operators over rows of logits
+  (``logprobs``, ``logprobs_bwd``, ``distill``), pinned to torch's float64 autograd.
 
 Definitions followed (page titles and sections):
 
@@ -39,6 +40,7 @@ import threading
 import numpy as np
 
 from . import numpy_ref  # noqa: F401  (re-exported for tests)
+from .numpy_ref import distill, logprobs, logprobs_bwd  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _SRC = os.path.join(_HERE, "ln_oracle.c")

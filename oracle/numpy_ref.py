@@ -127,6 +127,106 @@ def xent(x, targets, alpha: float = 0.0, dloss: float = 1.0, io: str = "f64"):
     return {"loss": -(p * logq).sum(axis=1), "dx": round_io(dloss * (np.exp(logq) - p), io)}
 
 
+def _log_softmax(x, scale):
+    """(log q, L) of scale * x per row; a logit of -inf has q = 0, a row of none other has NaN.
+    log q is z - max z - log Z: z - L would lose log Z in a row masked by its type's lowest
+    value (-3.4e38) throughout, whose softmax is uniform."""
+    z = scale * np.asarray(x, dtype=np.float64)
+    m = z.max(axis=1, keepdims=True)
+    m = np.where(np.isinf(m) & (m < 0), 0.0, m)
+    with np.errstate(all="ignore"):
+        logZ = np.log(np.exp(z - m).sum(axis=1, keepdims=True))
+        return z - m - logZ, (m + logZ)[:, 0]
+
+
+def _times_log(q, logq):
+    """q * log q with 0 log 0 = 0 (NaN stays NaN)."""
+    with np.errstate(invalid="ignore"):
+        return np.where(q == 0, 0.0, q * logq)
+
+
+def logprobs(x, tokens=None, scale: float = 1.0, top: int = 0):
+    """Token log probabilities, entropy, log-sum-exp, ranks and top alternatives (the stated
+    definition of ``ln_logprobs_*``), by a full sort of every row."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, V = x.shape
+    logq, L = _log_softmax(x, scale)
+    out = {"lse": L, "entropy": -_times_log(np.exp(logq), logq).sum(axis=1), "logq": logq}
+    if tokens is not None:
+        t = np.asarray(tokens)
+        ok = (t >= 0) & (t < V)
+        at = np.where(ok, t, 0)
+        r = np.arange(rows)
+        out["logp"] = np.where(t < 0, 0.0, np.where(ok, logq[r, at], np.nan))
+        out["ranks"] = np.where(ok, 1 + (x > x[r, at][:, None]).sum(axis=1), 0)
+    if top:
+        ids = np.full((rows, top), -1)
+        lp = np.full((rows, top), -np.inf)
+        for r in range(rows):
+            order = np.argsort(-np.where(np.isnan(x[r]), -np.inf, x[r]), kind="stable")
+            order = order[x[r][order] > -np.inf][:top]
+            ids[r, : len(order)] = order
+            lp[r, : len(order)] = logq[r, order]
+        out["top_ids"], out["top_logp"] = ids, lp
+    return out
+
+
+def logprobs_bwd(x, tokens, lse, entropy=None, dlogp=None, dentropy=None, scale: float = 1.0,
+                 io: str = "f64"):
+    """Gradient of logp and entropy with respect to the logits, from the forward's lse and
+    entropy (the stated definition of ``ln_logprobs_bwd_*``)."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, V = x.shape
+    r = np.arange(rows)
+    zero = np.zeros(rows)
+    with np.errstate(all="ignore"):
+        logq = scale * x - np.asarray(lse, dtype=np.float64)[:, None]
+        q = np.exp(logq)
+        g = np.zeros((rows, V))
+        t = np.full(rows, -1) if tokens is None else np.asarray(tokens)
+        dl = zero if dlogp is None else np.where(t < 0, 0.0, np.asarray(dlogp, dtype=np.float64))
+        de = zero if dentropy is None else np.asarray(dentropy, dtype=np.float64)
+        g = -dl[:, None] * q
+        ok = (t >= 0) & (t < V)
+        g[r[ok], t[ok]] += dl[ok]
+        if dentropy is not None:
+            H = np.asarray(entropy, dtype=np.float64)[:, None]
+            g = g - de[:, None] * (_times_log(q, logq) + np.where(q == 0, 0.0, q * H))
+        if dlogp is not None:
+            g[t >= V] = np.nan
+    g[(dl == 0) & (de == 0)] = 0.0
+    return round_io(scale * g, io)
+
+
+def distill(x, ids, teacher, weights=None, scale: float = 1.0, dloss: float = 1.0, io: str = "f64"):
+    """Distillation from a teacher's top logits: the Kullback-Leibler divergence of the student
+    from the teacher's distribution over its entries, and its gradient (the stated definition
+    of ``ln_distill_*``)."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, V = x.shape
+    ids = np.asarray(ids)
+    w = np.ones(rows) if weights is None else np.asarray(weights, dtype=np.float64)
+    t = np.where(ids >= 0, np.asarray(teacher, dtype=np.float64), -np.inf)
+    loss, dx = np.zeros(rows), np.zeros((rows, V))
+    for r in range(rows):
+        bad = bool((ids[r] >= V).any())
+        if w[r] == 0 or (not bad and bool((t[r] == -np.inf).all())):
+            continue
+        if bad:
+            loss[r], dx[r] = np.nan, np.nan
+            continue
+        with np.errstate(all="ignore"):
+            logp, _ = _log_softmax(t[r : r + 1], scale)
+            logq, _ = _log_softmax(x[r : r + 1], scale)
+            p, q = np.exp(logp[0]), np.exp(logq[0])
+            for k in range(ids.shape[1]):
+                if ids[r, k] >= 0 and p[k] != 0:
+                    loss[r] += w[r] * p[k] * (logp[0, k] - logq[0, ids[r, k]])
+                    q[ids[r, k]] -= p[k]
+            dx[r] = dloss * w[r] * scale * q
+    return {"loss": loss, "dx": round_io(dx, io)}
+
+
 _M0, _M1, _W0, _W1 = 0xD2511F53, 0xCD9E8D57, 0x9E3779B9, 0xBB67AE85
 
 
