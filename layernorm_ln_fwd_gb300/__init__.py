@@ -386,7 +386,7 @@ def xent(logits, targets, alpha: float = 0.0, dloss: float = 1.0, losses=None, d
     return losses, dlogits
 
 
-def _rows_of(t, name, device=None):
+def _rows_of(t, name):
     """(rows, V, ld) of a 2-D tensor whose rows are contiguous, ld >= V elements apart."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D [rows, V]")
@@ -396,31 +396,31 @@ def _rows_of(t, name, device=None):
         raise ValueError(f"{name} must have contiguous rows")
     if rows < 2:
         ld = V
-    if ld < V:
+    elif ld < V:
         raise ValueError(f"{name} must have rows that do not overlap")
     return rows, V, ld
 
 
-def _gradient_of(logits, dlogits, in_place):
-    """The gradient's tensor: the logits, the caller's, or a new one whose rows are as far apart
-    as those of the logits (so a padded vocabulary's gradient has the padding too)."""
+def _gradient_of(logits, ld, dlogits, in_place):
+    """(tensor, ld) of the gradient: the logits, the caller's, or a new one whose rows are as far
+    apart as those of the logits (so a padded vocabulary's gradient has the padding too)."""
     import torch
     if in_place:
         if dlogits is not None and dlogits is not logits:
             raise ValueError("in_place and dlogits exclude each other")
-        return logits
+        return logits, ld
     if dlogits is None:
-        rows, V, ld = _rows_of(logits, "logits")
-        if ld == V:
-            return torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
-        return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :V]
+        if logits.is_contiguous():
+            return torch.empty_like(logits), ld
+        rows, V = logits.shape
+        return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :V], ld
     if dlogits.device != logits.device:
         raise ValueError(f"dlogits is on {dlogits.device}, expected {logits.device}")
     if dlogits.dtype != logits.dtype:
         raise TypeError(f"dlogits has dtype {dlogits.dtype}, expected {logits.dtype}")
     if dlogits.shape != logits.shape:
         raise ValueError(f"dlogits has shape {tuple(dlogits.shape)}, expected {tuple(logits.shape)}")
-    return dlogits
+    return dlogits, _rows_of(dlogits, "dlogits")[2]
 
 
 _HERE_ALREADY = contextlib.nullcontext()
@@ -441,11 +441,18 @@ def _on(device, stream):
     return _HERE_ALREADY
 
 
-def _new(shape, dtype, device, given, name, wanted=True):
+def _current_raw_stream(device):
+    """The handle of the device's current stream (without building a Stream object, 2 us, where
+    torch has a way)."""
     import torch
-    if given is not None:
-        return _need(given, name, shape, dtype, device)
-    return torch.empty(shape, dtype=dtype, device=device) if wanted else None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+
+
+def _entry(op: str, dtype):
+    """(name, function) of an entry point for the dtype."""
+    name = op + _suffix(dtype)
+    return name, getattr(lib(), name)
 
 
 def _addr(t):
@@ -466,30 +473,41 @@ def logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy
     probabilities.  What is not asked for is None: logp without tokens, entropy without
     ``want_entropy``, ranks without ``want_ranks``, the alternatives with top = 0."""
     import torch
+    empty, f32, i32 = torch.empty, torch.float32, torch.int32
     rows, V, ld = _rows_of(logits, "logits")
-    sfx = _suffix(logits.dtype)
+    name, fn = _entry("ln_logprobs_", logits.dtype)
     dev = logits.device
-    f32, i32 = torch.float32, torch.int32
     if tokens is not None:
         _need(tokens, "tokens", (rows,), i32, dev)
     elif want_ranks or logp is not None or ranks is not None:
         raise ValueError("tokens are required for logp and ranks")
-    if not top and (top_ids is not None or top_logp is not None):
-        raise ValueError("top_ids and top_logp need top > 0")
     if top < 0:
         raise ValueError("top must be at least 0")
+    if not top and (top_ids is not None or top_logp is not None):
+        raise ValueError("top_ids and top_logp need top > 0")
+    for t, what, shape, dt in ((logp, "logp", (rows,), f32), (entropy, "entropy", (rows,), f32),
+                               (lse, "lse", (rows,), f32), (ranks, "ranks", (rows,), i32),
+                               (top_ids, "top_ids", (rows, top), i32),
+                               (top_logp, "top_logp", (rows, top), f32)):
+        if t is not None:
+            _need(t, what, shape, dt, dev)
     with _on(dev, stream):
-        logp = _new((rows,), f32, dev, logp, "logp", tokens is not None)
-        entropy = _new((rows,), f32, dev, entropy, "entropy", want_entropy)
-        lse = _new((rows,), f32, dev, lse, "lse")
-        ranks = _new((rows,), i32, dev, ranks, "ranks", want_ranks)
-        top_ids = _new((rows, top), i32, dev, top_ids, "top_ids", top > 0)
-        top_logp = _new((rows, top), f32, dev, top_logp, "top_logp", top > 0)
-        name = "ln_logprobs_" + sfx
-        _check(name, getattr(lib(), name)(
-            logits.data_ptr(), ld, _addr(tokens), rows, V, float(scale), int(top), _addr(logp), _addr(entropy),
-            lse.data_ptr(), _addr(ranks), _addr(top_ids), _addr(top_logp),
-            torch.cuda.current_stream(dev).cuda_stream))
+        if logp is None and tokens is not None:
+            logp = empty(rows, dtype=f32, device=dev)
+        if entropy is None and want_entropy:
+            entropy = empty(rows, dtype=f32, device=dev)
+        if lse is None:
+            lse = empty(rows, dtype=f32, device=dev)
+        if ranks is None and want_ranks:
+            ranks = empty(rows, dtype=i32, device=dev)
+        if top:
+            if top_ids is None:
+                top_ids = empty((rows, top), dtype=i32, device=dev)
+            if top_logp is None:
+                top_logp = empty((rows, top), dtype=f32, device=dev)
+        _check(name, fn(logits.data_ptr(), ld, _addr(tokens), rows, V, float(scale), int(top),
+                        _addr(logp), _addr(entropy), lse.data_ptr(), _addr(ranks), _addr(top_ids),
+                        _addr(top_logp), _current_raw_stream(dev)))
     return logp, entropy, lse, ranks, top_ids, top_logp
 
 
@@ -501,11 +519,11 @@ def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, s
     are 0 get 0 whatever they hold.  Returns dlogits; ``in_place`` writes it over the logits."""
     import torch
     rows, V, ld = _rows_of(logits, "logits")
-    sfx = _suffix(logits.dtype)
+    name, fn = _entry("ln_logprobs_bwd_", logits.dtype)
     dev = logits.device
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+    for t, what in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
         if t is not None:
-            _need(t, name, (rows,), torch.float32, dev)
+            _need(t, what, (rows,), torch.float32, dev)
     if lse is None:
         raise ValueError("lse is required")
     if dlogp is None and dentropy is None:
@@ -517,12 +535,10 @@ def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, s
     elif dlogp is not None:
         raise ValueError("tokens are required with dlogp")
     with _on(dev, stream):
-        dlogits = _gradient_of(logits, dlogits, in_place)
-        name = "ln_logprobs_bwd_" + sfx
-        _check(name, getattr(lib(), name)(
-            logits.data_ptr(), ld, _addr(tokens), lse.data_ptr(), _addr(entropy), _addr(dlogp),
-            _addr(dentropy), rows, V, float(scale), dlogits.data_ptr(), _rows_of(dlogits, "dlogits")[2],
-            torch.cuda.current_stream(dev).cuda_stream))
+        dlogits, ldd = _gradient_of(logits, ld, dlogits, in_place)
+        _check(name, fn(logits.data_ptr(), ld, _addr(tokens), lse.data_ptr(), _addr(entropy),
+                        _addr(dlogp), _addr(dentropy), rows, V, float(scale), dlogits.data_ptr(), ldd,
+                        _current_raw_stream(dev)))
     return dlogits
 
 
@@ -539,7 +555,7 @@ def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float
     weights * scale * (q - p at the ids).  ``in_place`` writes the gradient over the logits."""
     import torch
     rows, V, ld = _rows_of(logits, "logits")
-    sfx = _suffix(logits.dtype)
+    name, fn = _entry("ln_distill_", logits.dtype)
     dev = logits.device
     if ids is None or ids.dim() != 2:
         raise ValueError("ids must be 2-D [rows, K]")
@@ -548,16 +564,17 @@ def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float
     _need(teacher, "teacher", (rows, K), torch.float32, dev)
     if weights is not None:
         _need(weights, "weights", (rows,), torch.float32, dev)
+    if losses is not None:
+        _need(losses, "losses", (rows,), torch.float32, dev)
     with _on(dev, stream):
-        losses = _new((rows,), torch.float32, dev, losses, "losses", want_losses)
+        if losses is None and want_losses:
+            losses = torch.empty(rows, dtype=torch.float32, device=dev)
+        ldd = V
         if want_grad or in_place or dlogits is not None:
-            dlogits = _gradient_of(logits, dlogits, in_place)
-        name = "ln_distill_" + sfx
-        _check(name, getattr(lib(), name)(
-            logits.data_ptr(), ld, ids.data_ptr(), teacher.data_ptr(), _addr(weights), rows, V, K,
-            float(scale), float(dloss), _addr(losses), _addr(dlogits),
-            V if dlogits is None else _rows_of(dlogits, "dlogits")[2],
-            torch.cuda.current_stream(dev).cuda_stream))
+            dlogits, ldd = _gradient_of(logits, ld, dlogits, in_place)
+        _check(name, fn(logits.data_ptr(), ld, ids.data_ptr(), teacher.data_ptr(), _addr(weights),
+                        rows, V, K, float(scale), float(dloss), _addr(losses), _addr(dlogits), ldd,
+                        _current_raw_stream(dev)))
     return losses, dlogits
 
 

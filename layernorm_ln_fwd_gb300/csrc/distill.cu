@@ -115,21 +115,11 @@ __global__ void __launch_bounds__(kDsThreads, 2) distill_kernel(const DsParams p
     RowSums<false> s;
     s.clear();
     const f2 c2 = f2_splat(p.c);
-    for (int v0 = tid; v0 < nvec; v0 += kDsUnroll * kDsThreads) {
-        uint4 u[kDsUnroll];
-#pragma unroll
-        for (int k = 0; k < kDsUnroll; ++k) {
-            const int v = v0 + k * kDsThreads;
-            if (v < nvec) u[k] = __ldcg(xv + v);
-        }
-#pragma unroll
-        for (int k = 0; k < kDsUnroll; ++k) {
-            if (v0 + k * kDsThreads >= nvec) break;
-            s.see(vector_max<T>(u[k]), p.c);
-            f2 x2[H];
-            PR::unpack(u[k], x2);
-            s.add(x2, c2);
-        }
+    for (int v0 = tid; v0 < nvec; v0 += kBatch * kDsThreads) {
+        uint4 u[kBatch];
+        load_batch<T>(u, xv, v0, kDsThreads, nvec);
+        if (s.see_batch<T>(u, p.c) > -INFINITY)
+            s.add_batch<T>(u, c2, [&](int k) { return u[k]; });
     }
     if (tid < cut.nloose()) s.add_one(IO::to_f(xr[cut.loose(tid)]), p.c);
     const RowTotal a = block_total({s.ref, f2_lo(s.z2) + f2_hi(s.z2), 0.f}, p.c, sh.total);

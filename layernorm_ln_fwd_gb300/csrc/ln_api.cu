@@ -1,5 +1,6 @@
 // ln_api.cu -- the C ABI declared in include/ln.h: argument checks, kernel selection,
 // backward workspaces and the per-device status word.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -24,6 +25,7 @@ std::mutex g_mu;
 std::map<int, DeviceInfo> g_devices;
 std::map<int, unsigned*> g_status_ptrs;
 std::map<std::tuple<int, const void*, int, size_t>, int> g_occupancy;
+std::map<std::pair<int, const void*>, size_t> g_smem_allowed;
 
 struct Workspace {
     void* ptr = nullptr;
@@ -115,6 +117,36 @@ cudaError_t launch_kernel(const void* kern, dim3 grid, dim3 block, size_t smem,
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+cudaError_t allow_smem(const void* kern, size_t bytes) {
+    const int dev = current_device();
+    std::lock_guard<std::mutex> lk(g_mu);
+    size_t& have = g_smem_allowed[std::make_pair(dev, kern)];
+    if (bytes <= std::max(have, (size_t)48 << 10)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) have = bytes;
+    return e;
+}
+
+cudaError_t launch_cluster(const void* kern, dim3 grid, dim3 block, int blocks, size_t smem,
+                           cudaStream_t stream, void** args) {
+    if (blocks <= 1) return launch_kernel(kern, grid, block, smem, stream, args, false);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)blocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 

@@ -100,6 +100,14 @@ bool vector_ok(Dtype dt, int cols, const void* const* ptrs, int nptrs);
 cudaError_t launch_kernel(const void* kern, dim3 grid, dim3 block, size_t smem,
                           cudaStream_t stream, void** args, bool cooperative);
 
+// Lets `kern` have `bytes` of dynamic shared memory on the current device (asked of the driver only
+// when it is more than before).
+cudaError_t allow_smem(const void* kern, size_t bytes);
+
+// The same with clusters of `blocks` blocks along the grid (1: none; up to 8).
+cudaError_t launch_cluster(const void* kern, dim3 grid, dim3 block, int blocks, size_t smem,
+                           cudaStream_t stream, void** args);
+
 cudaError_t launch_fwd(Dtype dt, const FwdArgs& a, bool aligned, int path_override,
                        cudaStream_t stream, int* launches);
 // The RMSNorm forward: `beta` and `mean` are unused (may be null); `rstd` receives 1 / rms.

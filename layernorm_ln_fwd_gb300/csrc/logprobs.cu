@@ -17,11 +17,11 @@ namespace lnk {
 namespace {
 
 constexpr int kLpMaxThreads = 512;
-constexpr int kLpUnroll = 4;        // 128-bit loads in flight per thread
-constexpr int kLpSegments = 2048;   // segments of a row at most (and one thread's share more)
-constexpr int kLpCand = 4096;       // candidates held at once
+constexpr int kLpSegments = 1024;   // segments of a slice, about
+constexpr int kLpCand = 1024;       // candidates held at once
 constexpr int kLpFlagged = 2 * LN_MAX_TOP;
 constexpr int kLpLoose = 16;        // at least 2 * (kVec - 1) loose elements of a row
+constexpr int kLpMaxCluster = 8;
 
 struct LpParams {
     const void* x;
@@ -29,8 +29,9 @@ struct LpParams {
     const int* tokens;
     int V;
     int top;
-    int seglen;   // vectors of a thread that share a segment
-    int nseg;     // segments of vectors: a multiple of the block's threads
+    int seg_shift;  // log2 of the vectors of a thread that share a segment (kBatch or more)
+    int nt_shift;   // log2 of the block's threads
+    int nseg;     // segments of batches: a multiple of the block's threads
     float scale, c;  // c = scale * log2 e
     float* logp;
     float* entropy;
@@ -43,202 +44,183 @@ struct LpParams {
 struct TopShared {
     SelectShared sel;
     entry_t cand[kLpCand];
-    entry_t keep[LN_MAX_TOP];
     int flagged[kLpFlagged];
     int nflag, ncand;
-    // entry_t segs[nseg + kLpLoose] follows
+    // entry_t segs[nseg + kLpLoose], entry_t sorted[most] and, in a cluster, entry_t joined[blocks
+    // * top] follow, most = max(kLpCand, blocks * top)
 };
 
-// The top entries of a row whose segments' largest entries are in `segs`.
+// What a block of a cluster hands to the first.
+struct LpShare {
+    RowTotal total;
+    int above;
+};
+
+// The top entries of a slice of a row whose segments' largest values are in `segs`.
 //
 // While the row streams by, nothing is done for the top but to keep the largest value of each
-// segment (a few vectors of one thread) and the vector that first held it.  The k-th largest of
-// these entries is a lower bound of the row's k-th largest element: k different vectors hold an
-// element that is as large.  So only segments whose largest entry reaches the bound can hold a
-// top element -- k of them, or a few more for a bound found with some slack -- and those alone are
-// read again (k * seglen vectors of a row that has just been read, from L2), their elements that
-// reach the bound becoming the candidates.  An element equal in value to the bound counts only
-// in a vector no later than the bound's, so that rows of many equal values (constant rows, rows
-// masked by the type's lowest value) have few candidates too.
+// segment (a few batches of one thread), a value the running sums need anyway.  The k-th largest
+// of these is a lower bound of the k-th largest element: k different segments hold an element that
+// is as large.  So only segments whose largest value reaches the bound can hold a top element -- k
+// of them, or a few more for a bound found with some slack -- and those alone are read again (from
+// L2: the row has just been read), their elements that reach the bound becoming the candidates.
 //
-// Returns the number of entries left in *list (shared memory, in no order), all of the top among
-// them.
+// Where the candidates do not fit (many equal values at the bound: a constant row, a row masked by
+// the type's lowest value; or few segments that hold very many large ones), the k-th largest entry
+// of those that did fit is a bound as well, a higher one and one between columns of the same value.
+// Each such round leaves out all but k of the kLpCand that were held, so the rounds end.
+//
+// Returns the number of candidates in sh->cand (in no order), all of the top among them; at most
+// kLpCand.
 template <typename T>
-__device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, int nvec, int head,
-                                           TopShared* sh, const entry_t* segs, const entry_t** list) {
+__device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, int lo, int hi, int head,
+                                           TopShared* sh, const entry_t* segs) {
     using IO = Io<T>;
     constexpr int kVec = IO::kVec;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, k = p.top;
-    if (tid == 0) sh->nflag = sh->ncand = 0;
-    __syncthreads();
     const int nall = p.nseg + kLpLoose;
-    const entry_t bound = select_threshold(segs, nall, k, k / 4 + 16, &sh->sel);
-    const float least = bound == 1 ? -3.402823466e38f : entry_value(bound);
-    for (int i = tid; i < nall; i += nt) {
-        const entry_t e = segs[i];
-        if (e < bound) continue;
-        if (i < p.nseg)
-            sh->flagged[atomicAdd(&sh->nflag, 1)] = i;  // at most k + k / 4 + 16 < kLpFlagged
-        else
-            sh->cand[atomicAdd(&sh->ncand, 1)] = e;  // a loose element is a segment of its own
-    }
-    __syncthreads();
-    const int items = sh->nflag * p.seglen;
-    auto vector_of = [&](int w) {
-        const int seg = sh->flagged[w / p.seglen];
-        return seg % nt + nt * (seg / nt * p.seglen + w % p.seglen);
-    };
-    for (int w = tid; w < items; w += nt) {
-        const int v = vector_of(w);
-        if (v >= nvec) continue;
-        const uint4 u = __ldcg(xv + v);
-        if (!(vector_max<T>(u) >= least)) continue;
-        float f[kVec];
-        IO::unpack(u, f);
-        const int col = head + v * kVec;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (f[j] >= least && make_entry(f[j], col) >= bound) {
+    const entry_t first = select_threshold(segs, nall, k, k / 4 + 16, &sh->sel);
+    // Every element of the bound's value, whatever its column.
+    entry_t bound = max(first & ~(entry_t)0xffffffffu, (entry_t)1);
+    while (true) {
+        const float least = bound == 1 ? -3.402823466e38f : entry_value(bound);
+        const entry_t reach = bound & ~(entry_t)0xffffffffu;  // the same for segments: values alone
+        if (tid == 0) sh->nflag = sh->ncand = 0;
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < nall; i += nt) {
+            const entry_t e = segs[i];
+            if (e == 0 || e < reach) continue;
+            if (i < p.nseg) {
+                const int at = atomicAdd(&sh->nflag, 1);
+                if (at < kLpFlagged) sh->flagged[at] = i;
+            } else if (e >= bound) {  // a loose element: an entry itself
                 const int at = atomicAdd(&sh->ncand, 1);
-                if (at < kLpCand) sh->cand[at] = make_entry(f[j], col + j);
+                if (at < kLpCand) sh->cand[at] = e;
             }
-    }
-    __syncthreads();
-    int n = sh->ncand;
-    auto keep_top = [&](int have) {  // the top k of cand[0 .. have) into keep, in no order
-        const entry_t t = select_threshold(sh->cand, have, k, 0, &sh->sel);
-        if (tid == 0) sh->ncand = 0;
+        }
         __syncthreads();
-        for (int i = tid; i < have; i += nt)
-            if (sh->cand[i] >= t) sh->keep[atomicAdd(&sh->ncand, 1)] = sh->cand[i];
-        __syncthreads();
-        return t;
-    };
-    if (n > kLpCand) {
-        // More candidates than there is room for: few segments hold very many large values.  Go
-        // through them again one element a thread at a time, cutting down to the top k whenever
-        // the next step might not fit.
-        entry_t floor_e = 0;
-        __syncthreads();
-        if (tid == 0) sh->ncand = 0;
-        __syncthreads();
-        for (int w0 = 0; w0 < items + kLpLoose; w0 += nt) {
-            const int w = w0 + tid;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            int col = -1;
-            if (w < items) {
-                const int v = vector_of(w);
-                if (v < nvec) {
-                    u = __ldcg(xv + v);
-                    col = head + v * kVec;
-                }
-            }
-            float f[kVec];
-            IO::unpack(u, f);
+        const bool listed = sh->nflag <= kLpFlagged;  // else all segments are gone through
+        const int items = (listed ? sh->nflag : p.nseg) << p.seg_shift;
+#pragma unroll 1
+        for (int w0 = tid; w0 < items; w0 += kBatch * nt) {
+            uint4 u[kBatch];
+            int col[kBatch];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                entry_t e = 0;
-                if (col >= 0) {
-                    if (f[j] >= least && make_entry(f[j], col) >= bound) e = make_entry(f[j], col + j);
-                } else if (j == 0 && w >= items && w < items + kLpLoose) {
-                    e = segs[p.nseg + (w - items)];
-                    if (e < bound) e = 0;
-                }
-                if (e > floor_e) sh->cand[atomicAdd(&sh->ncand, 1)] = e;
-                __syncthreads();
-                const int have = sh->ncand;
-                __syncthreads();
-                if (have > kLpCand - nt) {
-                    floor_e = keep_top(have) - 1;  // entries below the k-th are out for good
-                    const int kept = sh->ncand;
-                    for (int i = tid; i < kept; i += nt) sh->cand[i] = sh->keep[i];
-                    __syncthreads();
+            for (int b = 0; b < kBatch; ++b) {
+                const int w = w0 + b * nt;
+                u[b] = no_logits<T>();
+                if (w >= items) continue;
+                const int q = w >> p.seg_shift, i = w & ((1 << p.seg_shift) - 1);
+                const int seg = listed ? sh->flagged[q] : q;
+                const int v = lo + (seg & (nt - 1)) + nt * ((seg >> p.nt_shift << p.seg_shift) + i);
+                if (v < hi) u[b] = __ldcg(xv + v);
+                col[b] = head + v * kVec;
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (!(vector_max<T>(u[b]) >= least)) continue;
+                float f[kVec];
+                IO::unpack(u[b], f);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    if (!(f[j] >= least)) continue;
+                    const entry_t e = make_entry(f[j], col[b] + j);
+                    if (e < bound) continue;
+                    const int at = atomicAdd(&sh->ncand, 1);
+                    if (at < kLpCand) sh->cand[at] = e;
                 }
             }
         }
-        n = sh->ncand;
+        __syncthreads();
+        const int n = sh->ncand;
+        if (n <= kLpCand) return n;
+        bound = select_threshold(sh->cand, kLpCand, k, k / 2, &sh->sel);
     }
-    if (n <= 2 * LN_MAX_TOP) {  // few enough to be put in order by counting
-        *list = sh->cand;
-        return n;
-    }
-    keep_top(n);
-    *list = sh->keep;
-    return sh->ncand;
 }
 
-// One block a row.  The row is read once, kLpUnroll vectors of a thread in flight at a time.
-template <typename T, bool ENT, bool TOP>
+// The top of `list` in order into sh->cand; returns how many there are.
+__device__ __forceinline__ int put_in_order(const entry_t* list, int n, int k, entry_t* sorted,
+                                            TopShared* sh) {
+    // Far more candidates than places (a short row, all of it): bins over the range of a few more
+    // than k of them, not over both signs.
+    const entry_t floor = n > 2 * k + 64 ? select_threshold(list, n, k, k / 2 + 16, &sh->sel) : 1;
+    return order_top(list, n, k, floor, sorted, sh->cand, &sh->sel);
+}
+
+// One row a block, or a cluster of blocks (CLUSTER) that take a slice of it each: few rows are
+// spread over many SMs, and a slice's results meet in the first block's shared memory.  A row's
+// slice is read once, a batch of each thread in flight while the one before is summed.
+template <typename T, bool ENT, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpParams p) {
     using IO = Io<T>;
-    using PR = Pairs<T>;
-    constexpr int kVec = IO::kVec;
-    constexpr int H = PR::kPairs;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ RowTotal sh_total[kLpMaxThreads / 32];
+    __shared__ LpShare sh_share[CLUSTER ? kLpMaxCluster : 1];
     __shared__ int sh_above;
     TopShared* sh = reinterpret_cast<TopShared*>(smem_raw);
     entry_t* segs = reinterpret_cast<entry_t*>(smem_raw + sizeof(TopShared));
+    entry_t* sorted = segs + p.nseg + kLpLoose;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
+    const int rank = CLUSTER ? (int)cluster_rank() : 0, blocks = CLUSTER ? (int)cluster_blocks() : 1;
+    if constexpr (CLUSTER) cluster_arrive();  // "this block's shared memory exists"
     pdl_enter();
-    const size_t row = blockIdx.x;
+    const size_t row = blockIdx.x / (unsigned)blocks;
     const T* xr = static_cast<const T*>(p.x) + row * (size_t)p.ld;
     const RowCut<T> cut(xr, p.V);
     const uint4* xv = reinterpret_cast<const uint4*>(xr + cut.head);
-    const int nvec = cut.nvec;
+    const int per = (cut.nvec + blocks - 1) / blocks;
+    const int lo = min(cut.nvec, rank * per), hi = min(cut.nvec, lo + per);
+    const int step = kBatch * nt;
+    uint4 u[kBatch];
+    load_batch<T>(u, xv, lo + tid, nt, hi);
     const int t = p.tokens ? p.tokens[row] : -1;
     const bool has = t >= 0 && t < p.V;
-    const float xt = has ? IO::to_f(xr[t]) : __int_as_float(0x7fc00000);
-    const float over = p.ranks ? xt : __int_as_float(0x7fc00000);  // values above it are counted
+    const float nan = __int_as_float(0x7fc00000);
+    const float xt = has ? IO::to_f(xr[t]) : nan;
+    const float over = p.ranks ? xt : nan;  // values above it are counted
     if (tid == 0) sh_above = 0;
     RowSums<ENT> s;
     s.clear();
     const f2 c2 = f2_splat(p.c);
     int above = 0;
     float best = -INFINITY;
-    int bestv = 0, left = p.seglen, seg = tid;
-    for (int v0 = tid; v0 < nvec; v0 += kLpUnroll * nt) {
-        uint4 u[kLpUnroll];
-#pragma unroll
-        for (int k = 0; k < kLpUnroll; ++k) {
-            const int v = v0 + k * nt;
-            if (v < nvec) u[k] = __ldcg(xv + v);
-        }
-#pragma unroll
-        for (int k = 0; k < kLpUnroll; ++k) {
-            const int v = v0 + k * nt;
-            if (v >= nvec) break;
-            const float m = vector_max<T>(u[k]);
-            s.see(m, p.c);
-            f2 x2[H];
-            PR::unpack(u[k], x2);
-            s.add(x2, c2);
-            if (m > over) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) above += (f2_lo(x2[h]) > over) + (f2_hi(x2[h]) > over);
-            }
-            if constexpr (TOP) {
-                if (m > best) {
-                    best = m;
-                    bestv = v;
-                }
-                if (--left == 0) {
-                    segs[seg] = best > -INFINITY ? make_entry(best, cut.col(bestv)) : 0;
-                    seg += nt;
-                    best = -INFINITY;
-                    left = p.seglen;
-                }
+    const int seglen = (1 << p.seg_shift) / kBatch;
+    int left = seglen, seg = tid;
+    auto take = [&](const uint4 (&b)[kBatch], int v0) {
+        const float m = s.template see_batch<T>(b, p.c);
+        if (m > over) above += count_above<T>(b, over);
+        if (m > -INFINITY)
+            s.template add_batch<T>(b, c2, [&](int k) {
+                const int v = v0 + k * nt;
+                return v < hi ? __ldcg(xv + v) : no_logits<T>();
+            });
+        if constexpr (TOP) {
+            best = fmaxf(best, m);
+            if (--left == 0) {
+                segs[seg] = best > -INFINITY ? make_entry(best, seg) : 0;
+                seg += nt;
+                best = -INFINITY;
+                left = seglen;
             }
         }
+    };
+    for (int v0 = lo + tid; v0 < hi; v0 += 2 * step) {
+        uint4 ahead[kBatch];
+        load_batch<T>(ahead, xv, v0 + step, nt, hi);
+        take(u, v0);
+        if (v0 + step >= hi) break;
+        load_batch<T>(u, xv, v0 + 2 * step, nt, hi);
+        take(ahead, v0 + step);
     }
     if constexpr (TOP) {
-        for (; seg < p.nseg; seg += nt) {  // the last, unfilled segment, and those of no vector
-            segs[seg] = best > -INFINITY ? make_entry(best, cut.col(bestv)) : 0;
+        for (; seg < p.nseg; seg += nt) {  // the last, unfilled segment, and those of no batch
+            segs[seg] = best > -INFINITY ? make_entry(best, seg) : 0;
             best = -INFINITY;
         }
         if (tid < kLpLoose) segs[p.nseg + tid] = 0;
     }
-    if (tid < cut.nloose()) {
+    if (rank == 0 && tid < cut.nloose()) {
         const int col = cut.loose(tid);
         const float x = IO::to_f(xr[col]);
         s.add_one(x, p.c);
@@ -246,42 +228,94 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
         if constexpr (TOP)
             if (x > -INFINITY) segs[p.nseg + tid] = make_entry(x, col);
     }
-    RowTotal mine{s.ref, f2_lo(s.z2) + f2_hi(s.z2), ENT ? f2_lo(s.w2) + f2_hi(s.w2) : 0.f};
+    const RowTotal mine{s.ref, f2_lo(s.z2) + f2_hi(s.z2), ENT ? f2_lo(s.w2) + f2_hi(s.w2) : 0.f};
     __syncthreads();  // sh_above, segs
     above = __reduce_add_sync(kFullMask, above);
     if ((tid & 31) == 0 && above) atomicAdd(&sh_above, above);
-    const RowTotal a = block_total(mine, p.c, sh_total);
+    RowTotal a = block_total(mine, p.c, sh_total);
     __syncthreads();
+    above = sh_above;
+    const entry_t* list = nullptr;
+    int n = 0;
+    if constexpr (TOP) {
+        n = collect_top<T>(p, xv, lo, hi, cut.head, sh, segs);
+        list = sh->cand;
+    }
+    if constexpr (CLUSTER) {
+        // Every block's sums and top entries go to the first, in the order of the blocks.
+        entry_t* joined = sorted + max(kLpCand, blocks * p.top);
+        cluster_wait();
+        if (tid == 0) {
+            const uint32_t to = in_block(&sh_share[rank], 0);
+            st_cluster_f32(to, a.ref);
+            st_cluster_f32(to + 4, a.z);
+            st_cluster_f32(to + 8, a.w);
+            st_cluster_f32(to + 12, __int_as_float(above));
+        }
+        if constexpr (TOP) {
+            const uint32_t to = in_block(joined + rank * p.top, 0);
+            const int real = put_in_order(list, n, p.top, sorted, sh);
+            for (int i = tid; i < p.top; i += nt) st_cluster_u64(to + 8 * i, i < real ? sh->cand[i] : 0);
+        }
+        cluster_arrive();
+        if (rank != 0) return;
+        cluster_wait();
+        a = sh_share[0].total;
+        above = sh_share[0].above;
+        for (int b = 1; b < blocks; ++b) {
+            a = total_join(a, sh_share[b].total, p.c);
+            above += sh_share[b].above;
+        }
+        if constexpr (TOP) {
+            list = joined;
+            n = blocks * p.top;
+        }
+    }
     const float r = a.ref == -INFINITY ? 0.f : a.ref;
     const float logz = logf(a.z);
     if (tid == 0) {
         if (p.lse) p.lse[row] = fmaf(r, p.scale, logz);
         if (ENT) p.entropy[row] = logz - kLn2 * a.w / a.z;
-        if (p.tokens) {
-            // No token (t < 0): 0, of rank 0.  A token outside the row: NaN, of rank 0.
-            if (p.logp) p.logp[row] = t < 0 ? 0.f : fmaf(xt - r, p.scale, -logz);
-            if (p.ranks) p.ranks[row] = has ? sh_above + 1 : 0;
-        }
+        // No token (t < 0): 0, of rank 0.  A token outside the row: NaN, of rank 0.
+        if (p.logp) p.logp[row] = t < 0 ? 0.f : fmaf(xt - r, p.scale, -logz);
+        if (p.ranks) p.ranks[row] = has ? above + 1 : 0;
     }
     if constexpr (TOP) {
-        const entry_t* list;
-        const int n = collect_top<T>(p, xv, nvec, cut.head, sh, segs, &list);
         int* ids = p.top_ids + row * (size_t)p.top;
         float* lp = p.top_logp + row * (size_t)p.top;
-        for (int i = tid; i < n; i += nt) {
-            const entry_t e = list[i];
-            const int at = place_of(e, list, n);
-            if (at < p.top) {
-                ids[at] = entry_col(e);
-                lp[at] = fmaf(entry_value(e) - r, p.scale, -logz);
-            }
-        }
-        for (int i = n + tid; i < p.top; i += nt) {  // fewer logits above -inf than places
-            ids[i] = -1;
-            lp[i] = -INFINITY;
+        const int real = put_in_order(list, n, p.top, sorted, sh);
+        for (int i = tid; i < p.top; i += nt) {
+            const bool is = i < real;  // else: fewer logits above -inf than places
+            ids[i] = is ? entry_col(sh->cand[i]) : -1;
+            lp[i] = is ? fmaf(entry_value(sh->cand[i]) - r, p.scale, -logz) : -INFINITY;
         }
     }
 }
+
+template <typename T, bool CLUSTER>
+const void* logprobs_variant(bool ent, bool top) {
+    return top ? (ent ? (const void*)logprobs_kernel<T, true, true, CLUSTER>
+                      : (const void*)logprobs_kernel<T, false, true, CLUSTER>)
+               : (ent ? (const void*)logprobs_kernel<T, true, false, CLUSTER>
+                      : (const void*)logprobs_kernel<T, false, false, CLUSTER>);
+}
+
+// Blocks a row is split over: as many as leave every SM no more than two blocks, of no less than 2048
+// vectors each.  (One row of 131072 bf16 logits, top 20: 14.5 us in one block, 10.0 in 4, 9.6 in 8, 11.9
+// in 16; of 16384 logits: 6.8 us in one block, 7.7 in 4.  64 rows of 131072: 18.2, 12.5 in 4, 16.0
+// in 8; 200 rows: 25.4, 26.3 in 2.)
+int logprobs_cluster(int rows, int nvec, int sms) {
+    int blocks = 1;
+    while (blocks < kLpMaxCluster && (long long)rows * blocks * 2 <= 2 * sms && nvec / (blocks * 2) >= 2048)
+        blocks *= 2;
+    return blocks;
+}
+
+// Threads of a block at most, a power of two: 256, four blocks an SM.  Where there are rows for more than
+// a wave of smaller blocks and no top to select, 128: a row's fixed costs are by the warp (4096 x
+// 50257 bf16: 68 us, 72 with 256; but 700 x 50304: 28 us, 22 with 256; with the top 64 of 2048 x 131072:
+// 143 us, 123 with 256).
+int logprobs_threads(int rows, bool top, int sms) { return !top && rows > 8 * sms ? 128 : 256; }
 
 template <typename T>
 cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
@@ -301,22 +335,40 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     p.top_ids = a.top_ids;
     p.top_logp = a.top_logp;
     const int nvec = a.V / kVec;
-    const int nt = nvec >= 2048 ? 512 : nvec >= 512 ? 256 : 128;
-    const int per = std::max(1, (nvec + nt - 1) / nt);  // vectors of a thread
-    p.seglen = std::max(1, (per * nt + kLpSegments - 1) / kLpSegments);
-    p.nseg = (per + p.seglen - 1) / p.seglen * nt;
+    const int sms = device_info(-1).sms;
+    const int blocks = logprobs_cluster(a.rows, nvec, sms);
+    const int slice = (nvec + blocks - 1) / blocks;
+    const int most = logprobs_threads(a.rows, a.top > 0, sms);
+    // A batch for every thread, if there are that many; the selection of a top is work for 4 warps.
+    int nt = a.top > 0 ? 128 : 32;
+    p.nt_shift = a.top > 0 ? 7 : 5;
+    while (nt < most && nt * kBatch < slice) {
+        nt *= 2;
+        ++p.nt_shift;
+    }
+    const int per = std::max(1, (slice + nt * kBatch - 1) / (nt * kBatch));  // batches of a thread
+    int seglen = 1;
+    p.seg_shift = 2;
+    static_assert(kBatch == 1 << 2, "seg_shift counts vectors");
+    while (per * nt > seglen * kLpSegments) {
+        seglen *= 2;
+        ++p.seg_shift;
+    }
+    p.nseg = (per + seglen - 1) / seglen * nt;
     const bool top = a.top > 0, ent = a.entropy != nullptr;
-    const size_t smem = top ? sizeof(TopShared) + ((size_t)p.nseg + kLpLoose) * sizeof(entry_t) : 0;
-    const void* kern = top ? (ent ? (const void*)logprobs_kernel<T, true, true>
-                                  : (const void*)logprobs_kernel<T, false, true>)
-                           : (ent ? (const void*)logprobs_kernel<T, true, false>
-                                  : (const void*)logprobs_kernel<T, false, false>);
+    size_t smem = 0;
     if (top) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const size_t joined = blocks > 1 ? (size_t)blocks * a.top : 0;
+        smem = sizeof(TopShared) +
+               (p.nseg + kLpLoose + std::max((size_t)kLpCand, joined) + joined) * sizeof(entry_t);
+    }
+    const void* kern = blocks > 1 ? logprobs_variant<T, true>(ent, top) : logprobs_variant<T, false>(ent, top);
+    if (top) {
+        const cudaError_t e = allow_smem(kern, smem);
         if (e != cudaSuccess) return e;
     }
     void* args[] = {&p};
-    return launch_kernel(kern, dim3((unsigned)a.rows), dim3(nt), smem, stream, args, false);
+    return launch_cluster(kern, dim3((unsigned)a.rows * (unsigned)blocks), dim3(nt), blocks, smem, stream, args);
 }
 
 // ---------------------------------------------------------------------------------------
