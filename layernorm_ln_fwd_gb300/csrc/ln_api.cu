@@ -1,6 +1,5 @@
 // ln_api.cu -- the C ABI declared in include/ln.h: argument checks, kernel selection,
 // backward workspaces and the per-device status word.
-#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
@@ -26,6 +25,7 @@ std::map<int, DeviceInfo> g_devices;
 std::map<int, unsigned*> g_status_ptrs;
 std::map<std::tuple<int, const void*, int, size_t>, int> g_occupancy;
 std::map<std::pair<int, const void*>, size_t> g_smem_allowed;
+std::map<std::tuple<int, const void*, int, int, size_t>, int> g_clusters;
 
 struct Workspace {
     void* ptr = nullptr;
@@ -120,11 +120,36 @@ cudaError_t launch_kernel(const void* kern, dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+int clusters_at_once(const void* kern, int threads, int blocks, size_t smem) {
+    if (blocks <= 1) return blocks_per_sm(kern, threads, smem) * device_info(-1).sms;
+    const auto key = std::make_tuple(current_device(), kern, threads, blocks, smem);
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        auto it = g_clusters.find(key);
+        if (it != g_clusters.end()) return it->second;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+    std::lock_guard<std::mutex> lk(g_mu);
+    return g_clusters[key] = n;
+}
+
 cudaError_t allow_smem(const void* kern, size_t bytes) {
     const int dev = current_device();
     std::lock_guard<std::mutex> lk(g_mu);
     size_t& have = g_smem_allowed[std::make_pair(dev, kern)];
-    if (bytes <= std::max(have, (size_t)48 << 10)) return cudaSuccess;
+    if (bytes <= have) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess) have = bytes;
     return e;
@@ -527,6 +552,8 @@ ln_status distill_impl(Dtype dt, const T* logits, int64_t ld, const int32_t* ids
     a.losses = losses;
     a.dlogits = dlogits;
     a.ldd = ldd;
+    a.status = status_word();
+    a.wait_limit_ns = wait_limit_ns();
     int launches = 0;
     cudaError_t e = launch_distill(dt, a, stream, &launches);
     return finish_call(e, launches, stream);

@@ -100,6 +100,10 @@ bool vector_ok(Dtype dt, int cols, const void* const* ptrs, int nptrs);
 cudaError_t launch_kernel(const void* kern, dim3 grid, dim3 block, size_t smem,
                           cudaStream_t stream, void** args, bool cooperative);
 
+// Clusters of `blocks` blocks (1: blocks) of a kernel that run on the current device at once,
+// cached.
+int clusters_at_once(const void* kern, int threads, int blocks, size_t smem);
+
 // Lets `kern` have `bytes` of dynamic shared memory on the current device (asked of the driver only
 // when it is more than before).
 cudaError_t allow_smem(const void* kern, size_t bytes);
@@ -243,6 +247,8 @@ struct DistillArgs {
     float* losses;
     void* dlogits;
     int64_t ldd;
+    unsigned* status;  // the per-device status word (bounded waits)
+    uint64_t wait_limit_ns;
 };
 
 cudaError_t launch_distill(Dtype dt, const DistillArgs& a, cudaStream_t stream, int* launches);

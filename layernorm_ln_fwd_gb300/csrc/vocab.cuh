@@ -302,6 +302,18 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 __device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
+// Asynchronous stores to another block, whose mbarrier at `bar` counts their bytes.
+__device__ __forceinline__ void send2(uint32_t a, float x, float y, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(a),
+                 "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send4(uint32_t a, float x, float y, float z, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+        "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(__float_as_uint(z)), "r"(0u), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void st_cluster_u64(uint32_t a, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
