@@ -373,11 +373,11 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------------------
 // The gradient.  The forward left L and H, so every element stands for itself: one warp takes a
-// piece of a row (kLbUnroll vectors a lane), reads it, and writes the gradient of the same
+// piece of a row (some batches a lane), reads it, and writes the gradient of the same
 // elements, which may be the logits' own place.
 // ---------------------------------------------------------------------------------------
 constexpr int kLbThreads = 256;
-constexpr int kLbUnroll = 4;
+constexpr int kLbBlocksPerSm = 4;
 
 struct LbParams {
     const void* x;
@@ -397,9 +397,11 @@ struct LbParams {
 
 // WIDE: logits and gradient lie at the same place of a 16-byte vector in every row.
 template <typename T, bool ENT, bool WIDE>
-__global__ void __launch_bounds__(kLbThreads) logprobs_bwd_kernel(const LbParams p) {
+__global__ void __launch_bounds__(kLbThreads, kLbBlocksPerSm) logprobs_bwd_kernel(const LbParams p) {
     using IO = Io<T>;
+    using PR = Pairs<T>;
     constexpr int kVec = IO::kVec;
+    constexpr int H = PR::kPairs;
     pdl_enter();
     const int lane = (int)threadIdx.x & 31;
     const long long piece = (long long)blockIdx.x * (kLbThreads / 32) + (threadIdx.x >> 5);
@@ -409,51 +411,90 @@ __global__ void __launch_bounds__(kLbThreads) logprobs_bwd_kernel(const LbParams
     const T* xr = static_cast<const T*>(p.x) + row * (size_t)p.ld;
     T* dr = static_cast<T*>(p.dx) + row * (size_t)p.ldd;
     const RowCut<T> cut(xr, p.V);
-    const int t = p.tokens ? p.tokens[row] : -1;
-    const bool bad = p.dlogp && t >= p.V;
-    float g = p.dlogp && t >= 0 ? p.dlogp[row] : 0.f;
-    const float de = ENT ? p.dent[row] : 0.f;
-    const bool none = g == 0.f && de == 0.f;  // nothing flows back: 0, whatever the row holds
-    if (bad) g = __int_as_float(0x7fc00000);
-    const float lse = p.lse[row], hh = ENT ? p.entropy[row] : 0.f;
-    const float sg = p.scale * g, sde = p.scale * de;
-    auto grad = [&](float x, int col) {
-        const float logq = fmaf(x, p.scale, -lse);
-        const float q = ex2_fast(logq * kLog2e);
-        float o = -sg * q;
-        if constexpr (ENT) o = fmaf(-sde * q, fmaxf(logq, -1e30f) + hh, o);
-        return col == t ? o + sg : o;
-    };
     const int lo = (int)((long long)cut.nvec * part / p.per_row);
     const int hi = (int)((long long)cut.nvec * (part + 1) / p.per_row);
     const uint4* xv = reinterpret_cast<const uint4*>(xr + cut.head);
-    for (int v0 = lo + lane; v0 < hi; v0 += 32 * kLbUnroll) {
-        uint4 u[kLbUnroll];
-#pragma unroll
-        for (int k = 0; k < kLbUnroll; ++k) {
-            const int v = v0 + 32 * k;
-            u[k] = v < hi && !none ? __ldcs(xv + v) : make_uint4(0, 0, 0, 0);
+    const bool has_loose = part == 0 && lane < cut.nloose();
+    float g = p.dlogp ? p.dlogp[row] : 0.f;
+    const float de = ENT ? p.dent[row] : 0.f;
+    const int t = p.dlogp ? p.tokens[row] : -1;
+    const float lse = p.lse[row], hh = ENT ? p.entropy[row] : 0.f;
+    if (t < 0) g = 0.f;
+    if (g == 0.f && de == 0.f) {  // nothing flows back: 0, whatever the row holds
+        if constexpr (WIDE) {
+            for (int v = lo + lane; v < hi; v += 32) st_stream(dr + cut.col(v), make_uint4(0, 0, 0, 0));
+        } else {
+            for (int j = cut.col(lo) + lane; j < cut.col(hi); j += 32) dr[j] = IO::from_f(0.f);
         }
+        if (has_loose) dr[cut.loose(lane)] = IO::from_f(0.f);
+        return;
+    }
+    if (t >= p.V) g = __int_as_float(0x7fc00000);
+    // With lq = log q: dx = q (a + b lq), a = -scale (dlogp + dH entropy), b = -scale dH, and at the
+    // token scale * dlogp more.
+    const float sg = p.scale * g, b = -p.scale * de;
+    const float ca = ENT ? fmaf(b, hh, -sg) : -sg;
+    auto grad = [&](float x, int col) {
+        const float lq = fmaf(x, p.scale, -lse);
+        const float q = ex2_fast(lq * kLog2e);
+        const float o = ENT ? q * fmaf(b, fmaxf(lq, -1e30f), ca) : q * ca;
+        return col == t ? o + sg : o;
+    };
+    const f2 s2 = f2_splat(p.scale), l2 = f2_splat(-lse), e2 = f2_splat(kLog2e), ca2 = f2_splat(ca), b2 = f2_splat(b);
+    auto deal = [&](const uint4 (&u)[kBatch], int v0) {
 #pragma unroll
-        for (int k = 0; k < kLbUnroll; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
             const int v = v0 + 32 * k;
             if (v >= hi) break;
             const int col = cut.col(v);
-            float f[kVec];
-            IO::unpack(u[k], f);
+            f2 o[H];
+            PR::unpack(u[k], o);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) f[j] = none ? 0.f : grad(f[j], col + j);
+            for (int h = 0; h < H; ++h) {
+                f2 lq = f2_fma(o[h], s2, l2);
+                const f2 y = f2_mul(lq, e2);
+                const f2 q = f2_make(ex2_fast(f2_lo(y)), ex2_fast(f2_hi(y)));
+                if constexpr (ENT) {  // 0 * -inf is no term
+                    lq = f2_make(fmaxf(f2_lo(lq), -1e30f), fmaxf(f2_hi(lq), -1e30f));
+                    o[h] = f2_mul(q, f2_fma(b2, lq, ca2));
+                } else {
+                    o[h] = f2_mul(q, ca2);
+                }
+            }
+            const int in = t - col;  // the token's place in this vector
+            if (in >= 0 && in < kVec) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    o[h] = f2_add(o[h], f2_make(in == 2 * h ? sg : 0.f, in == 2 * h + 1 ? sg : 0.f));
+            }
             if constexpr (WIDE) {
-                st_stream(dr + col, IO::pack(f));
+                st_stream(dr + col, PR::pack(o));
             } else {
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) dr[col + j] = IO::from_f(f[j]);
+                for (int h = 0; h < H; ++h) {
+                    dr[col + 2 * h] = IO::from_f(f2_lo(o[h]));
+                    dr[col + 2 * h + 1] = IO::from_f(f2_hi(o[h]));
+                }
             }
         }
+    };
+    constexpr int kStep = 32 * kBatch;
+    int v0 = lo + lane;
+    if (v0 < hi) {
+        uint4 u[kBatch], ahead[kBatch];
+        load_batch<T>(u, xv, v0, 32, hi);
+        while (true) {
+            load_batch<T>(ahead, xv, v0 + kStep, 32, hi);
+            deal(u, v0);
+            if ((v0 += kStep) >= hi) break;
+            load_batch<T>(u, xv, v0 + kStep, 32, hi);
+            deal(ahead, v0);
+            if ((v0 += kStep) >= hi) break;
+        }
     }
-    if (part == 0 && lane < cut.nloose()) {
+    if (has_loose) {
         const int col = cut.loose(lane);
-        dr[col] = IO::from_f(none ? 0.f : grad(IO::to_f(xr[col]), col));
+        dr[col] = IO::from_f(grad(IO::to_f(xr[col]), col));
     }
 }
 
@@ -473,7 +514,13 @@ cudaError_t launch_logprobs_bwd_t(const LogprobsBwdArgs& a, cudaStream_t stream)
     p.dx = a.dlogits;
     p.ldd = a.ldd;
     const int nvec = a.V / kVec;
-    p.per_row = std::max(1, (nvec + 32 * kLbUnroll - 1) / (32 * kLbUnroll));
+    // Batches of a lane: one after another they hide a row's own loads (its log-sum, its token) and the
+    // start of a warp, 151 us with one and 126 with four at 4096 x 50257 bf16 -- where there are some
+    // waves of warps all the same (200 x 50257 fp32: 16.3 us with four, 15.0 with one).
+    const long long resident = (long long)device_info(-1).sms * kLbBlocksPerSm * (kLbThreads / 32);
+    int batches = 4;
+    while (batches > 1 && (long long)a.rows * ((nvec + 31) / 32) < 3 * resident * kBatch * batches) batches /= 2;
+    p.per_row = std::max(1, (nvec + 32 * kBatch * batches - 1) / (32 * kBatch * batches));
     p.pieces = (long long)a.rows * p.per_row;
     const bool wide = rows_congruent(a.logits, a.ld, a.dlogits, a.ldd, sizeof(T), a.rows);
     const bool ent = a.dentropy != nullptr;
