@@ -17,8 +17,9 @@ namespace lnk {
 namespace {
 
 constexpr int kLpMaxThreads = 512;
-constexpr int kLpSegments = 1024;   // segments of a slice, about
+constexpr int kLpSegments = 2048;   // segments of a slice at most, about
 constexpr int kLpCand = 1024;       // candidates held at once
+constexpr int kLpCount = 128;       // entries that are put in order by counting
 constexpr int kLpFlagged = 2 * LN_MAX_TOP;
 constexpr int kLpLoose = 16;        // at least 2 * (kVec - 1) loose elements of a row
 constexpr int kLpMaxCluster = 8;
@@ -46,8 +47,8 @@ struct TopShared {
     entry_t cand[kLpCand];
     int flagged[kLpFlagged];
     int nflag, ncand;
-    // entry_t segs[nseg + kLpLoose], entry_t sorted[most] and, in a cluster, entry_t joined[blocks
-    // * top] follow, most = max(kLpCand, blocks * top)
+    // entry_t sorted[max(kLpCand, blocks * top)], in a cluster entry_t joined[blocks * top], and
+    // unsigned segs[nseg + kLpLoose] follow
 };
 
 // What a block of a cluster hands to the first.
@@ -73,28 +74,29 @@ struct LpShare {
 // Returns the number of candidates in sh->cand (in no order), all of the top among them; at most
 // kLpCand.
 template <typename T>
-__device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, int lo, int hi, int head,
-                                           TopShared* sh, const entry_t* segs) {
+__device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, int lo, int hi,
+                                           const RowCut<T>& cut, TopShared* sh, const unsigned* segs) {
     using IO = Io<T>;
     constexpr int kVec = IO::kVec;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, k = p.top;
     const int nall = p.nseg + kLpLoose;
-    const entry_t first = select_threshold(segs, nall, k, k / 4 + 16, &sh->sel);
     // Every element of the bound's value, whatever its column.
-    entry_t bound = max(first & ~(entry_t)0xffffffffu, (entry_t)1);
+    entry_t bound = (entry_t)select_threshold(segs, nall, k, k / 4 + 16, &sh->sel) << 32;
     while (true) {
-        const float least = bound == 1 ? -3.402823466e38f : entry_value(bound);
-        const entry_t reach = bound & ~(entry_t)0xffffffffu;  // the same for segments: values alone
+        const unsigned reach = (unsigned)(bound >> 32);  // the same for segments: values alone
+        const float least = reach <= 1 ? -3.402823466e38f : order_value(reach);
         if (tid == 0) sh->nflag = sh->ncand = 0;
         __syncthreads();
 #pragma unroll 1
         for (int i = tid; i < nall; i += nt) {
-            const entry_t e = segs[i];
-            if (e == 0 || e < reach) continue;
+            const unsigned key = segs[i];
+            if (key == 0 || key < reach) continue;
             if (i < p.nseg) {
                 const int at = atomicAdd(&sh->nflag, 1);
                 if (at < kLpFlagged) sh->flagged[at] = i;
-            } else if (e >= bound) {  // a loose element: an entry itself
+            } else {  // a loose element
+                const entry_t e = (entry_t)key << 32 | (uint32_t)~(uint32_t)cut.loose(i - p.nseg);
+                if (e < bound) continue;
                 const int at = atomicAdd(&sh->ncand, 1);
                 if (at < kLpCand) sh->cand[at] = e;
             }
@@ -115,7 +117,7 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
                 const int seg = listed ? sh->flagged[q] : q;
                 const int v = lo + (seg & (nt - 1)) + nt * ((seg >> p.nt_shift << p.seg_shift) + i);
                 if (v < hi) u[b] = __ldcg(xv + v);
-                col[b] = head + v * kVec;
+                col[b] = cut.col(v);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
@@ -139,9 +141,25 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
     }
 }
 
-// The top of `list` in order into sh->cand; returns how many there are.
+// The top of `list` in order into `out`; returns how many there are.
 __device__ __forceinline__ int put_in_order(const entry_t* list, int n, int k, entry_t* sorted,
-                                            TopShared* sh) {
+                                            TopShared* sh, entry_t** out) {
+    if (n <= kLpCount) {
+        // Few: each counts those above it, which takes no barrier but the last.
+        int real = 0;
+        for (int i0 = 0; i0 < n; i0 += (int)blockDim.x) {
+            const int i = i0 + (int)threadIdx.x;
+            const entry_t e = i < n ? list[i] : 0;
+            if (e) {
+                const int at = place_of(e, list, n);
+                if (at < k) sorted[at] = e;
+            }
+            real += __syncthreads_count(e != 0);
+        }
+        *out = sorted;
+        return min(real, k);
+    }
+    *out = sh->cand;
     // Far more candidates than places (a short row, all of it): bins over the range of a few more
     // than k of them, not over both signs.
     const entry_t floor = n > 2 * k + 64 ? select_threshold(list, n, k, k / 2 + 16, &sh->sel) : 1;
@@ -158,11 +176,12 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
     __shared__ RowTotal sh_total[kLpMaxThreads / 32];
     __shared__ LpShare sh_share[CLUSTER ? kLpMaxCluster : 1];
     __shared__ int sh_above;
-    TopShared* sh = reinterpret_cast<TopShared*>(smem_raw);
-    entry_t* segs = reinterpret_cast<entry_t*>(smem_raw + sizeof(TopShared));
-    entry_t* sorted = segs + p.nseg + kLpLoose;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
+    TopShared* sh = reinterpret_cast<TopShared*>(smem_raw);
     const int rank = CLUSTER ? (int)cluster_rank() : 0, blocks = CLUSTER ? (int)cluster_blocks() : 1;
+    entry_t* sorted = reinterpret_cast<entry_t*>(smem_raw + sizeof(TopShared));
+    entry_t* joined = sorted + max(kLpCand, blocks * p.top);  // in a cluster: all blocks' entries
+    unsigned* segs = reinterpret_cast<unsigned*>(CLUSTER ? joined + blocks * p.top : joined);
     if constexpr (CLUSTER) cluster_arrive();  // "this block's shared memory exists"
     pdl_enter();
     const size_t row = blockIdx.x / (unsigned)blocks;
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
         if constexpr (TOP) {
             best = fmaxf(best, m);
             if (--left == 0) {
-                segs[seg] = best > -INFINITY ? make_entry(best, seg) : 0;
+                segs[seg] = best > -INFINITY ? order_key(best) : 0;
                 seg += nt;
                 best = -INFINITY;
                 left = seglen;
@@ -215,7 +234,7 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
     }
     if constexpr (TOP) {
         for (; seg < p.nseg; seg += nt) {  // the last, unfilled segment, and those of no batch
-            segs[seg] = best > -INFINITY ? make_entry(best, seg) : 0;
+            segs[seg] = best > -INFINITY ? order_key(best) : 0;
             best = -INFINITY;
         }
         if (tid < kLpLoose) segs[p.nseg + tid] = 0;
@@ -226,7 +245,7 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
         s.add_one(x, p.c);
         above += x > over;
         if constexpr (TOP)
-            if (x > -INFINITY) segs[p.nseg + tid] = make_entry(x, col);
+            if (x > -INFINITY) segs[p.nseg + tid] = order_key(x);
     }
     const RowTotal mine{s.ref, f2_lo(s.z2) + f2_hi(s.z2), ENT ? f2_lo(s.w2) + f2_hi(s.w2) : 0.f};
     __syncthreads();  // sh_above, segs
@@ -238,12 +257,11 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
     const entry_t* list = nullptr;
     int n = 0;
     if constexpr (TOP) {
-        n = collect_top<T>(p, xv, lo, hi, cut.head, sh, segs);
+        n = collect_top<T>(p, xv, lo, hi, cut, sh, segs);
         list = sh->cand;
     }
     if constexpr (CLUSTER) {
         // Every block's sums and top entries go to the first, in the order of the blocks.
-        entry_t* joined = sorted + max(kLpCand, blocks * p.top);
         cluster_wait();
         if (tid == 0) {
             const uint32_t to = in_block(&sh_share[rank], 0);
@@ -254,8 +272,9 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
         }
         if constexpr (TOP) {
             const uint32_t to = in_block(joined + rank * p.top, 0);
-            const int real = put_in_order(list, n, p.top, sorted, sh);
-            for (int i = tid; i < p.top; i += nt) st_cluster_u64(to + 8 * i, i < real ? sh->cand[i] : 0);
+            entry_t* top;
+            const int real = put_in_order(list, n, p.top, sorted, sh, &top);
+            for (int i = tid; i < p.top; i += nt) st_cluster_u64(to + 8 * i, i < real ? top[i] : 0);
         }
         cluster_arrive();
         if (rank != 0) return;
@@ -283,11 +302,12 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
     if constexpr (TOP) {
         int* ids = p.top_ids + row * (size_t)p.top;
         float* lp = p.top_logp + row * (size_t)p.top;
-        const int real = put_in_order(list, n, p.top, sorted, sh);
+        entry_t* top;
+        const int real = put_in_order(list, n, p.top, sorted, sh, &top);
         for (int i = tid; i < p.top; i += nt) {
             const bool is = i < real;  // else: fewer logits above -inf than places
-            ids[i] = is ? entry_col(sh->cand[i]) : -1;
-            lp[i] = is ? fmaf(entry_value(sh->cand[i]) - r, p.scale, -logz) : -INFINITY;
+            ids[i] = is ? entry_col(top[i]) : -1;
+            lp[i] = is ? fmaf(entry_value(top[i]) - r, p.scale, -logz) : -INFINITY;
         }
     }
 }
@@ -350,7 +370,10 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     int seglen = 1;
     p.seg_shift = 2;
     static_assert(kBatch == 1 << 2, "seg_shift counts vectors");
-    while (per * nt > seglen * kLpSegments) {
+    // Segments enough that few of them hold a top element: what is read again is about top / segments of
+    // the row, what the selection goes through is the segments.
+    const int segments = std::min(std::max(32 * a.top, 512), kLpSegments);
+    while (per * nt > seglen * segments) {
         seglen *= 2;
         ++p.seg_shift;
     }
@@ -359,8 +382,8 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     size_t smem = 0;
     if (top) {
         const size_t joined = blocks > 1 ? (size_t)blocks * a.top : 0;
-        smem = sizeof(TopShared) +
-               (p.nseg + kLpLoose + std::max((size_t)kLpCand, joined) + joined) * sizeof(entry_t);
+        smem = sizeof(TopShared) + (std::max((size_t)kLpCand, joined) + joined) * sizeof(entry_t) +
+               ((size_t)p.nseg + kLpLoose) * sizeof(unsigned);
     }
     const void* kern = blocks > 1 ? logprobs_variant<T, true>(ent, top) : logprobs_variant<T, false>(ent, top);
     if (top) {

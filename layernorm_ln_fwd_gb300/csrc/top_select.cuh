@@ -38,25 +38,26 @@ struct __align__(16) SelectShared {
     int above, taken, done;
 };
 
-// A threshold t with at least k, and at most k + slack, of the n entries >= t; the list may hold
-// zeros (no entry), which never count.  With k + slack entries or fewer: 1 (every entry).  With
-// slack 0 the entries have to differ from one another; then exactly k are >= t.
+// A threshold t with at least k, and where the values allow it at most k + slack, of the n entries (or
+// bare keys, E = unsigned) >= t; the list may hold zeros (no entry), which never count.  With
+// k + slack entries or fewer: 1 (every entry).
 //
 // One step spreads the entries of a range [lo, hi] over at most 256 bins of equal width (a power
 // of two), finds from the top the bin that holds the k-th, and goes on within it.  The first range
 // is that of the entries themselves, so that logits of any size fill the bins; with some slack one
 // step is usually enough.  Every thread of the block calls it, with the entries in shared memory
 // and visible; it returns the same value to all.
-static __device__ __noinline__ entry_t select_threshold(const entry_t* list, int n, int k, int slack,
-                                                    SelectShared* sh) {
+template <typename E>
+static __device__ __noinline__ E select_threshold(const E* list, int n, int k, int slack, SelectShared* sh) {
+    constexpr int kBits = 8 * sizeof(E), kKeyShift = kBits - 32;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, lane = tid & 31;
     unsigned mn = ~0u, mx = 0;
     int have = 0;
 #pragma unroll 1
     for (int i = tid; i < n; i += nt) {
-        const entry_t e = list[i];
+        const E e = list[i];
         if (e == 0) continue;
-        const unsigned key = (unsigned)(e >> 32);
+        const unsigned key = (unsigned)(e >> kKeyShift);
         mn = min(mn, key);
         mx = max(mx, key);
         ++have;
@@ -82,14 +83,15 @@ static __device__ __noinline__ entry_t select_threshold(const entry_t* list, int
         __syncthreads();
         return 1;
     }
-    entry_t lo = (entry_t)sh->least << 32, hi = ((entry_t)sh->most << 32) | 0xffffffffu;
+    E lo = (E)sh->least << kKeyShift, hi = (E)(((E)sh->most << kKeyShift) | (((E)1 << kKeyShift) - 1));
     // Each step leaves a range of at most 2^-7 of the one before.
 #pragma unroll 1
     for (int step = 0; step < 10; ++step) {
-        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - kSelBinBits);
+        const int width = sizeof(E) == 8 ? 64 - __clzll((long long)(hi - lo)) : 32 - __clz((int)(hi - lo));
+        const int shift = max(0, width - kSelBinBits);
 #pragma unroll 1
     for (int i = tid; i < n; i += nt) {
-            const entry_t e = list[i];
+            const E e = list[i];
             if (e >= lo && e <= hi) atomicAdd(&sh->bins[(int)((e - lo) >> shift)], 1u);
         }
         __syncthreads();
@@ -120,16 +122,16 @@ static __device__ __noinline__ entry_t select_threshold(const entry_t* list, int
                     else
                         --bin;
                 }
-                const entry_t nlo = lo + ((entry_t)bin << shift);
+                const E nlo = lo + ((E)bin << shift);
                 sh->done = shift == 0 || sh->above + cum <= k + slack;
                 sh->above += cum - here;
                 sh->lo = nlo;
-                sh->hi = min(hi, nlo + (((entry_t)1 << shift) - 1));
+                sh->hi = min(hi, (E)(nlo + (((E)1 << shift) - 1)));
             }
         }
         __syncthreads();
-        lo = sh->lo;
-        hi = sh->hi;
+        lo = (E)sh->lo;
+        hi = (E)sh->hi;
         if (sh->done) break;
 #pragma unroll 1
     for (int i = tid; i < kSelBins; i += nt) sh->bins[i] = 0;
@@ -137,6 +139,14 @@ static __device__ __noinline__ entry_t select_threshold(const entry_t* list, int
     }
     __syncthreads();  // *sh is free for the next use
     return lo;
+}
+
+// Each entry's place among n entries in falling order, by counting the larger ones.
+__device__ __forceinline__ int place_of(entry_t e, const entry_t* list, int n) {
+    int r = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) r += list[i] > e;
+    return r;
 }
 
 // The k largest, or all, of the entries >= floor among n, in falling order, into `out`; returns how many
