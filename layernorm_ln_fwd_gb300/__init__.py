@@ -441,18 +441,27 @@ def _on(device, stream):
     return _HERE_ALREADY
 
 
-def _current_raw_stream(device):
-    """The handle of the device's current stream (without building a Stream object, 2 us, where
-    torch has a way)."""
+def _find_raw_stream():
+    """device index -> handle of its current stream, without building a Stream object (2 us) where
+    torch has a way."""
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_raw_stream = None
+_entries = {}
 
 
 def _entry(op: str, dtype):
-    """(name, function) of an entry point for the dtype."""
-    name = op + _suffix(dtype)
-    return name, getattr(lib(), name)
+    """(name, function, raw_stream) of an entry point for the dtype."""
+    global _raw_stream
+    found = _entries.get((op, dtype))
+    if found is None:
+        name = op + _suffix(dtype)
+        _raw_stream = _raw_stream or _find_raw_stream()
+        found = _entries[op, dtype] = name, getattr(lib(), name), _raw_stream
+    return found
 
 
 def _addr(t):
@@ -475,7 +484,7 @@ def logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy
     import torch
     empty, f32, i32 = torch.empty, torch.float32, torch.int32
     rows, V, ld = _rows_of(logits, "logits")
-    name, fn = _entry("ln_logprobs_", logits.dtype)
+    name, fn, raw_stream = _entry("ln_logprobs_", logits.dtype)
     dev = logits.device
     if tokens is not None:
         _need(tokens, "tokens", (rows,), i32, dev)
@@ -507,7 +516,7 @@ def logprobs(logits, tokens=None, scale: float = 1.0, top: int = 0, want_entropy
                 top_logp = empty((rows, top), dtype=f32, device=dev)
         _check(name, fn(logits.data_ptr(), ld, _addr(tokens), rows, V, float(scale), int(top),
                         _addr(logp), _addr(entropy), lse.data_ptr(), _addr(ranks), _addr(top_ids),
-                        _addr(top_logp), _current_raw_stream(dev)))
+                        _addr(top_logp), raw_stream(dev.index)))
     return logp, entropy, lse, ranks, top_ids, top_logp
 
 
@@ -519,7 +528,7 @@ def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, s
     are 0 get 0 whatever they hold.  Returns dlogits; ``in_place`` writes it over the logits."""
     import torch
     rows, V, ld = _rows_of(logits, "logits")
-    name, fn = _entry("ln_logprobs_bwd_", logits.dtype)
+    name, fn, raw_stream = _entry("ln_logprobs_bwd_", logits.dtype)
     dev = logits.device
     for t, what in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
         if t is not None:
@@ -538,7 +547,7 @@ def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, s
         dlogits, ldd = _gradient_of(logits, ld, dlogits, in_place)
         _check(name, fn(logits.data_ptr(), ld, _addr(tokens), lse.data_ptr(), _addr(entropy),
                         _addr(dlogp), _addr(dentropy), rows, V, float(scale), dlogits.data_ptr(), ldd,
-                        _current_raw_stream(dev)))
+                        raw_stream(dev.index)))
     return dlogits
 
 
@@ -555,7 +564,7 @@ def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float
     weights * scale * (q - p at the ids).  ``in_place`` writes the gradient over the logits."""
     import torch
     rows, V, ld = _rows_of(logits, "logits")
-    name, fn = _entry("ln_distill_", logits.dtype)
+    name, fn, raw_stream = _entry("ln_distill_", logits.dtype)
     dev = logits.device
     if ids is None or ids.dim() != 2:
         raise ValueError("ids must be 2-D [rows, K]")
@@ -574,7 +583,7 @@ def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float
             dlogits, ldd = _gradient_of(logits, ld, dlogits, in_place)
         _check(name, fn(logits.data_ptr(), ld, ids.data_ptr(), teacher.data_ptr(), _addr(weights),
                         rows, V, K, float(scale), float(dloss), _addr(losses), _addr(dlogits), ldd,
-                        _current_raw_stream(dev)))
+                        raw_stream(dev.index)))
     return losses, dlogits
 
 
