@@ -315,7 +315,7 @@ ln_status ln_xent_bf16(const ln_bf16* logits, const int32_t* targets, int64_t ro
  *   logits    [rows, V], row r at logits + r * ld (ld >= V; rows of a padded vocabulary, say)
  *   tokens    [rows] int32, or NULL (then logp and ranks must be NULL).  A negative token is no
  *             token (a padded position): logp 0, rank 0.  One of V or more: logp NaN, rank 0.
- *   scale     1 / temperature, finite and > 0
+ *   scale     1 / temperature, > 0 and finite (after a product with log2 e, too)
  *   top       0 <= top <= LN_MAX_TOP; more than V is allowed
  *   logp      [rows] fp32        may be NULL
  *   entropy   [rows] fp32        may be NULL
@@ -326,9 +326,10 @@ ln_status ln_xent_bf16(const ln_bf16* logits, const int32_t* targets, int64_t ro
  *
  * At least one output must be given.  A logit of -inf has probability 0 and adds nothing to the
  * entropy.  A row that holds NaN or +inf has no distribution, nor has one whose logits are all
- * -inf: its logp and entropy are NaN (lse is -inf for the latter).  Outputs must not overlap the
- * inputs.  Limits: 1 <= V <= LN_XENT_MAX_V, 0 <= rows <= LN_MAX_ROWS.  Other conventions and
- * errors as for ln_fwd_*; nothing is allocated, and results are bitwise repeatable.
+ * -inf: its logp and entropy are NaN (lse is -inf for the latter); its alternatives' ids are as for
+ * any row.  Outputs must not overlap the inputs.  Limits: 1 <= V <= LN_XENT_MAX_V, 0 <= rows <= LN_MAX_ROWS.  Other conventions and
+ * errors as for ln_fwd_*; nothing is allocated, and results are bitwise repeatable for the same
+ * sizes and addresses (modulo 16).
  */
 #define LN_MAX_TOP 256
 

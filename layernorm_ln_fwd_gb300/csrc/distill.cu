@@ -68,7 +68,7 @@ struct __align__(16) DsShared {
     float2 total[2][kDsMaxCluster * kDsMaxWarps];
     // The blocks' entries, for the first block's loss: the largest of their x, sum p, sum p (x - largest).
     float4 list[2][kDsMaxCluster];
-    int table[kDsTable];                             // columns seen in a list
+    int table[kDsTable];  // columns seen in a list
 };
 
 // A block's slice of a row: vectors [lo, hi), of which [lo, mid) are kept in shared memory.
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
             if (learn) {
                 const int turn = (int)(meetings & 1u);
                 if (blocks > 1 && lane == 0)
-                    mbar_arrive_expect_tx(&sh.met[turn], (unsigned)blocks * kWarps * 8u + 16u * (rank == 0 ? (unsigned)blocks : 1u));
+                    mbar_arrive_expect_tx(&sh.met[turn], (unsigned)blocks * kWarps * 8u +
+                                                             16u * (rank == 0 ? (unsigned)blocks : 1u));
                 if (!dead || blocks == 1) gone = !meet();
                 ++meetings;
                 a = all_total(sh.total[turn], blocks * kWarps, p.c);
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_short_kernel(const DsPa
     float pk = 0.f;
     if (id >= 0) {
         pk = ex2_fast((t - most) * p.c) / sum;
-        unsigned at = ((unsigned)id * 0x9e3779b1u) % kTable;
+        unsigned at = ((unsigned)id * 0x9e3779b1u >> 22) % kTable;
         while (true) {
             const int old = atomicCAS(&sh_table[at], -1, id);
             twin = old == id;

@@ -443,7 +443,8 @@ namespace lnk {
 namespace {
 // Sizes shared by the operators over rows of logits.
 ln_status check_logits(int64_t ld, int64_t rows, int64_t V, float scale) {
-    if (!std::isfinite(scale) || scale <= 0.f) return LN_EINVAL;
+    // (times log2 e as well: the kernels work in powers of two)
+    if (!std::isfinite(scale * 1.4426950408889634f) || !(scale > 0.f)) return LN_EINVAL;
     if (rows < 0 || V <= 0 || ld < V) return LN_EINVAL;
     if (rows > LN_MAX_ROWS || V > LN_XENT_MAX_V) return LN_EUNSUPPORTED;
     // A row's address must stay within 63 bits of byte offset.

@@ -97,6 +97,62 @@ def test_in_place(dtype):
         assert b.data_ptr() == x.data_ptr() and torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("dtype,rows,V,K", [("bf16", 700, 20003, 40), ("f32", 500, 10007, 70), ("bf16", 200, 50304, 256),
+                                            ("bf16", 340, 66001, 9)])
+def test_many_rows_of_all_kinds(dtype, rows, V, K):
+    """Blocks that take several rows each: rows of weight 0 and without entries, one after another and
+    between others, short lists, repeated columns and a column outside the row, next to each other."""
+    x = R.logits(rows, V, dtype, V)
+    ids, t = teacher_of(rows, V, K, V)
+    g = torch.Generator().manual_seed(V)
+    kind = torch.randint(0, 7, (rows,), generator=g).cuda()
+    w = torch.where(kind == 0, 0.0, torch.rand(rows, generator=g).cuda() + 0.5)
+    w[rows // 3: rows // 2] = 0
+    ids[kind == 1] = -1
+    t[kind == 2] = -float("inf")
+    twice = kind == 3
+    ids[twice, K // 2:] = ids[twice, : K - K // 2]
+    ids[kind == 4, -1] = ids[kind == 4, 0]
+    ids[(kind == 5) & (torch.arange(rows).cuda() % 5 == 0), 0] = V
+    check(x, ids, t, w, scale=0.6, dtype=dtype)
+
+
+@pytest.mark.parametrize("V,rows", [(1000, 5), (5000, 5), (50304, 200), (131072, 3)])
+@pytest.mark.parametrize("step", [256, 1024, 2048])
+def test_columns_at_equal_distances(V, rows, step):
+    """Lists whose columns meet in a table by their low bits, if it goes by those."""
+    K = min(200, V // step)
+    ids = (torch.arange(K) * step).flip(0).repeat(rows, 1).to(torch.int32).cuda()
+    t = torch.randn(rows, K, generator=torch.Generator().manual_seed(V)).cuda()
+    check(R.logits(rows, V, "bf16", V), ids, t, dtype="bf16") if K else None
+
+
+@pytest.mark.parametrize("dtype,V,rows", [("bf16", 131072, 160), ("bf16", 65537, 333), ("f32", 150001, 80),
+                                          ("f32", 262144, 155)])
+def test_wide_rows_of_a_batch_in_place(dtype, V, rows):
+    """Rows that do not fit a block's shared memory whole, in place and not, against torch in 64 bits."""
+    x = R.logits(rows, V, dtype, rows)
+    g = torch.Generator().manual_seed(V)
+    ids = (torch.randint(0, V // 12, (rows, 12), generator=g) * 12 + torch.arange(12)).to(torch.int32).cuda()
+    t = torch.randn(rows, 12, generator=g).cuda()
+    la, a = ln.distill(x, ids, t, dloss=1.0 / rows)
+    full = x.clone()
+    lb, b = ln.distill(full, ids, t, dloss=1.0 / rows, in_place=True)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(la, lb) and b.data_ptr() == full.data_ptr()
+    for r in (0, 1, rows // 2, rows - 1):
+        xr = x[r].double()
+        p = torch.softmax(t[r].double(), 0)
+        lq = torch.log_softmax(xr, 0)
+        want = (p * (p.log() - lq[ids[r].long()])).sum()
+        grad = (lq.exp().index_add(0, ids[r].long(), -p)) / rows
+        # the entropy of such a row is ~10: E of vocabref.py with A = 12 and a chain of V / 256
+        E = R.U * (136 + V / 256)
+        assert abs(la[r].double() - want) <= E + 400 * R.U
+        err = (a[r].double() - grad).abs()
+        assert (err <= R.HALF[dtype] * grad.abs() + (lq.exp() + 1e-3) * (E + 100 * R.U) / rows + 1e-30).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_that_teach_nothing(dtype):
     V = 700
@@ -209,6 +265,36 @@ def test_teacher_to_student_to_policy(dtype):
     assert (hard + logp).abs().max() < 2e-5 and (hard - xl).abs().max() < 2e-5
     step = 2 * R.HALF[dtype] * xg.float().abs() + 2e-6
     assert ((g.float() - xg.float()).abs() <= step).all() and ((gh.float() - xg.float()).abs() <= step).all()
+
+
+def test_operators_in_a_captured_chain():
+    """Teacher to student to policy, captured once and replayed on new logits, the same as eager calls."""
+    rows, V, K = 60, 40001, 20
+    teacher, student = R.logits(rows, V, "bf16", 1), R.logits(rows, V, "bf16", 2)
+    dl = torch.full((rows,), -1.0 / rows, device="cuda")
+
+    def chain():
+        _, _, _, _, ids, lp = ln.logprobs(teacher, top=K, want_entropy=False)
+        losses, dx = ln.distill(student, ids, lp, scale=0.5)
+        tok = ids[:, 0].contiguous()
+        logp, ent, lse, ranks, _, _ = ln.logprobs(student, tok, want_ranks=True)
+        return losses, dx, logp, ent, ranks, ln.logprobs_bwd(student, tok, lse, ent, dl, dl)
+
+    chain()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = chain()
+    for seed in (3, 4):
+        teacher.copy_(R.logits(rows, V, "bf16", seed))
+        student.copy_(R.logits(rows, V, "bf16", seed + 10))
+        for _ in range(5):
+            g.replay()
+        eager = chain()
+        torch.cuda.synchronize()
+        for u, v in zip(out, eager):
+            assert torch.equal(u, v)
+    assert ln.device_check() == 0
 
 
 def test_refusals():

@@ -292,6 +292,29 @@ def test_repeatable_on_streams_and_in_graphs():
     assert torch.equal(first[4].flip(0), out[4]) and torch.equal(first[3].flip(0), out[3])
 
 
+def test_rows_past_32_bits_of_elements():
+    """17000 rows of 131072: the last ones lie more than 2^31 elements behind the first."""
+    rows, V, K = 17000, 131072, 4
+    x = torch.empty(rows, V, dtype=torch.bfloat16, device="cuda").normal_()
+    last = slice(rows - 3, rows)
+    t = tokens_of(rows, V, 0)
+    out = ln.logprobs(x, t, top=5, want_ranks=True)
+    torch.cuda.synchronize()
+    R.check_logprobs(tuple(o[last] for o in out), R.to64(x[last]), t[last], 1.0, 5)
+    dl = torch.ones(rows, device="cuda")
+    g = ln.logprobs_bwd(x, t, out[2], dlogp=dl)
+    few = ln.logprobs_bwd(x[last].contiguous(), t[last].contiguous(), out[2][last].contiguous(), dlogp=dl[last].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(g[last], few)
+    del few
+    losses, d = ln.distill(x, out[4][:, :K].contiguous(), out[5][:, :K].contiguous(), dlogits=g)
+    small, ds = ln.distill(x[last].contiguous(), out[4][last, :K].contiguous(), out[5][last, :K].contiguous())
+    torch.cuda.synchronize()
+    # the same rows, split otherwise over blocks: sums in another order
+    assert (losses[last] - small).abs().max() < 2e-5
+    assert (d[last].float() - ds.float()).abs().max() <= 2.0 ** -8 and (d[last] != ds).float().mean() < 0.01
+
+
 def test_refusals():
     x, t = R.logits(4, 16, "f32", 1), tokens_of(4, 16, 1)
     f = torch.zeros(4, device="cuda")

@@ -26,7 +26,7 @@ def test_logprobs_arguments(lib):
             return f(x, ld, tok, rows, V, scale, top, logp, ent, lse, ranks, ids, lp, N)
         assert call(x=N) == 1 and call(tok=N) == 1 and call(logp=N) == 1
         assert call(rows=-1) == 1 and call(V=0) == 1 and call(ld=7) == 1
-        for bad in (0.0, -1.0, float("inf"), float("nan")):
+        for bad in (0.0, -1.0, float("inf"), float("nan"), 3e38):  # (3e38 log2 e is not finite)
             assert call(scale=bad) == 1
         assert call(top=-1) == 1 and call(top=2) == 1 and call(top=2, ids=P) == 1 and call(top=2, lp=P) == 1
         assert call(ids=P, lp=P) == 1  # alternatives of none

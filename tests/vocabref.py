@@ -122,8 +122,8 @@ def tol_distill(x64, ids, teacher, w, scale, dloss, ref, dtype):
     tl, tg = np.zeros(rows), np.zeros((rows, V))
     for r in range(rows):
         kept = (ids[r] >= 0) & (ids[r] < V)
-        if not kept.any() or w[r] == 0:
-            continue
+        if w[r] == 0 or not (kept & (teacher[r] != -np.inf)).any():
+            continue  # nothing to learn from: 0 exactly
         with np.errstate(all="ignore"):
             u = np.where(kept, scale * teacher[r], -np.inf)
             dk = u.max() - u
