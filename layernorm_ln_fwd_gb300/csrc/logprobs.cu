@@ -21,7 +21,7 @@ constexpr int kLpSegments = 2048;   // segments of a slice at most, about
 constexpr int kLpCand = 1024;       // candidates held at once
 constexpr int kLpCount = 128;       // entries that are put in order by counting
 constexpr int kLpFlagged = 2 * LN_MAX_TOP;
-constexpr int kLpLoose = 16;        // at least 2 * (kVec - 1) loose elements of a row
+constexpr int kLpLoose = 32;        // more than the loose elements of a row cut at 32 bytes
 constexpr int kLpMaxCluster = 8;
 
 struct LpParams {
@@ -75,7 +75,7 @@ struct LpShare {
 // kLpCand.
 template <typename T>
 __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, int lo, int hi,
-                                           const RowCut<T>& cut, TopShared* sh, const unsigned* segs) {
+                                           const RowCut<T, 32>& cut, TopShared* sh, const unsigned* segs) {
     using IO = Io<T>;
     constexpr int kVec = IO::kVec;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, k = p.top;
@@ -115,7 +115,8 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
                 if (w >= items) continue;
                 const int q = w >> p.seg_shift, i = w & ((1 << p.seg_shift) - 1);
                 const int seg = listed ? sh->flagged[q] : q;
-                const int v = lo + (seg & (nt - 1)) + nt * ((seg >> p.nt_shift << p.seg_shift) + i);
+                const int first = (seg >> p.nt_shift << p.seg_shift) + (i & ~(kBatch - 1));  // of the batch
+                const int v = pair_vector(lo + 2 * (seg & (nt - 1)) + nt * first, nt, i & (kBatch - 1));
                 if (v < hi) u[b] = __ldcg(xv + v);
                 col[b] = cut.col(v);
             }
@@ -186,13 +187,13 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
     pdl_enter();
     const size_t row = blockIdx.x / (unsigned)blocks;
     const T* xr = static_cast<const T*>(p.x) + row * (size_t)p.ld;
-    const RowCut<T> cut(xr, p.V);
+    const RowCut<T, 32> cut(xr, p.V);
     const uint4* xv = reinterpret_cast<const uint4*>(xr + cut.head);
-    const int per = (cut.nvec + blocks - 1) / blocks;
+    const int per = ((cut.nvec + blocks - 1) / blocks + 1) & ~1;  // whole pairs
     const int lo = min(cut.nvec, rank * per), hi = min(cut.nvec, lo + per);
     const int step = kBatch * nt;
     uint4 u[kBatch];
-    load_batch<T>(u, xv, lo + tid, nt, hi);
+    load_pairs<T>(u, xv, lo + 2 * tid, nt, hi);
     const int t = p.tokens ? p.tokens[row] : -1;
     const bool has = t >= 0 && t < p.V;
     const float nan = __int_as_float(0x7fc00000);
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
         if (m > over) above += count_above<T>(b, over);
         if (m > -INFINITY)
             s.template add_batch<T>(b, c2, [&](int k) {
-                const int v = v0 + k * nt;
+                const int v = pair_vector(v0, nt, k);
                 return v < hi ? __ldcg(xv + v) : no_logits<T>();
             });
         if constexpr (TOP) {
@@ -224,12 +225,12 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
             }
         }
     };
-    for (int v0 = lo + tid; v0 < hi; v0 += 2 * step) {
+    for (int v0 = lo + 2 * tid; v0 < hi; v0 += 2 * step) {
         uint4 ahead[kBatch];
-        load_batch<T>(ahead, xv, v0 + step, nt, hi);
+        load_pairs<T>(ahead, xv, v0 + step, nt, hi);
         take(u, v0);
         if (v0 + step >= hi) break;
-        load_batch<T>(u, xv, v0 + 2 * step, nt, hi);
+        load_pairs<T>(u, xv, v0 + 2 * step, nt, hi);
         take(ahead, v0 + step);
     }
     if constexpr (TOP) {
@@ -357,7 +358,7 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     const int nvec = a.V / kVec;
     const int sms = device_info(-1).sms;
     const int blocks = logprobs_cluster(a.rows, nvec, sms);
-    const int slice = (nvec + blocks - 1) / blocks;
+    const int slice = ((nvec + blocks - 1) / blocks + 1) & ~1;
     const int most = logprobs_threads(a.rows, a.top > 0, sms);
     // A batch for every thread, if there are that many; the selection of a top is work for 4 warps.
     int nt = a.top > 0 ? 128 : 32;

@@ -12,17 +12,17 @@ namespace lnk {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A row of V logits at any element-aligned address: `head` loose elements up to the first
-// 16-byte boundary, `nvec` aligned vectors, `tail` loose elements behind them.  Rows of an odd
-// length one after another start at a different place of a vector each; cutting every row at its
-// own boundaries keeps all but at most 2 * (kVec - 1) elements on 16-byte accesses.
-template <typename T>
+// A row of V logits at any element-aligned address: `head` loose elements up to the first boundary of
+// BYTES (16, or 32 where vectors are taken in pairs), `nvec` 16-byte vectors, `tail` loose elements
+// behind them.  Rows of an odd length one after another start at a different place of a vector each;
+// cutting every row at its own boundaries keeps all but a few elements on wide accesses.
+template <typename T, int BYTES = 16>
 struct RowCut {
     int head, nvec, tail;
     __device__ __forceinline__ RowCut(const T* row, int V) {
-        constexpr int kVec = Io<T>::kVec;
-        const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
-        head = min(V, (kVec - mis) % kVec);
+        constexpr int kVec = Io<T>::kVec, kUnit = BYTES / (int)sizeof(T);
+        const int mis = (int)(reinterpret_cast<uintptr_t>(row) & (BYTES - 1u)) / (int)sizeof(T);
+        head = min(V, (kUnit - mis) % kUnit);
         nvec = (V - head) / kVec;
         tail = V - head - nvec * kVec;
     }
@@ -55,6 +55,30 @@ __device__ __forceinline__ void load_batch(uint4 (&u)[kBatch], const uint4* xv, 
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int v = v0 + k * step;
+            u[k] = v < end ? __ldcg(xv + v) : no_logits<T>();
+        }
+    }
+}
+
+// The same with a batch of two pairs of neighbouring vectors, the second pair 2 * step behind the first,
+// each pair one 256-bit access (v0 even, the row cut at 32 bytes): a thread's vectors fill whole
+// 32-byte sectors, which counts when few of them are read again.
+__device__ __forceinline__ int pair_vector(int v0, int step, int k) { return v0 + (k >> 1) * 2 * step + (k & 1); }
+template <typename T>
+__device__ __forceinline__ void load_pairs(uint4 (&u)[kBatch], const uint4* xv, int v0, int step, int end) {
+    static_assert(kBatch == 4, "two pairs");
+    if (v0 + 2 * step + 1 < end) {
+#pragma unroll
+        for (int k = 0; k < kBatch; k += 2) {
+            uint4 &a = u[k], &b = u[k + 1];
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                         : "l"(xv + v0 + k * step));
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = pair_vector(v0, step, k);
             u[k] = v < end ? __ldcg(xv + v) : no_logits<T>();
         }
     }
