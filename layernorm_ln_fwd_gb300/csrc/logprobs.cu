@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kLpMaxThreads = 512;
 constexpr int kLpSegments = 2048;   // segments of a slice at most, about
-constexpr int kLpCand = 1024;       // candidates held at once
+constexpr int kLpCand = 512;        // candidates held at once
 constexpr int kLpCount = 128;       // entries that are put in order by counting
 constexpr int kLpFlagged = 2 * LN_MAX_TOP;
 constexpr int kLpLoose = 32;        // more than the loose elements of a row cut at 32 bytes
@@ -30,7 +30,7 @@ struct LpParams {
     const int* tokens;
     int V;
     int top;
-    int seg_shift;  // log2 of the vectors of a thread that share a segment (kBatch or more)
+    int seg_shift;  // log2 of the vectors of a thread that share a segment: whole batches, or one vector (0)
     int nt_shift;   // log2 of the block's threads
     int nseg;     // segments of batches: a multiple of the block's threads
     float scale, c;  // c = scale * log2 e
@@ -115,8 +115,8 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
                 if (w >= items) continue;
                 const int q = w >> p.seg_shift, i = w & ((1 << p.seg_shift) - 1);
                 const int seg = listed ? sh->flagged[q] : q;
-                const int first = (seg >> p.nt_shift << p.seg_shift) + (i & ~(kBatch - 1));  // of the batch
-                const int v = pair_vector(lo + 2 * (seg & (nt - 1)) + nt * first, nt, i & (kBatch - 1));
+                const int f = (seg >> p.nt_shift << p.seg_shift) + i;  // of the thread's vectors
+                const int v = pair_vector(lo + 2 * (seg & (nt - 1)) + nt * (f & ~(kBatch - 1)), nt, f & (kBatch - 1));
                 if (v < hi) u[b] = __ldcg(xv + v);
                 col[b] = cut.col(v);
             }
@@ -216,6 +216,14 @@ __global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpPara
                 return v < hi ? __ldcg(xv + v) : no_logits<T>();
             });
         if constexpr (TOP) {
+            if (p.seg_shift == 0) {  // a short row: this batch is the thread's only one
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k, seg += nt) {
+                    const float mk = vector_max<T>(b[k]);
+                    segs[seg] = mk > -INFINITY ? order_key(mk) : 0;
+                }
+                return;
+            }
             best = fmaxf(best, m);
             if (--left == 0) {
                 segs[seg] = best > -INFINITY ? order_key(best) : 0;
@@ -324,7 +332,7 @@ const void* logprobs_variant(bool ent, bool top) {
 // Blocks a row is split over: as many as leave every SM no more than two blocks, of no less than 2048
 // vectors each.  (One row of 131072 bf16 logits, top 20: 14.5 us in one block, 10.0 in 4, 9.6 in 8, 11.9
 // in 16; of 16384 logits: 6.8 us in one block, 7.7 in 4.  64 rows of 131072: 18.2, 12.5 in 4, 16.0
-// in 8; 200 rows: 25.4, 26.3 in 2.)
+// in 8; 200 rows: 25.4, 26.3 in 2.  Taken with 256 threads.)
 int logprobs_cluster(int rows, int nvec, int sms) {
     int blocks = 1;
     while (blocks < kLpMaxCluster && (long long)rows * blocks * 2 <= 2 * sms && nvec / (blocks * 2) >= 2048)
@@ -333,10 +341,9 @@ int logprobs_cluster(int rows, int nvec, int sms) {
 }
 
 // Threads of a block at most, a power of two: 256, four blocks an SM.  Where there are rows for more than
-// a wave of smaller blocks and no top to select, 128: a row's fixed costs are by the warp (4096 x
-// 50257 bf16: 68 us, 72 with 256; but 700 x 50304: 28 us, 22 with 256; with the top 64 of 2048 x 131072:
-// 143 us, 123 with 256).
-int logprobs_threads(int rows, bool top, int sms) { return !top && rows > 8 * sms ? 128 : 256; }
+// a wave of smaller blocks, 128: a row's fixed costs are by the warp (4096 x 50257 bf16: 68 us, 72 with
+// 256; 4096 x 32000 with the top 20: 69 us, 80 with 256; but 700 x 50304: 28 us, 22 with 256).
+int logprobs_threads(int rows, int sms) { return rows > 8 * sms ? 128 : 256; }
 
 template <typename T>
 cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
@@ -359,10 +366,13 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     const int sms = device_info(-1).sms;
     const int blocks = logprobs_cluster(a.rows, nvec, sms);
     const int slice = ((nvec + blocks - 1) / blocks + 1) & ~1;
-    const int most = logprobs_threads(a.rows, a.top > 0, sms);
-    // A batch for every thread, if there are that many; the selection of a top is work for 4 warps.
-    int nt = a.top > 0 ? 128 : 32;
-    p.nt_shift = a.top > 0 ? 7 : 5;
+    const int most = logprobs_threads(a.rows, sms);
+    // A batch for every thread, if there are that many.  The selection of a top is work for 4 warps
+    // (1000 x 1024, top 20: 8.3 us), but for one where rows abound: more of them run at once (8192 x 1000,
+    // top 20: 36 us, 44 with two warps, 61 with four).
+    const int least = a.top > 0 && a.rows <= 8 * sms ? 7 : 5;  // log2
+    int nt = 1 << least;
+    p.nt_shift = least;
     while (nt < most && nt * kBatch < slice) {
         nt *= 2;
         ++p.nt_shift;
@@ -379,6 +389,12 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
         ++p.seg_shift;
     }
     p.nseg = (per + seglen - 1) / seglen * nt;
+    // Short rows have few batches: a segment for every vector, or all of the row would be candidates
+    // (8192 x 256 with the top 10, four warps: 53 us, 63 with a segment for each batch).
+    if (per == 1) {
+        p.seg_shift = 0;
+        p.nseg = kBatch * nt;
+    }
     const bool top = a.top > 0, ent = a.entropy != nullptr;
     size_t smem = 0;
     if (top) {
