@@ -16,7 +16,7 @@
 namespace lnk {
 namespace {
 
-constexpr int kLpMaxThreads = 512;
+constexpr int kLpMaxThreads = 256;  // four such blocks an SM, of 64 registers a thread
 constexpr int kLpSegments = 2048;   // segments of a slice at most, about
 constexpr int kLpCand = 512;        // candidates held at once
 constexpr int kLpCount = 128;       // entries that are put in order by counting
@@ -32,7 +32,7 @@ struct LpParams {
     int top;
     int seg_shift;  // log2 of the vectors of a thread that share a segment: whole batches, or one vector (0)
     int nt_shift;   // log2 of the block's threads
-    int nseg;     // segments of batches: a multiple of the block's threads
+    int nseg;       // segments: a multiple of the block's threads
     float scale, c;  // c = scale * log2 e
     float* logp;
     float* entropy;
@@ -170,8 +170,14 @@ __device__ __forceinline__ int put_in_order(const entry_t* list, int n, int k, e
 // One row a block, or a cluster of blocks (CLUSTER) that take a slice of it each: few rows are
 // spread over many SMs, and a slice's results meet in the first block's shared memory.  A row's
 // slice is read once, a batch of each thread in flight while the one before is summed.
+//
+// Bound by the one read of the logits where no top is asked for: 4096 x 50257 bf16 with the entropy
+// takes 68 us, 6.0 TB/s (about 35 instructions a vector of 8, 55 % of the issue slots).  With a top,
+// the selection's instructions and its chain of barriers, a few us of a block's time, weigh as much as the
+// reading of a row of some 10^4 logits: 2048 x 131072 with the top 64 takes 108 us (5.0 TB/s), 4096 x
+// 32000 with the top 20 69 us.  One row is the length of that chain: 9.3 us with the top 20, 3.6 without.
 template <typename T, bool ENT, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kLpMaxThreads, 2) logprobs_kernel(const LpParams p) {
+__global__ void __launch_bounds__(kLpMaxThreads, 4) logprobs_kernel(const LpParams p) {
     using IO = Io<T>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ RowTotal sh_total[kLpMaxThreads / 32];
@@ -414,7 +420,8 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------------------
 // The gradient.  The forward left L and H, so every element stands for itself: one warp takes a
 // piece of a row (some batches a lane), reads it, and writes the gradient of the same
-// elements, which may be the logits' own place.
+// elements, which may be the logits' own place.  Bound by the read and the write: 4096 x 50257 bf16 with
+// the entropy's part takes 126 us, 6.5 TB/s, 0.98 of what a copy gets.
 // ---------------------------------------------------------------------------------------
 constexpr int kLbThreads = 256;
 constexpr int kLbBlocksPerSm = 4;
