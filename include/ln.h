@@ -395,7 +395,7 @@ ln_status ln_logprobs_bwd_bf16(const ln_bf16* logits, int64_t ld, const int32_t*
  *
  * At least one of losses and dlogits must be given.  A row without entries (or with teacher logits
  * of -inf only), or of weight 0, has loss 0 and gradient 0 whatever its logits hold (they are not
- * read).  An entry of weight p_k = 0 adds nothing, even where the student has -inf; elsewhere a
+ * used, and those of a row of weight 0 not read).  An entry of weight p_k = 0 adds nothing, even where the student has -inf; elsewhere a
  * student's -inf gives an infinite loss.  Limits: 1 <= K <= LN_MAX_TOP, 1 <= V <= LN_XENT_MAX_V,
  * 0 <= rows <= LN_MAX_ROWS.  Other conventions and errors as for ln_fwd_*; nothing is allocated,
  * and results are bitwise repeatable.

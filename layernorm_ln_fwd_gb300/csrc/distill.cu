@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                             u[k] = v0 + k * NT < to ? xs[v0 + k * NT] : no_logits<T>();
                     }
                     if (s.see_batch<T>(u, p.c) > -INFINITY)
-                        s.add_batch<T>(u, c2, [&](int k) { return u[k]; });
+                        s.add_batch<T>(u, c2);
                 }
             }
             phases ^= 1u << slot;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         if (learn) {
             each_batch(g, [&](const uint4 (&u)[kBatch], int) {
                 if (s.see_batch<T>(u, p.c) > -INFINITY)
-                    s.add_batch<T>(u, c2, [&](int k) { return u[k]; });
+                    s.add_batch<T>(u, c2);
             });
             const float xl = has_loose ? IO::to_f(g.xr[g.cut.loose(tid)]) : 0.f;
             if (has_loose) s.add_one(xl, p.c);
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_short_kernel(const DsPa
     s.clear();
     const f2 c2 = f2_splat(p.c);
     if (tid < cut.nvec && s.see_batch<T>(u, p.c) > -INFINITY)
-        s.add_batch<T>(u, c2, [&](int k) { return u[k]; });
+        s.add_batch<T>(u, c2);
     if (has_loose) s.add_one(xl, p.c);
     RowTotal a = warp_total({s.ref, f2_lo(s.z2) + f2_hi(s.z2), 0.f}, p.c);
     if (lane == 0) sh_total[warp] = a;

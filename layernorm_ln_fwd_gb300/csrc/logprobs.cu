@@ -80,6 +80,11 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
     constexpr int kVec = IO::kVec;
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x, k = p.top;
     const int nall = p.nseg + kLpLoose;
+    // Vector i of a segment, counted from the slice's first.
+    auto vector_of = [&](int seg, int i) {
+        const int f = (seg >> p.nt_shift << p.seg_shift) + i;  // of the thread's vectors
+        return pair_vector(2 * (seg & (nt - 1)) + nt * (f & ~(kBatch - 1)), nt, f & (kBatch - 1));
+    };
     // Every element of the bound's value, whatever its column.
     entry_t bound = (entry_t)select_threshold(segs, nall, k, k / 4 + 16, &sh->sel) << 32;
     while (true) {
@@ -91,21 +96,25 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
         for (int i = tid; i < nall; i += nt) {
             const unsigned key = segs[i];
             if (key == 0 || key < reach) continue;
-            if (i < p.nseg) {
-                const int at = atomicAdd(&sh->nflag, 1);
-                if (at < kLpFlagged) sh->flagged[at] = i;
-            } else {  // a loose element
+            if (i >= p.nseg) {  // a loose element
                 const entry_t e = (entry_t)key << 32 | (uint32_t)~(uint32_t)cut.loose(i - p.nseg);
                 if (e < bound) continue;
                 const int at = atomicAdd(&sh->ncand, 1);
                 if (at < kLpCand) sh->cand[at] = e;
+                continue;
             }
+            // A segment of the bound's value has nothing behind the bound's column.
+            if (key == reach && (unsigned)cut.col(lo + vector_of(i, 0)) > ~(unsigned)bound) continue;
+            if (*(volatile int*)&sh->nflag > kLpFlagged) continue;  // too many to list
+            const int at = atomicAdd(&sh->nflag, 1);
+            if (at < kLpFlagged) sh->flagged[at] = i;
         }
         __syncthreads();
         const bool listed = sh->nflag <= kLpFlagged;  // else all segments are gone through
         const int items = (listed ? sh->nflag : p.nseg) << p.seg_shift;
 #pragma unroll 1
         for (int w0 = tid; w0 < items; w0 += kBatch * nt) {
+            if (*(volatile int*)&sh->ncand > kLpCand) break;  // another round anyway
             uint4 u[kBatch];
             int col[kBatch];
 #pragma unroll
@@ -115,24 +124,29 @@ __device__ __forceinline__ int collect_top(const LpParams& p, const uint4* xv, i
                 if (w >= items) continue;
                 const int q = w >> p.seg_shift, i = w & ((1 << p.seg_shift) - 1);
                 const int seg = listed ? sh->flagged[q] : q;
-                const int f = (seg >> p.nt_shift << p.seg_shift) + i;  // of the thread's vectors
-                const int v = pair_vector(lo + 2 * (seg & (nt - 1)) + nt * (f & ~(kBatch - 1)), nt, f & (kBatch - 1));
-                if (v < hi) u[b] = __ldcg(xv + v);
+                const unsigned key = segs[seg];
+                const int v = lo + vector_of(seg, i);
                 col[b] = cut.col(v);
+                if (v >= hi || key < reach || (key == reach && (unsigned)col[b] > ~(unsigned)bound)) continue;
+                u[b] = __ldcg(xv + v);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (!(vector_max<T>(u[b]) >= least)) continue;
                 float f[kVec];
                 IO::unpack(u[b], f);
+                unsigned take = 0;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    if (!(f[j] >= least)) continue;
-                    const entry_t e = make_entry(f[j], col[b] + j);
-                    if (e < bound) continue;
-                    const int at = atomicAdd(&sh->ncand, 1);
-                    if (at < kLpCand) sh->cand[at] = e;
-                }
+                for (int j = 0; j < kVec; ++j)
+                    take |= (unsigned)(f[j] >= least && make_entry(f[j], col[b] + j) >= bound) << j;
+                if (take == 0) continue;
+                int at = atomicAdd(&sh->ncand, __popc(take));
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (take >> j & 1u) {
+                        if (at < kLpCand) sh->cand[at] = make_entry(f[j], col[b] + j);
+                        ++at;
+                    }
             }
         }
         __syncthreads();
@@ -216,11 +230,7 @@ __global__ void __launch_bounds__(kLpMaxThreads, 4) logprobs_kernel(const LpPara
     auto take = [&](const uint4 (&b)[kBatch], int v0) {
         const float m = s.template see_batch<T>(b, p.c);
         if (m > over) above += count_above<T>(b, over);
-        if (m > -INFINITY)
-            s.template add_batch<T>(b, c2, [&](int k) {
-                const int v = pair_vector(v0, nt, k);
-                return v < hi ? __ldcg(xv + v) : no_logits<T>();
-            });
+        if (m > -INFINITY) s.template add_batch<T>(b, c2);
         if constexpr (TOP) {
             if (p.seg_shift == 0) {  // a short row: this batch is the thread's only one
 #pragma unroll

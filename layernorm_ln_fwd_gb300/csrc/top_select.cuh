@@ -90,7 +90,7 @@ static __device__ __noinline__ E select_threshold(const E* list, int n, int k, i
         const int width = sizeof(E) == 8 ? 64 - __clzll((long long)(hi - lo)) : 32 - __clz((int)(hi - lo));
         const int shift = max(0, width - kSelBinBits);
 #pragma unroll 1
-    for (int i = tid; i < n; i += nt) {
+        for (int i = tid; i < n; i += nt) {
             const E e = list[i];
             if (e >= lo && e <= hi) atomicAdd(&sh->bins[(int)((e - lo) >> shift)], 1u);
         }
@@ -134,7 +134,7 @@ static __device__ __noinline__ E select_threshold(const E* list, int n, int k, i
         hi = (E)sh->hi;
         if (sh->done) break;
 #pragma unroll 1
-    for (int i = tid; i < kSelBins; i += nt) sh->bins[i] = 0;
+        for (int i = tid; i < kSelBins; i += nt) sh->bins[i] = 0;
         __syncthreads();
     }
     __syncthreads();  // *sh is free for the next use

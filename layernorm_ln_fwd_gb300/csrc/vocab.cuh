@@ -197,20 +197,19 @@ struct RowSums {
         ref = refu = m;
         lim = fminf(m + kSlack / c, 3.402823466e38f);
     }
-    // One vector's terms.  HELD: 0 * -inf is no term of w, the exponent is held at a value whose
-    // weight is 0 as well.
-    template <typename T, bool HELD>
-    __device__ __forceinline__ void add(const uint4& v, float r, f2 c2) {
+    // One vector's terms.  0 * -inf is no term of w: the exponent is held at a value whose weight is 0 too.
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4& v, f2 c2) {
         constexpr int H = Pairs<T>::kPairs;
         f2 d[H];
-        less<T>(v, r, d);
+        less<T>(v, refu, d);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const f2 u = f2_mul(d[h], c2);
             const f2 e = f2_make(ex2_fast(f2_lo(u)), ex2_fast(f2_hi(u)));
             z2 = f2_add(z2, e);
             if constexpr (ENT)
-                w2 = f2_fma(e, HELD ? f2_make(fmaxf(f2_lo(u), -1e30f), fmaxf(f2_hi(u), -1e30f)) : u, w2);
+                w2 = f2_fma(e, f2_make(fmaxf(f2_lo(u), -1e30f), fmaxf(f2_hi(u), -1e30f)), w2);
         }
     }
     // A batch's largest value, NaN left out, after seeing it; -inf: there is nothing to add.
@@ -226,24 +225,11 @@ struct RowSums {
         }
         return m;
     }
-    // Add the batch that see_batch() has seen.  again(k): its vector k, read once more (only in
-    // batches with some -inf among others; keeping the vectors for them would cost registers).
-    template <typename T, typename Again>
-    __device__ __forceinline__ void add_batch(const uint4 (&u)[kBatch], f2 c2, Again again) {
-        const f2 w0 = w2;
+    // Add the batch that see_batch() has seen.
+    template <typename T>
+    __device__ __forceinline__ void add_batch(const uint4 (&u)[kBatch], f2 c2) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) add<T, false>(u[k], refu, c2);
-        if constexpr (ENT) {
-            // Some exponent was -inf: the batch's w again, held.
-            const float w = f2_lo(w2) + f2_hi(w2), z = f2_lo(z2) + f2_hi(z2);
-            if (w != w && z == z) {
-                const f2 z0 = z2;
-                w2 = w0;
-#pragma unroll 1
-                for (int k = 0; k < kBatch; ++k) add<T, true>(again(k), refu, c2);
-                z2 = z0;
-            }
-        }
+        for (int k = 0; k < kBatch; ++k) add<T>(u[k], c2);
     }
     __device__ __forceinline__ void add_one(float x, float c) {
         see(x, c);
