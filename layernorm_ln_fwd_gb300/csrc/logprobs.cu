@@ -186,10 +186,10 @@ __device__ __forceinline__ int put_in_order(const entry_t* list, int n, int k, e
 // slice is read once, a batch of each thread in flight while the one before is summed.
 //
 // Bound by the one read of the logits where no top is asked for: 4096 x 50257 bf16 with the entropy
-// takes 68 us, 6.0 TB/s (about 35 instructions a vector of 8, 55 % of the issue slots).  With a top,
+// takes 67 us, 6.2 TB/s (some 40 instructions a vector of 8, over half of the issue slots).  With a top,
 // the selection's instructions and its chain of barriers, a few us of a block's time, weigh as much as the
-// reading of a row of some 10^4 logits: 2048 x 131072 with the top 64 takes 108 us (5.0 TB/s), 4096 x
-// 32000 with the top 20 69 us.  One row is the length of that chain: 9.3 us with the top 20, 3.6 without.
+// reading of a row of some 10^4 logits: 2048 x 131072 with the top 64 takes 114 us (4.7 TB/s), 4096 x
+// 32000 with the top 20 70 us.  One row is the length of that chain: 9.5 us with the top 20, 3.6 without.
 template <typename T, bool ENT, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLpMaxThreads, 4) logprobs_kernel(const LpParams p) {
     using IO = Io<T>;
@@ -358,7 +358,8 @@ int logprobs_cluster(int rows, int nvec, int sms) {
 
 // Threads of a block at most, a power of two: 256, four blocks an SM.  Where there are rows for more than
 // a wave of smaller blocks, 128: a row's fixed costs are by the warp (4096 x 50257 bf16: 68 us, 72 with
-// 256; 4096 x 32000 with the top 20: 69 us, 80 with 256; but 700 x 50304: 28 us, 22 with 256).
+// 256; 4096 x 32000 with the top 20: 69 us, 80 with 256; but 700 x 50304: 28 us, 22 with 256; taken side by
+// side, before the entropy's last step).
 int logprobs_threads(int rows, int sms) { return rows > 8 * sms ? 128 : 256; }
 
 template <typename T>
