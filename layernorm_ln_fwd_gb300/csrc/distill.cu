@@ -12,8 +12,8 @@
 #include <algorithm>
 #include <math.h>
 
-#include "ln_internal.h"
 #include "vocab.cuh"
+#include "vocab_ops.h"
 
 namespace lnk {
 namespace {

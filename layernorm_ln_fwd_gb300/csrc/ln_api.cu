@@ -12,6 +12,7 @@
 #include "ln.h"
 #include "ln_device.cuh"
 #include "ln_internal.h"
+#include "vocab_ops.h"
 
 // One status word per device.  Kernels OR kStatusTimeout into it when a bounded wait runs
 // out; ln_device_check reads and clears it.

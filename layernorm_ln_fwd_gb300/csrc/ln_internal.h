@@ -100,18 +100,6 @@ bool vector_ok(Dtype dt, int cols, const void* const* ptrs, int nptrs);
 cudaError_t launch_kernel(const void* kern, dim3 grid, dim3 block, size_t smem,
                           cudaStream_t stream, void** args, bool cooperative);
 
-// Clusters of `blocks` blocks (1: blocks) of a kernel that run on the current device at once,
-// cached.
-int clusters_at_once(const void* kern, int threads, int blocks, size_t smem);
-
-// Lets `kern` have `bytes` of dynamic shared memory on the current device (asked of the driver only
-// when it is more than before).
-cudaError_t allow_smem(const void* kern, size_t bytes);
-
-// The same with clusters of `blocks` blocks along the grid (1: none; up to 8).
-cudaError_t launch_cluster(const void* kern, dim3 grid, dim3 block, int blocks, size_t smem,
-                           cudaStream_t stream, void** args);
-
 cudaError_t launch_fwd(Dtype dt, const FwdArgs& a, bool aligned, int path_override,
                        cudaStream_t stream, int* launches);
 // The RMSNorm forward: `beta` and `mean` are unused (may be null); `rstd` receives 1 / rms.
@@ -191,71 +179,6 @@ struct XentArgs {
 
 cudaError_t launch_xent(Dtype dt, const XentArgs& a, bool aligned, cudaStream_t stream,
                         int* launches);
-
-// Token log probabilities with entropy, rank and top alternatives (null outputs are left out;
-// `tokens` null: no logp and no ranks; `top` 0: no alternatives).
-struct LogprobsArgs {
-    const void* logits;
-    int64_t ld;
-    const int* tokens;
-    int rows;
-    int V;
-    float scale;
-    int top;
-    float* logp;
-    float* entropy;
-    float* lse;
-    int* ranks;
-    int* top_ids;
-    float* top_logp;
-};
-
-cudaError_t launch_logprobs(Dtype dt, const LogprobsArgs& a, cudaStream_t stream, int* launches);
-
-// Their gradient (dlogp or dentropy may be null; dlogits may alias logits).
-struct LogprobsBwdArgs {
-    const void* logits;
-    int64_t ld;
-    const int* tokens;
-    const float* lse;
-    const float* entropy;
-    const float* dlogp;
-    const float* dentropy;
-    int rows;
-    int V;
-    float scale;
-    void* dlogits;
-    int64_t ldd;
-};
-
-cudaError_t launch_logprobs_bwd(Dtype dt, const LogprobsBwdArgs& a, cudaStream_t stream,
-                                int* launches);
-
-// Distillation from a teacher's top logits: losses (optional) and dlogits (optional; may alias
-// logits).
-struct DistillArgs {
-    const void* logits;
-    int64_t ld;
-    const int* ids;
-    const float* teacher;
-    const float* weights;
-    int rows;
-    int V;
-    int K;
-    float scale;
-    float dloss;
-    float* losses;
-    void* dlogits;
-    int64_t ldd;
-    unsigned* status;  // the per-device status word (bounded waits)
-    uint64_t wait_limit_ns;
-};
-
-cudaError_t launch_distill(Dtype dt, const DistillArgs& a, cudaStream_t stream, int* launches);
-
-// Whether rows of `lda` elements at a and of `ldb` at b start at the same place of a 16-byte vector,
-// every row of them.
-bool rows_congruent(const void* a, int64_t lda, const void* b, int64_t ldb, size_t esize, int rows);
 
 // Backward of the bias + dropout + residual prologue: dh = ds * keep * scale (keep from the
 // generator, or from the bits the forward stored) and the deterministic column sums dbias (partials: [segs][cols] (hi, lo) fp32 pairs that announce

@@ -9,9 +9,9 @@
 #include <algorithm>
 #include <math.h>
 
-#include "ln_internal.h"
 #include "top_select.cuh"
 #include "vocab.cuh"
+#include "vocab_ops.h"
 
 namespace lnk {
 namespace {
