@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <math.h>
 
+#include "distill_plan.h"
 #include "vocab.cuh"
 #include "vocab_ops.h"
 
@@ -20,8 +21,6 @@ namespace {
 
 constexpr int kDsMaxWarps = 16;
 constexpr int kDsMaxCluster = 8;
-constexpr int kDsChunks = 8;  // bulk copies of a row's slice
-constexpr int kDsSlots = 2;   // rows a block holds: the one it works on and the next
 constexpr int kDsShare = LN_MAX_TOP / 32;  // a lane's entries of a teacher's list
 constexpr int kDsTable = 8 * LN_MAX_TOP;
 
@@ -35,7 +34,8 @@ struct DsParams {
     int V;
     int K;
     int staged;        // vectors of a slice that are kept in shared memory
-    int chunk;         // vectors of one bulk copy: whole batches of the block
+    int chunk;         // vectors of one bulk copy
+    int copies;        // of a slice, at most
     int blocks_shift;  // log2 of the blocks of a cluster
     float scale, c;    // c = scale * log2 e
     float dloss;
@@ -168,14 +168,19 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
 
     if (warp == kWarps) {
         // ---- The warp that starts the copies and finishes the rows.
+        SlotPhases started;
         auto issue = [&](int row, int slot) {  // lane 0
             const DsSlice<T> g(p, row, rank);
             unsigned char* to = smem_raw + 16 * (size_t)(slot * p.staged);
-            for (int i = 0, v = g.lo; v < g.mid; ++i, v += p.chunk) {
+            int i = 0;
+            for (int v = g.lo; v < g.mid; ++i, v += p.chunk) {
                 const unsigned bytes = 16u * (unsigned)(min(g.mid, v + p.chunk) - v);
                 mbar_arrive_expect_tx(&sh.full[slot][i], bytes);
                 bulk_g2s(to + 16 * (size_t)(v - g.lo), g.vectors() + v, bytes, &sh.full[slot][i]);
             }
+            // Every row arms all of the plan's copies (SlotPhases), with nothing where its slice ends before.
+            for (; i < p.copies; ++i) mbar_arrive(&sh.full[slot][i]);
+            started.used(slot);
         };
         if (lane == 0) {
             for (int i = 0; i < kDsSlots * kDsChunks; ++i) mbar_init(&sh.full[0][0] + i, 1);
@@ -244,7 +249,12 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                 __syncwarp();
             }
         }
-        if (dead && lane == 0) raise_status(p.status, kStatusTimeout);
+        if (dead && lane == 0) {
+            raise_status(p.status, kStatusTimeout);
+            for (int slot = 0; slot < kDsSlots; ++slot)  // copies still in flight
+                for (int i = 0; i < p.copies; ++i)
+                    (void)mbar_wait(&sh.full[slot][i], started.parity(slot) ^ 1u, p.limit_ns);
+        }
         end_together();
         return;
     }
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         // ---- The warp that reads the logits of the list's columns.
         pdl_enter();
         begin();
-        unsigned phases = 0;
+        SlotPhases phases;
         for (int row = first, slot = 0, n = 0; row < p.rows; row += stride, slot ^= 1, n = n == 2 ? 0 : n + 1) {
             DsRow& q = sh.row[n];
             bool gone = false;
@@ -370,8 +380,8 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                 const DsSlice<T> g(p, row, rank);
                 const T* xs = reinterpret_cast<const T*>(smem_raw + 16 * (size_t)(slot * p.staged));
                 for (int i = 0, v = g.lo; v < g.mid && !dead; ++i, v += p.chunk)
-                    gone |= !mbar_wait(&sh.full[slot][i], (phases >> slot) & 1u, p.limit_ns);
-                phases ^= 1u << slot;
+                    gone |= !mbar_wait(&sh.full[slot][i], phases.parity(slot), p.limit_ns);
+                phases.used(slot);
                 if (q.learn) {
                     // The student's logits at the list's columns, and this block's part of the loss about
                     // the largest of them.  An entry of weight 0 adds nothing, whatever the student has
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
     // ---- The warps that sum up the rows and write the gradient.
     pdl_enter();
     const f2 c2 = f2_splat(p.c);
-    unsigned phases = 0;  // bit s: the parity of slot s's next use
+    SlotPhases phases;
     // The part of a slice that is not kept, a batch in flight while the one before is dealt with.
     auto each_batch = [&](const DsSlice<T>& g, auto deal) {
         const uint4* xv = g.vectors();
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         if (q.w != 0.f) {
             // Pass 1: the slice's sums.
             for (int i = 0, from = 0; from < end; ++i, from += p.chunk) {
-                if (!dead) gone |= !mbar_wait(&sh.full[slot][i], (phases >> slot) & 1u, p.limit_ns);
+                if (!dead) gone |= !mbar_wait(&sh.full[slot][i], phases.parity(slot), p.limit_ns);
                 if (!learn) continue;
                 const int to = min(end, from + p.chunk);
                 for (int v0 = from + tid; v0 < to; v0 += kStep) {
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                         s.add_batch<T>(u, c2);
                 }
             }
-            phases ^= 1u << slot;
+            phases.used(slot);
         }
         if (learn) {
             each_batch(g, [&](const uint4 (&u)[kBatch], int) {
@@ -546,9 +556,6 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         }
         dead |= __syncthreads_or(gone);
     }
-    if (dead)  // copies still in flight
-        for (int i = 0; i < kDsSlots * kDsChunks; ++i)
-            (void)mbar_wait(&sh.full[0][0] + i, (phases >> (i / kDsChunks)) & 1u, p.limit_ns / kDsChunks);
     end_together();
 }
 
@@ -744,26 +751,13 @@ cudaError_t launch_distill_t(const DistillArgs& a, cudaStream_t stream) {
                                        : distill_short_variant<T, 512>(wide);
         return launch_kernel(kern, dim3((unsigned)a.rows), dim3(nt), 0, stream, args, false);
     }
-    constexpr int room = 100 * 64;  // vectors of a slot at most: two slots, and a block an SM
-    // Blocks of a cluster: where there are fewer rows than SMs, as many as keep them all busy; and where
-    // far more of a row than a slot would be read again.
-    int blocks = 1;
-    while (blocks < kDsMaxCluster && (nvec / blocks > 11 * room / 4 ||
-                                      ((long long)a.rows * blocks * 2 <= sms && nvec / (blocks * 2) >= 512)))
-        blocks *= 2;
-    // A row a little too long for a slot goes to two blocks where that leaves less of the last round idle:
-    // 512 x 65536 bf16 takes 7 rounds of half rows, 31.6 us, for 4 of whole ones, 35.0 (where both come out
-    // alike, one block: 300 x 65536 20.2 us, 21.7 in two).
-    if (blocks == 1 && nvec > room && nvec <= 2 * room) {
-        const int ones = (a.rows + sms - 1) / sms, twos = (a.rows + sms / 2 - 1) / (sms / 2);
-        if (10 * twos < 18 * ones) blocks = 2;
-    }
+    const DistillPlan plan = distill_plan(a.rows, nvec, sms, kBatch);
+    static_assert(kDsMaxCluster == 8, "distill_plan goes up to 8 blocks");
+    const int blocks = plan.blocks, nt = plan.threads;
     p.blocks_shift = blocks == 8 ? 3 : blocks == 4 ? 2 : blocks == 2 ? 1 : 0;
-    const int slice = std::max(1, (nvec + blocks - 1) / blocks);
-    const int nt = slice > 36 * 64 ? 512 : 256;
-    p.staged = std::min(slice, room);
-    const int batch = nt * kBatch;
-    p.chunk = ((p.staged + 3) / 4 + batch - 1) / batch * batch;
+    p.staged = plan.staged;
+    p.chunk = plan.chunk;
+    p.copies = plan.copies;
     const size_t smem = (size_t)kDsSlots * p.staged * 16;
     const void* kern = nt == 512 ? distill_variant<T, 512>(wide) : distill_variant<T, 256>(wide);
     const cudaError_t e = allow_smem(kern, smem);
