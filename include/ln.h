@@ -356,6 +356,11 @@ ln_status ln_logprobs_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tok
  *   dlogits    [rows, V], row r at dlogits + r * ldd (ldd >= V); written (columns V .. ldd of a
  *              row are left as they are); may be the logits themselves, with ldd = ld
  *
+ * The row's log-sum is fp32, exact to half a step of |lse|, and so is log q taken from it: below 512
+ * that is at most 2^-16.  A row of |lse| >= 512 (or of -inf, or +inf) has its sums formed again from the
+ * logits, as the forward forms them, and does not go by lse: exact for logits of any size, also for a
+ * row that is its type's lowest value throughout, whose softmax is uniform; it is read twice.
+ *
  * A row without a token has no gradient of logp.  A row whose upstream gradients are both 0
  * has gradient 0 whatever its logits hold (they are not used); a token of V or more gives a row
  * of NaN.  Conventions, limits and errors as for ln_logprobs_*; nothing is allocated.

@@ -524,8 +524,9 @@ def logprobs_bwd(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, s
                  dlogits=None, in_place: bool = False, stream=None):
     """Gradient of :func:`logprobs`: scale * (dlogp (onehot(token) - q) - dentropy q (log q +
     entropy)) with q = softmax(scale * logits).  lse and entropy (needed with dentropy): the
-    forward's; dlogp, dentropy: fp32 [rows], at least one of them.  Rows whose upstream gradients
-    are 0 get 0 whatever they hold.  Returns dlogits; ``in_place`` writes it over the logits."""
+    forward's (a row of |lse| >= 512, where fp32 has no room left for the row's log-sum, has its sums
+    formed again from the logits); dlogp, dentropy: fp32 [rows], at least one of them.  Rows whose
+    upstream gradients are 0 get 0 whatever they hold.  Returns dlogits; ``in_place`` writes it over the logits."""
     import torch
     rows, V, ld = _rows_of(logits, "logits")
     name, fn, raw_stream = _entry("ln_logprobs_bwd_", logits.dtype)

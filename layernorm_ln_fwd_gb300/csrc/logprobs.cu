@@ -433,9 +433,16 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
 // piece of a row (some batches a lane), reads it, and writes the gradient of the same
 // elements, which may be the logits' own place.  Bound by the read and the write: 4096 x 50257 bf16 with
 // the entropy's part takes 126 us, 6.5 TB/s, 0.98 of what a copy gets.
+//
+// L in fp32 gives log q = z - L to half a step of L.  From kFineLse on (half a step is 2^-15 there) log Z
+// gets lost in it -- altogether in a row masked throughout by its type's lowest value, where the
+// softmax is uniform but z - L is 0 -- and the row's sums are formed again, about a value r of the row
+// as in the forward: its first warp takes all of it, twice, and the others leave it (all rows so: 254 us,
+// 2000 x 50304 fp32 208 us for 119, one row of 131072 bf16 105 us for 2).
 // ---------------------------------------------------------------------------------------
 constexpr int kLbThreads = 256;
 constexpr int kLbBlocksPerSm = 4;
+constexpr float kFineLse = 512.f;
 
 struct LbParams {
     const void* x;
@@ -453,92 +460,29 @@ struct LbParams {
     long long ldd;
 };
 
-// WIDE: logits and gradient lie at the same place of a 16-byte vector in every row.
-template <typename T, bool ENT, bool WIDE>
-__global__ void __launch_bounds__(kLbThreads, kLbBlocksPerSm) logprobs_bwd_kernel(const LbParams p) {
-    using IO = Io<T>;
-    using PR = Pairs<T>;
-    constexpr int kVec = IO::kVec;
-    constexpr int H = PR::kPairs;
-    pdl_enter();
-    const int lane = (int)threadIdx.x & 31;
-    const long long piece = (long long)blockIdx.x * (kLbThreads / 32) + (threadIdx.x >> 5);
-    if (piece >= p.pieces) return;
-    const size_t row = (size_t)(piece / p.per_row);
-    const int part = (int)(piece % p.per_row);
-    const T* xr = static_cast<const T*>(p.x) + row * (size_t)p.ld;
-    T* dr = static_cast<T*>(p.dx) + row * (size_t)p.ldd;
-    const RowCut<T> cut(xr, p.V);
-    const int lo = (int)((long long)cut.nvec * part / p.per_row);
-    const int hi = (int)((long long)cut.nvec * (part + 1) / p.per_row);
-    const uint4* xv = reinterpret_cast<const uint4*>(xr + cut.head);
-    const bool has_loose = part == 0 && lane < cut.nloose();
-    float g = p.dlogp ? p.dlogp[row] : 0.f;
-    const float de = ENT ? p.dent[row] : 0.f;
-    const int t = p.dlogp ? p.tokens[row] : -1;
-    const float lse = p.lse[row], hh = ENT ? p.entropy[row] : 0.f;
-    if (t < 0) g = 0.f;
-    if (g == 0.f && de == 0.f) {  // nothing flows back: 0, whatever the row holds
-        if constexpr (WIDE) {
-            for (int v = lo + lane; v < hi; v += 32) st_stream(dr + cut.col(v), make_uint4(0, 0, 0, 0));
-        } else {
-            for (int j = cut.col(lo) + lane; j < cut.col(hi); j += 32) dr[j] = IO::from_f(0.f);
-        }
-        if (has_loose) dr[cut.loose(lane)] = IO::from_f(0.f);
-        return;
+// A warp's part of a row: vectors [lo, hi), and the loose elements where `loose`.
+template <typename T>
+struct LbPart {
+    const T* xr;
+    T* dr;
+    RowCut<T> cut;
+    int lo, hi;
+    bool loose;
+    __device__ __forceinline__ LbPart(const LbParams& p, size_t row, int part, int parts)
+        : xr(static_cast<const T*>(p.x) + row * (size_t)p.ld),
+          dr(static_cast<T*>(p.dx) + row * (size_t)p.ldd),
+          cut(xr, p.V) {
+        lo = (int)((long long)cut.nvec * part / parts);
+        hi = (int)((long long)cut.nvec * (part + 1) / parts);
+        loose = part == 0 && ((int)threadIdx.x & 31) < cut.nloose();
     }
-    if (t >= p.V) g = __int_as_float(0x7fc00000);
-    // With lq = log q: dx = q (a + b lq), a = -scale (dlogp + dH entropy), b = -scale dH, and at the
-    // token scale * dlogp more.
-    const float sg = p.scale * g, b = -p.scale * de;
-    const float ca = ENT ? fmaf(b, hh, -sg) : -sg;
-    auto grad = [&](float x, int col) {
-        const float lq = fmaf(x, p.scale, -lse);
-        const float q = ex2_fast(lq * kLog2e);
-        const float o = ENT ? q * fmaf(b, fmaxf(lq, -1e30f), ca) : q * ca;
-        return col == t ? o + sg : o;
-    };
-    const f2 s2 = f2_splat(p.scale), l2 = f2_splat(-lse), e2 = f2_splat(kLog2e), ca2 = f2_splat(ca), b2 = f2_splat(b);
-    auto deal = [&](const uint4 (&u)[kBatch], int v0) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int v = v0 + 32 * k;
-            if (v >= hi) break;
-            const int col = cut.col(v);
-            f2 o[H];
-            PR::unpack(u[k], o);
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                f2 lq = f2_fma(o[h], s2, l2);
-                const f2 y = f2_mul(lq, e2);
-                const f2 q = f2_make(ex2_fast(f2_lo(y)), ex2_fast(f2_hi(y)));
-                if constexpr (ENT) {  // 0 * -inf is no term
-                    lq = f2_make(fmaxf(f2_lo(lq), -1e30f), fmaxf(f2_hi(lq), -1e30f));
-                    o[h] = f2_mul(q, f2_fma(b2, lq, ca2));
-                } else {
-                    o[h] = f2_mul(q, ca2);
-                }
-            }
-            const int in = t - col;  // the token's place in this vector
-            if (in >= 0 && in < kVec) {
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-                    o[h] = f2_add(o[h], f2_make(in == 2 * h ? sg : 0.f, in == 2 * h + 1 ? sg : 0.f));
-            }
-            if constexpr (WIDE) {
-                st_stream(dr + col, PR::pack(o));
-            } else {
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    dr[col + 2 * h] = IO::from_f(f2_lo(o[h]));
-                    dr[col + 2 * h + 1] = IO::from_f(f2_hi(o[h]));
-                }
-            }
-        }
-    };
-    constexpr int kStep = 32 * kBatch;
-    int v0 = lo + lane;
-    if (v0 < hi) {
+    // A batch in flight while the one before is dealt with.
+    template <typename F>
+    __device__ __forceinline__ void each_batch(F deal) const {
+        constexpr int kStep = 32 * kBatch;
+        const uint4* xv = reinterpret_cast<const uint4*>(xr + cut.head);
+        int v0 = lo + ((int)threadIdx.x & 31);
+        if (v0 >= hi) return;
         uint4 u[kBatch], ahead[kBatch];
         load_batch<T>(u, xv, v0, 32, hi);
         while (true) {
@@ -550,10 +494,123 @@ __global__ void __launch_bounds__(kLbThreads, kLbBlocksPerSm) logprobs_bwd_kerne
             if ((v0 += kStep) >= hi) break;
         }
     }
-    if (has_loose) {
-        const int col = cut.loose(lane);
-        dr[col] = IO::from_f(grad(IO::to_f(xr[col]), col));
+};
+
+// With lq = log q: dx = q (a + b lq), a = -scale (dlogp + dH entropy), b = -scale dH, and at the token sg =
+// scale * dlogp more.
+struct LbFactors {
+    int t;
+    float sg, b, a;
+};
+
+// The gradient of a part, lq = z - l, or (x - r) scale - l (ABOUT r).
+template <typename T, bool ENT, bool WIDE, bool ABOUT>
+__device__ __forceinline__ void put_gradient(const LbPart<T>& g, float scale, const LbFactors& k, float l, float r) {
+    using IO = Io<T>;
+    using PR = Pairs<T>;
+    constexpr int kVec = IO::kVec;
+    constexpr int H = PR::kPairs;
+    const f2 s2 = f2_splat(scale), l2 = f2_splat(-l), e2 = f2_splat(kLog2e), a2 = f2_splat(k.a), b2 = f2_splat(k.b);
+    g.each_batch([&](const uint4 (&u)[kBatch], int v0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int v = v0 + 32 * i;
+            if (v >= g.hi) break;
+            const int col = g.cut.col(v);
+            f2 o[H];
+            if constexpr (ABOUT)
+                less<T>(u[i], r, o);
+            else
+                PR::unpack(u[i], o);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                f2 lq = f2_fma(o[h], s2, l2);
+                const f2 y = f2_mul(lq, e2);
+                const f2 q = f2_make(ex2_fast(f2_lo(y)), ex2_fast(f2_hi(y)));
+                if constexpr (ENT) {  // 0 * -inf is no term
+                    lq = f2_make(fmaxf(f2_lo(lq), -1e30f), fmaxf(f2_hi(lq), -1e30f));
+                    o[h] = f2_mul(q, f2_fma(b2, lq, a2));
+                } else {
+                    o[h] = f2_mul(q, a2);
+                }
+            }
+            const int in = k.t - col;  // the token's place in this vector
+            if (in >= 0 && in < kVec) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    o[h] = f2_add(o[h], f2_make(in == 2 * h ? k.sg : 0.f, in == 2 * h + 1 ? k.sg : 0.f));
+            }
+            if constexpr (WIDE) {
+                st_stream(g.dr + col, PR::pack(o));
+            } else {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    g.dr[col + 2 * h] = IO::from_f(f2_lo(o[h]));
+                    g.dr[col + 2 * h + 1] = IO::from_f(f2_hi(o[h]));
+                }
+            }
+        }
+    });
+    if (g.loose) {
+        const int col = g.cut.loose((int)threadIdx.x & 31);
+        const float x = IO::to_f(g.xr[col]);
+        const float lq = fmaf(ABOUT ? x - r : x, scale, -l);
+        const float q = ex2_fast(lq * kLog2e);
+        const float o = ENT ? q * fmaf(k.b, fmaxf(lq, -1e30f), k.a) : q * k.a;
+        g.dr[col] = IO::from_f(col == k.t ? o + k.sg : o);
     }
+}
+
+// A whole row, from its own sums.
+template <typename T, bool ENT, bool WIDE>
+static __device__ __noinline__ void put_row_from_sums(const LbParams& p, size_t row, const LbFactors k) {
+    const LbPart<T> g(p, row, 0, 1);
+    const float c = p.scale * kLog2e;
+    const f2 c2 = f2_splat(c);
+    RowSums<false> s;
+    s.clear();
+    g.each_batch([&](const uint4 (&u)[kBatch], int) {
+        if (s.see_batch<T>(u, c) > -INFINITY) s.add_batch<T>(u, c2);
+    });
+    if (g.loose) s.add_one(Io<T>::to_f(g.xr[g.cut.loose((int)threadIdx.x & 31)]), c);
+    const RowTotal a = warp_total({s.ref, f2_lo(s.z2) + f2_hi(s.z2), 0.f}, c);
+    put_gradient<T, ENT, WIDE, true>(g, p.scale, k, logf(a.z), a.ref == -INFINITY ? 0.f : a.ref);
+}
+
+// WIDE: logits and gradient lie at the same place of a 16-byte vector in every row.
+template <typename T, bool ENT, bool WIDE>
+__global__ void __launch_bounds__(kLbThreads, kLbBlocksPerSm)
+    logprobs_bwd_kernel(const __grid_constant__ LbParams p) {
+    using IO = Io<T>;
+    pdl_enter();
+    const int lane = (int)threadIdx.x & 31;
+    const long long piece = (long long)blockIdx.x * (kLbThreads / 32) + (threadIdx.x >> 5);
+    if (piece >= p.pieces) return;
+    const size_t row = (size_t)(piece / p.per_row);
+    const int part = (int)(piece % p.per_row);
+    const LbPart<T> g(p, row, part, p.per_row);
+    float dl = p.dlogp ? p.dlogp[row] : 0.f;
+    const float de = ENT ? p.dent[row] : 0.f;
+    const int t = p.dlogp ? p.tokens[row] : -1;
+    const float lse = p.lse[row], hh = ENT ? p.entropy[row] : 0.f;
+    if (t < 0) dl = 0.f;
+    if (dl == 0.f && de == 0.f) {  // nothing flows back: 0, whatever the row holds
+        if constexpr (WIDE) {
+            for (int v = g.lo + lane; v < g.hi; v += 32) st_stream(g.dr + g.cut.col(v), make_uint4(0, 0, 0, 0));
+        } else {
+            for (int j = g.cut.col(g.lo) + lane; j < g.cut.col(g.hi); j += 32) g.dr[j] = IO::from_f(0.f);
+        }
+        if (g.loose) g.dr[g.cut.loose(lane)] = IO::from_f(0.f);
+        return;
+    }
+    if (t >= p.V) dl = __int_as_float(0x7fc00000);
+    const float sg = p.scale * dl, b = -p.scale * de;
+    const LbFactors k{t, sg, b, ENT ? fmaf(b, hh, -sg) : -sg};
+    if (fabsf(lse) >= kFineLse) {
+        if (part == 0) put_row_from_sums<T, ENT, WIDE>(p, row, k);
+        return;
+    }
+    put_gradient<T, ENT, WIDE, false>(g, p.scale, k, lse, 0.f);
 }
 
 template <typename T>

@@ -174,13 +174,16 @@ def logprobs(x, tokens=None, scale: float = 1.0, top: int = 0):
 def logprobs_bwd(x, tokens, lse, entropy=None, dlogp=None, dentropy=None, scale: float = 1.0,
                  io: str = "f64"):
     """Gradient of logp and entropy with respect to the logits, from the forward's lse and
-    entropy (the stated definition of ``ln_logprobs_bwd_*``)."""
+    entropy (the stated definition of ``ln_logprobs_bwd_*``).  The forward's lse is fp32: a row of
+    |lse| >= 512 goes by the log-sum of its own logits (one of -3.4e38 throughout would have q = 1 in
+    every column by its lse, which has lost log V)."""
     x = np.asarray(x, dtype=np.float64)
     rows, V = x.shape
     r = np.arange(rows)
     zero = np.zeros(rows)
     with np.errstate(all="ignore"):
-        logq = scale * x - np.asarray(lse, dtype=np.float64)[:, None]
+        lse = np.asarray(lse, dtype=np.float64)[:, None]
+        logq = np.where(np.abs(lse) >= 512, _log_softmax(x, scale)[0], scale * x - lse)
         q = np.exp(logq)
         g = np.zeros((rows, V))
         t = np.full(rows, -1) if tokens is None else np.asarray(tokens)

@@ -1,0 +1,128 @@
+"""Forms of the token log probabilities' calls beside those of test_logprobs_gpu.py: the gradient of rows of
+large logits, against the softmax in 64 bits and not by the forward's log-sum.  Tolerances: vocabref.py, and
+at each test."""
+import numpy as np
+import pytest
+import torch
+
+import layernorm_ln_fwd_gb300 as ln
+import vocabref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def true_gradient(x64, tokens, dl, de, scale):
+    """From the logits alone: log q = z - max z - log Z."""
+    z = scale * x64
+    d = z - z.max(axis=1, keepdims=True)
+    logq = d - np.log(np.exp(d).sum(axis=1, keepdims=True))
+    q = np.exp(logq)
+    logq = np.where(q > 0, logq, 0.0)
+    H = -(q * logq).sum(axis=1, keepdims=True)
+    g = -dl[:, None] * q - de[:, None] * q * (logq + H)
+    g[np.arange(len(q)), tokens] += dl
+    return scale * g, q, logq, H
+
+
+def check_true_gradient(x, tokens, dl, de, scale, dtype, **kw):
+    """log q errs by 3 u |log q| of the products, E of the sums (the row's own, or the forward's, which is
+    then rounded to fp32: half a step of |lse| < 512, 2^-16, and 4 u of its last steps), and the weight by 8 u;
+    the entropy by E (2 + A) + 6 u B (vocabref.py); the store rounds."""
+    x64 = R.to64(x)
+    _, ent, lse, _, _, _ = ln.logprobs(x, tokens, scale)
+    got = ln.logprobs_bwd(x, tokens, lse, ent, dl, de, scale, **kw)
+    torch.cuda.synchronize()
+    scale = R.f32(scale)
+    dl, de = R.to64(dl), R.to64(de)
+    want, q, logq, H = true_gradient(x64, tokens.cpu().numpy(), dl, de, scale)
+    _, d, _, A, B, E = R.row_stats(x64, scale)
+    coarse = np.abs(R.to64(lse))
+    E, A, B = E[:, None], A[:, None], B[:, None]
+    with np.errstate(all="ignore"):
+        half = np.where(coarse < 512, np.exp2(np.floor(np.log2(np.maximum(coarse, 1)))) * R.U, 0.0)[:, None]
+    eq = q * (R.U * (3 * (np.abs(logq) + 6) + 12) + E + half) + 2.0 ** -125
+    hit = np.zeros_like(q)
+    hit[np.arange(len(q)), tokens.cpu().numpy()] = 1
+    size = np.abs(logq) + H
+    eH = E * (2 + A) + 6 * R.U * B + 4 * R.U * H
+    err = np.abs(dl)[:, None] * (eq + 4 * R.U * (q + hit))
+    err += np.abs(de)[:, None] * (eq * (size + 1) + q * (4 * R.U * size + eH))
+    err *= scale
+    R.close("gradient", R.to64(got), want, err + R.HALF[dtype] * (np.abs(want) + err) + 2.0 ** -133)
+    return got, want
+
+
+def upstream(rows, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(rows, generator=g).cuda(), torch.randn(rows, generator=g).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 5, 130, 1000, 1001, 50257])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_gradient_of_rows_of_the_lowest_value(dtype, V, scale):
+    """Every word masked by the type's lowest value: uniform, by definition and by the forward."""
+    rows = 5
+    x = torch.full((rows, V), torch.finfo(R.TYPES[dtype]).min, dtype=R.TYPES[dtype], device="cuda")
+    x[1] = R.logits(1, V, dtype, V)  # next to a row of ordinary logits
+    t = torch.tensor([0, V - 1, V // 2, V // 3, 0], dtype=torch.int32).cuda()
+    got, want = check_true_gradient(x, t, *upstream(rows, V), scale, dtype)
+    dl = torch.ones(rows, device="cuda")
+    _, ent, lse, _, _, _ = ln.logprobs(x, t, scale)
+    one = ln.logprobs_bwd(x, t, lse, dlogp=dl, scale=scale).double()
+    torch.cuda.synchronize()
+    for r in (0, 2, 3, 4):
+        uniform = torch.full((V,), -scale / V, dtype=torch.float64, device="cuda")
+        uniform[t[r].item()] += scale
+        assert ((one[r] - uniform).abs() <= R.HALF[dtype] * uniform.abs() + 2.0 ** -12 / V + 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift", [-1e30, -3e4, -600.0, -500.0, 300.0, 511.0, 1e4, 1e6])
+@pytest.mark.parametrize("V", [33, 4001, 50304])
+def test_gradient_of_shifted_rows(dtype, shift, V):
+    rows = 6
+    x = (R.logits(rows, V, "f32", V) + shift).to(R.TYPES[dtype])
+    x[2] = R.logits(1, V, dtype, 1)[0]
+    g = torch.Generator().manual_seed(V)
+    t = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).cuda()
+    dl, de = upstream(rows, V)
+    dl[3], de[3] = 0.0, 0.0  # nothing flows back
+    check_true_gradient(x, t, dl, de, 0.9, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_of_large_logits_in_place_and_elsewhere(dtype):
+    rows, V, ld = 40, 5003, 5009
+    x = R.logits(rows, V, dtype, 3, ld=ld)
+    x[::3] = x[::3] * 500
+    x[1] = -float("inf")
+    x[1, 7] = -2000.0
+    g = torch.Generator().manual_seed(1)
+    t = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).cuda()
+    t[1] = 7
+    dl, de = upstream(rows, 5)
+    _, ent, lse, _, _, _ = ln.logprobs(x, t)
+    a, _ = check_true_gradient(x, t, dl, de, 1.0, dtype)
+    buf = torch.full((rows * 5011 + 1,), 7.0, dtype=x.dtype, device="cuda")
+    out = buf[1:].view(rows, 5011)[:, :V]
+    b = ln.logprobs_bwd(x, t, lse, ent, dl, de, dlogits=out)
+    full = torch.full((rows, ld), 7.0, dtype=x.dtype, device="cuda")
+    full[:, :V] = x
+    c = ln.logprobs_bwd(full[:, :V], t, lse, ent, dl, de, in_place=True)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, c)
+    assert (buf[1:].view(rows, 5011)[:, V:] == 7).all() and (full[:, V:] == 7).all() and buf[0] == 7
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_where_the_log_sum_overflows(dtype):
+    """scale * logits past fp32: lse is +-inf, the distribution is not lost."""
+    x = torch.tensor([[3e38, 3e38, 1.0], [-3e38, -3e38, -3e38], [3e38, 0.0, -3e38]]).to(R.TYPES[dtype]).cuda()
+    t = torch.tensor([0, 2, 1], dtype=torch.int32).cuda()
+    logp, ent, lse, _, _, _ = ln.logprobs(x, t, 2.0)
+    g = ln.logprobs_bwd(x, t, lse, ent, torch.ones(3).cuda(), torch.ones(3).cuda(), 2.0)
+    torch.cuda.synchronize()
+    assert torch.isinf(lse[:2]).all()
+    want = torch.tensor([[1.0, -1.0, 0.0], [-2 / 3, -2 / 3, 4 / 3], [-2.0, 2.0, 0.0]], device="cuda")
+    assert (g.float() - want).abs().max() <= 2 * R.HALF[dtype] * 2 + 1e-5
