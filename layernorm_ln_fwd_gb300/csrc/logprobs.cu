@@ -443,6 +443,9 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
 constexpr int kLbThreads = 256;
 constexpr int kLbBlocksPerSm = 4;
 constexpr float kFineLse = 512.f;
+// 0 * -inf is no term: log q is held where q is 0 in fp32 all the same, and no lower, or its product with a
+// large upstream gradient would be infinite itself.
+constexpr float kHeldLog = -128.f;
 
 struct LbParams {
     const void* x;
@@ -527,8 +530,8 @@ __device__ __forceinline__ void put_gradient(const LbPart<T>& g, float scale, co
                 f2 lq = f2_fma(o[h], s2, l2);
                 const f2 y = f2_mul(lq, e2);
                 const f2 q = f2_make(ex2_fast(f2_lo(y)), ex2_fast(f2_hi(y)));
-                if constexpr (ENT) {  // 0 * -inf is no term
-                    lq = f2_make(fmaxf(f2_lo(lq), -1e30f), fmaxf(f2_hi(lq), -1e30f));
+                if constexpr (ENT) {
+                    lq = f2_make(fmaxf(f2_lo(lq), kHeldLog), fmaxf(f2_hi(lq), kHeldLog));
                     o[h] = f2_mul(q, f2_fma(b2, lq, a2));
                 } else {
                     o[h] = f2_mul(q, a2);
@@ -556,7 +559,7 @@ __device__ __forceinline__ void put_gradient(const LbPart<T>& g, float scale, co
         const float x = IO::to_f(g.xr[col]);
         const float lq = fmaf(ABOUT ? x - r : x, scale, -l);
         const float q = ex2_fast(lq * kLog2e);
-        const float o = ENT ? q * fmaf(k.b, fmaxf(lq, -1e30f), k.a) : q * k.a;
+        const float o = ENT ? q * fmaf(k.b, fmaxf(lq, kHeldLog), k.a) : q * k.a;
         g.dr[col] = IO::from_f(col == k.t ? o + k.sg : o);
     }
 }

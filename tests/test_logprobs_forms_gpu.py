@@ -1,5 +1,5 @@
 """Forms of the token log probabilities' calls beside those of test_logprobs_gpu.py: the gradient of rows of
-large logits, against the softmax in 64 bits and not by the forward's log-sum.  Tolerances: vocabref.py, and
+large logits and of masked words, against the softmax in 64 bits and not by the forward's log-sum.  Tolerances: vocabref.py, and
 at each test."""
 import numpy as np
 import pytest
@@ -126,3 +126,19 @@ def test_gradient_where_the_log_sum_overflows(dtype):
     assert torch.isinf(lse[:2]).all()
     want = torch.tensor([[1.0, -1.0, 0.0], [-2 / 3, -2 / 3, 4 / 3], [-2.0, 2.0, 0.0]], device="cuda")
     assert (g.float() - want).abs().max() <= 2 * R.HALF[dtype] * 2 + 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [9, 1000, 40003])
+@pytest.mark.parametrize("size", [1e3, 1e10, 1e30])
+def test_gradient_of_masked_words_with_large_upstream_gradients(dtype, V, size):
+    """A word without probability has no gradient, however large the entropy's (a scaled loss, say)."""
+    rows = 6
+    x = R.logits(rows, V, dtype, V)
+    x[1:3, ::2] = -float("inf")
+    x[3:5, 1::3] = torch.finfo(x.dtype).min
+    x[5, : V - 1] = -float("inf")
+    t = torch.tensor([0, 1, 3, 0, 3, V - 1], dtype=torch.int32).cuda()
+    dl, de = upstream(rows, V)
+    got, want = check_true_gradient(x, t, dl, de * size, 1.0, dtype)
+    assert torch.isfinite(got).all() and (got[torch.isinf(x)] == 0).all()
