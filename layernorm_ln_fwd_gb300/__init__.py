@@ -402,8 +402,10 @@ def _rows_of(t, name):
 
 
 def _gradient_of(logits, ld, dlogits, in_place):
-    """(tensor, ld) of the gradient: the logits, the caller's, or a new one whose rows are as far
-    apart as those of the logits (so a padded vocabulary's gradient has the padding too)."""
+    """(tensor, ld) of the gradient: the logits, the caller's, or a new one.  Its rows are as far apart
+    as those of the logits where that is a padded vocabulary (by up to an eighth, or 64 words), so
+    that the gradient has the padding too; those of a view that leaves out more (the last position of
+    every sequence, some columns of a wide buffer) start at the same place of 16 bytes, no further apart."""
     import torch
     if in_place:
         if dlogits is not None and dlogits is not logits:
@@ -413,6 +415,8 @@ def _gradient_of(logits, ld, dlogits, in_place):
         if logits.is_contiguous():
             return torch.empty_like(logits), ld
         rows, V = logits.shape
+        if ld - V > max(V // 8, 64):
+            ld = V + (ld - V) % (16 // logits.element_size())
         return torch.empty((rows, ld), dtype=logits.dtype, device=logits.device)[:, :V], ld
     if dlogits.device != logits.device:
         raise ValueError(f"dlogits is on {dlogits.device}, expected {logits.device}")

@@ -1,6 +1,6 @@
 """Forms of the token log probabilities' calls beside those of test_logprobs_gpu.py: the gradient of rows of
-large logits and of masked words, against the softmax in 64 bits and not by the forward's log-sum.  Tolerances: vocabref.py, and
-at each test."""
+large logits and of masked words, against the softmax in 64 bits and not by the forward's log-sum, and of
+views.  Tolerances: vocabref.py, and at each test."""
 import numpy as np
 import pytest
 import torch
@@ -142,3 +142,28 @@ def test_gradient_of_masked_words_with_large_upstream_gradients(dtype, V, size):
     dl, de = upstream(rows, V)
     got, want = check_true_gradient(x, t, dl, de * size, 1.0, dtype)
     assert torch.isfinite(got).all() and (got[torch.isinf(x)] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("view", ["last position", "every second row", "some columns", "padding"])
+def test_gradient_of_a_view_is_no_larger_than_its_rows(dtype, view):
+    V = 1003
+    wide = R.logits(6 * 40, 1024, dtype, 2).view(6, 40, 1024)
+    x = {"last position": wide[:, -1], "every second row": wide[0, ::2, :V], "some columns": wide[0, :, 5:105],
+         "padding": wide[0, :, :V]}[view]
+    rows, V = x.shape
+    t = torch.arange(rows, dtype=torch.int32, device="cuda")
+    dl = torch.randn(rows, generator=torch.Generator().manual_seed(1)).cuda()
+    lse = ln.logprobs(x, t)[2]
+    g = ln.logprobs_bwd(x, t, lse, dlogp=dl)
+    losses, d = ln.distill(x, t[:, None], dl[:, None].contiguous())
+    packed = x.contiguous()
+    g2 = ln.logprobs_bwd(packed, t, lse, dlogp=dl)
+    l2, d2 = ln.distill(packed, t[:, None], dl[:, None].contiguous())
+    torch.cuda.synchronize()
+    for a, b in ((g, g2), (d, d2)):
+        assert a.shape == x.shape and a.untyped_storage().nbytes() <= rows * (V + max(V // 8, 64)) * x.element_size()
+        assert (a.stride(0) - x.stride(0)) * x.element_size() % 16 == 0
+        # sums in another order may round to the neighbouring value
+        assert ((a.double() - b.double()).abs() <= 2.01 * R.HALF[dtype] * b.double().abs() + 1e-5).all()
+    assert (g.stride(0) == x.stride(0)) == (view == "padding") and (losses - l2).abs().max() <= 1e-5
