@@ -327,9 +327,10 @@ ln_status ln_xent_bf16(const ln_bf16* logits, const int32_t* targets, int64_t ro
  * At least one output must be given.  A logit of -inf has probability 0 and adds nothing to the
  * entropy.  A row that holds NaN or +inf has no distribution, nor has one whose logits are all
  * -inf: its logp and entropy are NaN (lse is -inf for the latter); its alternatives' ids are as for
- * any row.  Outputs must not overlap the inputs.  Limits: 1 <= V <= LN_XENT_MAX_V, 0 <= rows <= LN_MAX_ROWS.  Other conventions and
- * errors as for ln_fwd_*; nothing is allocated, and results are bitwise repeatable for the same
- * sizes and addresses (modulo 16).
+ * any row.  Outputs must not overlap the inputs.  Limits: 1 <= V <= LN_XENT_MAX_V, 0 <= rows <=
+ * LN_MAX_ROWS.  Other conventions and errors as for ln_fwd_*; nothing is allocated.  Results are
+ * bitwise repeatable for the same sizes (ld and top among them) and the same address of the logits
+ * modulo 32, on devices of as many SMs: rows are cut at 32 bytes, and split by the number of rows.
  */
 #define LN_MAX_TOP 256
 
@@ -363,7 +364,8 @@ ln_status ln_logprobs_bf16(const ln_bf16* logits, int64_t ld, const int32_t* tok
  *
  * A row without a token has no gradient of logp.  A row whose upstream gradients are both 0
  * has gradient 0 whatever its logits hold (they are not used); a token of V or more gives a row
- * of NaN.  Conventions, limits and errors as for ln_logprobs_*; nothing is allocated.
+ * of NaN.  Conventions, limits and errors as for ln_logprobs_*; nothing is allocated, and results are
+ * bitwise repeatable for the same sizes and addresses modulo 16.
  */
 ln_status ln_logprobs_bwd_f32(const float* logits, int64_t ld, const int32_t* tokens,
                               const float* lse, const float* entropy, const float* dlogp,
@@ -402,8 +404,9 @@ ln_status ln_logprobs_bwd_bf16(const ln_bf16* logits, int64_t ld, const int32_t*
  * of -inf only), or of weight 0, has loss 0 and gradient 0 whatever its logits hold (they are not
  * used, and those of a row of weight 0 not read).  An entry of weight p_k = 0 adds nothing, even where the student has -inf; elsewhere a
  * student's -inf gives an infinite loss.  Limits: 1 <= K <= LN_MAX_TOP, 1 <= V <= LN_XENT_MAX_V,
- * 0 <= rows <= LN_MAX_ROWS.  Other conventions and errors as for ln_fwd_*; nothing is allocated,
- * and results are bitwise repeatable.
+ * 0 <= rows <= LN_MAX_ROWS.  Other conventions and errors as for ln_fwd_*; nothing is allocated.
+ * Results are bitwise repeatable for the same sizes (ld among them) and the same address of the logits
+ * modulo 16, on devices of as many SMs: rows are cut at 16 bytes, and split by the number of rows.
  */
 ln_status ln_distill_f32(const float* logits, int64_t ld, const int32_t* ids, const float* teacher,
                          const float* weights, int64_t rows, int64_t V, int64_t K, float scale,

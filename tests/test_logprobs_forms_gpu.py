@@ -167,3 +167,35 @@ def test_gradient_of_a_view_is_no_larger_than_its_rows(dtype, view):
         # sums in another order may round to the neighbouring value
         assert ((a.double() - b.double()).abs() <= 2.01 * R.HALF[dtype] * b.double().abs() + 1e-5).all()
     assert (g.stride(0) == x.stride(0)) == (view == "padding") and (losses - l2).abs().max() <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V,ld", [(5, 1003, 1003), (300, 20001, 20003), (3, 131072, 131072), (2, 70001, 70001)])
+def test_repeatable_where_the_header_says_so(dtype, rows, V, ld):
+    """Copies of the logits at addresses that are equal modulo 32 (logprobs) and modulo 16 (its gradient, distill)."""
+    size = R.TYPES[dtype].itemsize
+    x = R.logits(rows, V, dtype, V, ld=ld)
+    t = torch.randint(0, V, (rows,), generator=torch.Generator().manual_seed(V), dtype=torch.int32).cuda()
+    ids = ((t[:, None] + torch.arange(7, device="cuda") * 3) % V).to(torch.int32)
+    teacher = torch.randn(rows, 7, generator=torch.Generator().manual_seed(3)).cuda()
+    dl = torch.randn(rows, generator=torch.Generator().manual_seed(4)).cuda()
+
+    def copy(offset_bytes):
+        flat = torch.empty(offset_bytes // size + rows * ld, dtype=x.dtype, device="cuda")
+        assert flat.data_ptr() % 256 == 0
+        c = flat[offset_bytes // size:].view(rows, ld)[:, :V]
+        return c.copy_(x)
+
+    def all_of(a, b):
+        torch.cuda.synchronize()
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+    for at in (0, 4, 24):
+        p, q = copy(at), copy(at + 96)
+        all_of(ln.logprobs(p, t, 0.8, 9, True, True), ln.logprobs(q, t, 0.8, 9, True, True))
+        q = copy(at + 48)
+        for k in (1.0, 3e4):  # the forward's log-sum, and one beyond 512
+            lse = torch.full((rows,), 12.0, device="cuda") * k
+            all_of([ln.logprobs_bwd(p, t, lse, dlogp=dl)], [ln.logprobs_bwd(q, t, lse, dlogp=dl)])
+        all_of(ln.distill(p, ids, teacher), ln.distill(q, ids, teacher))
