@@ -199,3 +199,48 @@ def test_repeatable_where_the_header_says_so(dtype, rows, V, ld):
             lse = torch.full((rows,), 12.0, device="cuda") * k
             all_of([ln.logprobs_bwd(p, t, lse, dlogp=dl)], [ln.logprobs_bwd(q, t, lse, dlogp=dl)])
         all_of(ln.distill(p, ids, teacher), ln.distill(q, ids, teacher))
+
+
+def segments(rows, V, top):
+    """The segment of every column of an aligned fp32 row, whose largest values the selection of the top begins
+    with: launch_logprobs_t's cut of a row into slices, threads, pairs of vectors and batches, restated."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    nvec, blocks = V // 4, 1
+    while blocks < 8 and rows * blocks * 2 <= 2 * sms and nvec // (blocks * 2) >= 2048:
+        blocks *= 2
+    piece = (-(-nvec // blocks) + 1) & ~1
+    few = rows <= 8 * sms
+    nt = 128 if few else 32
+    while nt < (256 if few else 128) and nt * 4 < piece:
+        nt *= 2
+    per = max(1, -(-piece // (nt * 4)))
+    seglen = 1
+    while per * nt > seglen * min(max(32 * top, 512), 2048):
+        seglen *= 2
+    v = torch.arange(V) // 4
+    rank, i = v // piece, v % piece
+    tid, batch = i % (2 * nt) // 2, i // (4 * nt)
+    return rank * (per * nt) + (batch // seglen) * nt + tid
+
+
+@pytest.mark.parametrize("V", [4096, 50304, 131072, 262144, 1 << 21])
+@pytest.mark.parametrize("order", ["random", "rising", "falling"])
+@pytest.mark.parametrize("top", [1, 20, 256])
+@pytest.mark.parametrize("rows", [1, 400])
+def test_rows_of_levels_of_whole_segments(V, order, top, rows):
+    """Every value of a segment above all those of a lower one: few segments hold very many large values, and
+    all of them are candidates of the top."""
+    rows = min(rows, (1 << 28) // V)
+    g = torch.Generator().manual_seed(V + top)
+    seg = segments(rows, V, top)
+    count = int(seg.max()) + 1
+    level = {"random": torch.randperm(count, generator=g), "rising": torch.arange(count),
+             "falling": torch.arange(count).flip(0)}[order]
+    x = (level[seg] + 0.5 * torch.rand(V, generator=g)) * (20.0 / count)
+    x = x.repeat(rows, 1).cuda()
+    x[rows // 2] = x[0].flip(0)
+    t = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).cuda()
+    out = ln.logprobs(x, t, 1.0, top, True, True)
+    torch.cuda.synchronize()
+    some = sorted({0, rows // 2, rows - 1})
+    R.check_logprobs(tuple(o[some] for o in out), R.to64(x[some]), t[some], 1.0, top)
