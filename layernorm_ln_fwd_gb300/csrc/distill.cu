@@ -146,7 +146,9 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         }
         return mbar_wait(&sh.met[meetings & 1u], meetings >> 1 & 1u, p.limit_ns);
     };
-    bool dead = false;  // a copy did not arrive in time: what follows is void, and waits no more
+    // A wait ran out somewhere in the block: what has been written is void, and the block ends with this
+    // row -- going on, it would send the other blocks of its cluster sums that they do not wait for yet.
+    bool dead = false;
 
     // The mbarriers and the first list are there, in all blocks of the cluster.
     auto begin = [&]() {
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                 if (blocks > 1 && lane == 0)
                     mbar_arrive_expect_tx(&sh.met[turn], (unsigned)blocks * kWarps * 8u +
                                                              16u * (rank == 0 ? (unsigned)blocks : 1u));
-                if (!dead || blocks == 1) gone = !meet();
+                gone = !meet();
                 ++meetings;
                 a = all_total(sh.total[turn], blocks * kWarps, p.c);
                 r = a.ref == -INFINITY ? 0.f : a.ref;
@@ -223,8 +225,9 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
             } else if (rank == 0 && lane == 0 && p.losses) {
                 p.losses[row] = 0.f;
             }
-            dead |= __syncthreads_or(gone);  // the slice is written, its slot free, the next list ready
-            if (lane == 0 && w2 != 0.f && !dead) issue(row + 2 * stride, slot);
+            dead = __syncthreads_or(gone);  // the slice is written, its slot free, the next list ready
+            if (dead) break;
+            if (lane == 0 && w2 != 0.f) issue(row + 2 * stride, slot);
             if (learn && p.dx) {
                 const DsSlice<T> g(p, row, rank);
                 T* dr = static_cast<T*>(p.dx) + (size_t)row * (size_t)p.ldd;
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                 load_list(row + 2 * stride);
             }
             if (learn && blocks == 1) meet();
-            dead |= __syncthreads_or(0);
+            if (__syncthreads_or(0)) break;
         }
         end_together();
         return;
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
             if (q.w != 0.f) {
                 const DsSlice<T> g(p, row, rank);
                 const T* xs = reinterpret_cast<const T*>(smem_raw + 16 * (size_t)(slot * p.staged));
-                for (int i = 0, v = g.lo; v < g.mid && !dead; ++i, v += p.chunk)
+                for (int i = 0, v = g.lo; v < g.mid; ++i, v += p.chunk)
                     gone |= !mbar_wait(&sh.full[slot][i], phases.parity(slot), p.limit_ns);
                 phases.used(slot);
                 if (q.learn) {
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
                     ++meetings;
                 }
             }
-            dead |= __syncthreads_or(gone);
+            if (__syncthreads_or(gone)) break;
         }
         end_together();
         return;
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
         if (q.w != 0.f) {
             // Pass 1: the slice's sums.
             for (int i = 0, from = 0; from < end; ++i, from += p.chunk) {
-                if (!dead) gone |= !mbar_wait(&sh.full[slot][i], phases.parity(slot), p.limit_ns);
+                gone |= !mbar_wait(&sh.full[slot][i], phases.parity(slot), p.limit_ns);
                 if (!learn) continue;
                 const int to = min(end, from + p.chunk);
                 for (int v0 = from + tid; v0 < to; v0 += kStep) {
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
             } else if (lane == 0) {
                 *mine = make_float2(a.ref, a.z);
             }
-            if (!dead || blocks == 1) gone |= !meet();
+            gone |= !meet();
             ++meetings;
             a = all_total(sh.total[turn], blocks * kWarps, p.c);
             if (dr) {
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(NT + 96, NT == 512 ? 1 : 2) distill_kernel(con
             }
             if (has_loose) dr[g.cut.loose(tid)] = IO::from_f(0.f);
         }
-        dead |= __syncthreads_or(gone);
+        if (__syncthreads_or(gone)) break;
     }
     end_together();
 }
