@@ -126,7 +126,7 @@ static __device__ __noinline__ E select_threshold(const E* list, int n, int k, i
                 sh->done = shift == 0 || sh->above + cum <= k + slack;
                 sh->above += cum - here;
                 sh->lo = nlo;
-                sh->hi = min(hi, (E)(nlo + (((E)1 << shift) - 1)));
+                sh->hi = nlo + min((E)(hi - nlo), (E)(((E)1 << shift) - 1));  // (the bin may end past the type's range)
             }
         }
         __syncthreads();

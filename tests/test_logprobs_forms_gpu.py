@@ -244,3 +244,21 @@ def test_rows_of_levels_of_whole_segments(V, order, top, rows):
     torch.cuda.synchronize()
     some = sorted({0, rows // 2, rows - 1})
     R.check_logprobs(tuple(o[some] for o in out), R.to64(x[some]), t[some], 1.0, top)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,infs", [(900, 3), (5000, 2000), (50257, 700), (50257, 40000), (131072, 130000)])
+@pytest.mark.parametrize("top", [1, 20, 256])
+def test_top_of_rows_from_the_lowest_value_to_infinity(dtype, V, infs, top):
+    """Values over the type's whole range, most of the large ones equal: the lowest columns of +inf first."""
+    g = torch.Generator().manual_seed(V + infs)
+    x = torch.full((3, V), torch.finfo(R.TYPES[dtype]).min, dtype=R.TYPES[dtype])
+    x[1] = torch.randn(V, generator=g).to(x.dtype)
+    x[2, ::2] = torch.finfo(R.TYPES[dtype]).max
+    for r in range(3):
+        x[r, torch.randperm(V, generator=g)[:infs]] = float("inf")
+    out = ln.logprobs(x.cuda(), top=top)
+    torch.cuda.synchronize()
+    want = x.float().sort(dim=1, descending=True, stable=True).indices[:, :top]
+    np.testing.assert_array_equal(out[4].cpu().numpy(), want.numpy())
+    assert torch.isnan(out[1]).all() and not torch.isfinite(out[2]).any()
