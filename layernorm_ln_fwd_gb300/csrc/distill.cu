@@ -114,10 +114,10 @@ __device__ __forceinline__ RowTotal all_total(const float2* total, int n, float 
 // (As part of the other threads' work it made a row of 50304 take 6.7 us instead of 5.2.)
 //
 // Bound by the read and the write where a slice is kept whole and is not short: 8192 x 50304 bf16 with 64
-// entries takes 276 us, 6.0 TB/s, 0.90 of what a copy gets (348 us with 256 entries: the list's warps set
+// entries takes 273 us, 6.0 TB/s, 0.90 of what a copy gets (351 us with 256 entries: the list's warps set
 // the pace).  A row's chain of meetings takes about 3 us whatever its length, which shows for rows of
 // 32 KB (4000 x 16384: 54 us, 0.73).  Rows that do not fit are read again through L2, which also holds the
-// gradient that is being written: 1024 x 131072 takes 112 us (0.72), split over clusters of four to keep
+// gradient that is being written: 1024 x 131072 takes 111 us (0.72), split over clusters of four to keep
 // all of it 112 us too, and over eight 230.
 //
 // WIDE: logits and gradient lie at the same place of a 16-byte vector in every row.

@@ -386,7 +386,7 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     const int most = logprobs_threads(a.rows, sms);
     // A batch for every thread, if there are that many.  The selection of a top is work for 4 warps
     // (1000 x 1024, top 20: 8.3 us), but for one where rows abound: more of them run at once (8192 x 1000,
-    // top 20: 36 us, 44 with two warps, 61 with four).
+    // top 20: 32 us, 39 with two warps, 54 with four).
     const int least = a.top > 0 && a.rows <= 8 * sms ? 7 : 5;  // log2
     int nt = 1 << least;
     p.nt_shift = least;
@@ -407,7 +407,7 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
     }
     p.nseg = (per + seglen - 1) / seglen * nt;
     // Short rows have few batches: a segment for every vector, or all of the row would be candidates
-    // (8192 x 256 with the top 10, four warps: 53 us, 63 with a segment for each batch).
+    // (8192 x 256 with the top 10, four warps: 53 us, 63 with a segment for each batch; with one warp 27).
     if (per == 1) {
         p.seg_shift = 0;
         p.nseg = kBatch * nt;
@@ -438,7 +438,7 @@ cudaError_t launch_logprobs_t(const LogprobsArgs& a, cudaStream_t stream) {
 // gets lost in it -- altogether in a row masked throughout by its type's lowest value, where the
 // softmax is uniform but z - L is 0 -- and the row's sums are formed again, about a value r of the row
 // as in the forward: its first warp takes all of it, twice, and the others leave it (all rows so: 254 us,
-// 2000 x 50304 fp32 208 us for 119, one row of 131072 bf16 105 us for 2).
+// 2000 x 50304 fp32 209 us for 119, one row of 131072 bf16 105 us for 2).
 // ---------------------------------------------------------------------------------------
 constexpr int kLbThreads = 256;
 constexpr int kLbBlocksPerSm = 4;
