@@ -3,7 +3,9 @@
  * with the bias + dropout + residual prologue (ln_fwd_bias_dropout_*, ln_dropout_bwd_*), the
  * fused residual-add + RMSNorm (ln_rms_*), the fused row softmax (ln_softmax_*), the fused
  * cross-entropy (ln_xent_*) and the operators over rows of logits -- token log probabilities with
- * their gradient (ln_logprobs_*) and distillation from a teacher's top logits (ln_distill_*) --
+ * their gradient (ln_logprobs_*) and distillation from a teacher's top logits (ln_distill_*) --,
+ * the softmax with a learned relative position bias (ln_softmax_rel_*) and 8-bit checkpoints of
+ * activations with the backwards that read them (ln_ckpt8_*, ln_bwd_ckpt8_*, ln_rms_bwd_ckpt8_*)
  * alongside.
  *
  * The library computes, for a row-major [rows, cols] problem:
@@ -73,7 +75,8 @@ typedef struct CUstream_st* ln_stream_t;
 typedef enum ln_status {
     LN_OK = 0,
     LN_EINVAL = 1,        /* a NULL required pointer, rows < 0, cols <= 0, eps < 0 or not finite */
-    LN_EALIGN = 2,        /* a workspace pointer that is not 256-byte aligned */
+    LN_EALIGN = 2,        /* a workspace pointer that is not 256-byte aligned, or a checkpoint's
+                             integers that are not 16-byte aligned */
     LN_EUNSUPPORTED = 3,  /* cols > LN_MAX_COLS, rows > LN_MAX_ROWS, or not an sm_103 device */
     LN_ECUDA = 4,         /* a CUDA runtime call failed; see ln_last_cuda_error() */
     LN_ETIMEOUT = 5,      /* a bounded device-side wait ran out (reported by ln_device_check) */
@@ -417,6 +420,145 @@ ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
                           const float* teacher, const float* weights, int64_t rows, int64_t V,
                           int64_t K, float scale, float dloss, float* losses, ln_bf16* dlogits,
                           int64_t ldd, ln_stream_t stream);
+
+/*
+ * Softmax of attention scores with a learned relative position bias, and its gradients.  For sequence b,
+ * head h, its query i at position p = q_pos[b] + i and key j at distance d = j - p:
+ *
+ *   z_j = scale x_j + table[bucket(d), h] + mask_j,  y = softmax(z) over the keys that take part
+ *   dS = y (dy - sum_j dy_j y_j),  dx = scale dS
+ *   dtable[k, h] = sum of dS over b, i and the j with bucket(j - p) = k
+ *
+ * A key j >= lens[b], or, where the call is causal, j > p, takes no part: its score, mask and dy are not
+ * read, whatever they are.  Nor does one whose mask or z is -inf (a mask of -inf removes a key whatever its
+ * score is).  y and dx are 0 at such keys, and throughout a row that has no other.  A mask of the type's
+ * lowest finite value is an ordinary addend: a row of nothing else is a softmax of its scores at that
+ * magnitude, as the formula says.  In the backward a key of probability 0 counts for nothing, whatever its dy.
+ *
+ * bucket(d) is the number of edges at or below max(-d, 0), or, where the call is bidirectional, at or below |d|,
+ * plus n_edges + 1 for d > 0; so the table has n_edges + 1 rows, or twice as many.  The customary
+ * logarithmic buckets of a side of s = 2 m buckets up to a distance D are the edges 1 .. m followed by the least n
+ * with (n / m)^m >= (D / m)^k for k = 1 .. m - 1 (the binding's rel_edges gives them exactly).
+ *
+ *   B, H, Lq, Lk           sequences, heads, queries and keys of each (H, Lk >= 1)
+ *   table      [buckets, H]  fp32 (table_f32 != 0) or bf16; also the type of dtable
+ *   edges      [n_edges]   HOST memory, read before the call returns; 1 <= edges[0] <= edges[1] <= ...
+ *   lens       [B] int32   keys of each sequence (held to 0 .. Lk), or NULL (Lk)
+ *   q_pos      [B] int32   position of each sequence's query 0, or NULL (0); may be negative, or past Lk
+ *   x, y, dy, dx [B, H, Lq, Lk], row r = (b H + h) Lq + i at r * ld elements (ld >= Lk)
+ *   mask       [mask_rows, Lk]  additive, row r % mask_rows; or NULL
+ *   q, k                   a checkpoint of y (ln_ckpt8_*, rows B H Lq, cols Lk): written by the forward where
+ *                          they are given; read by the backward in place of y (exactly one of the two)
+ *   dtable                 overwritten; may be NULL, and then so may workspace
+ *
+ * y may be x itself, and dx may be dy itself, with the same ld; otherwise outputs overlap nothing.  Columns
+ * Lk .. ld of a row are left as they are.  Pointers and ld need no alignment (q: 16 bytes).  Limits: Lk <=
+ * LN_REL_MAX_KEYS, H <= LN_REL_MAX_HEADS, n_edges <= LN_REL_MAX_EDGES, edges <= LN_REL_MAX_SPAN, B H Lq <=
+ * LN_MAX_ROWS.  No rows: the forward does nothing, the backward zeroes dtable.
+ *
+ * The workspace (the backward with dtable) is the caller's, of ln_softmax_rel_workspace_bytes_* bytes; what it
+ * holds before and after a call is of no account, and calls that may overlap need one each.  Nothing is
+ * allocated, nothing is atomic, and no kernel waits for another block: results are bitwise repeatable for the same
+ * sizes on devices of as many SMs.
+ */
+#define LN_REL_MAX_KEYS (1 << 20)
+#define LN_REL_MAX_HEADS 65536
+#define LN_REL_MAX_EDGES 255
+#define LN_REL_MAX_SPAN 16384
+
+typedef struct ln_rel {
+    int64_t B, H, Lq, Lk;
+    const void* table;
+    const int32_t* edges;
+    const int32_t* lens;
+    const int32_t* q_pos;
+    int32_t n_edges;
+    int32_t table_f32;
+    int32_t bidirectional;
+    int32_t causal;
+    float scale;
+} ln_rel;
+
+ln_status ln_softmax_rel_fwd_f32(const ln_rel* r, const float* x, int64_t ldx, const float* mask,
+                                 int64_t mask_rows, float* y, int64_t ldy, int8_t* q, uint8_t* k,
+                                 ln_stream_t stream);
+
+ln_status ln_softmax_rel_bwd_f32(const ln_rel* r, const float* dy, int64_t ldd, const float* y, int64_t ldy,
+                                 const int8_t* q, const uint8_t* k, float* dx, int64_t ldx, void* dtable,
+                                 void* workspace, size_t workspace_bytes, ln_stream_t stream);
+
+/* 0 for invalid arguments (and for no rows). */
+size_t ln_softmax_rel_workspace_bytes_f32(const ln_rel* r);
+
+ln_status ln_softmax_rel_fwd_bf16(const ln_rel* r, const ln_bf16* x, int64_t ldx, const ln_bf16* mask,
+                                 int64_t mask_rows, ln_bf16* y, int64_t ldy, int8_t* q, uint8_t* k,
+                                 ln_stream_t stream);
+
+ln_status ln_softmax_rel_bwd_bf16(const ln_rel* r, const ln_bf16* dy, int64_t ldd, const ln_bf16* y, int64_t ldy,
+                                 const int8_t* q, const uint8_t* k, ln_bf16* dx, int64_t ldx, void* dtable,
+                                 void* workspace, size_t workspace_bytes, ln_stream_t stream);
+
+/* 0 for invalid arguments (and for no rows). */
+size_t ln_softmax_rel_workspace_bytes_bf16(const ln_rel* r);
+
+/*
+ * 8-bit checkpoints of activations.  Each 32 columns of a row (a block; a row's last may be shorter) are kept as
+ * integers q in -127 .. 127 and one byte k that stands for the step 2^(k - 127), the least power of two, and at
+ * least 2^-126, for which the block's largest magnitude rounds to at most 127:
+ *
+ *   store  q = x / 2^(k - 127), rounded to nearest, ties to even      load  x = q 2^(k - 127)
+ *
+ * Off by at most half a step, so by at most 1/127 of the block's largest magnitude (or 2^-127, where that is
+ * more).  The largest step is 2^121: magnitudes of 127.5 * 2^121 and more are held to 127 * 2^121.  What a checkpoint stands for is exact in both types, and storing it again gives the same checkpoint
+ * or one that stands for the same values.  A block that holds an infinity or a NaN has k = 255 and q = 0 and comes
+ * back as NaN throughout.
+ *
+ *   x   [rows, cols], row r at x + r * ld (ld >= cols; columns cols .. ld are left as they are)
+ *   q   [rows, 32 ceil(cols / 32)]  16-byte aligned; the columns past cols are written as 0
+ *   k   [rows, ceil(cols / 32)]
+ *
+ * Limits: 1 <= cols <= LN_REL_MAX_KEYS, 0 <= rows <= LN_MAX_ROWS.  Nothing is allocated.
+ */
+ln_status ln_ckpt8_store_f32(const float* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,
+                             ln_stream_t stream);
+
+ln_status ln_ckpt8_load_f32(const int8_t* q, const uint8_t* k, int64_t rows, int64_t cols, float* x,
+                            int64_t ld, ln_stream_t stream);
+
+ln_status ln_ckpt8_store_bf16(const ln_bf16* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,
+                             ln_stream_t stream);
+
+ln_status ln_ckpt8_load_bf16(const int8_t* q, const uint8_t* k, int64_t rows, int64_t cols, ln_bf16* x,
+                            int64_t ld, ln_stream_t stream);
+
+/*
+ * Backward of the fused residual-add + LayerNorm (RMSNorm) from a checkpoint of the tensor that the forward
+ * normalised (its res_out, or x): ln_bwd_* (ln_rms_bwd_*) with x_or_res_out as the checkpoint gives it back, and
+ * the forward's own mean and rstd (rrms).  q, k as ln_ckpt8_store_* writes them.  The workspace is the caller's,
+ * 256-byte aligned, of ln_bwd_ckpt8_workspace_bytes(rows, cols) bytes (enough for both); what it holds before
+ * and after is of no account, and calls that may overlap need one each.  dx may be dy itself.  Two launches; no
+ * atomics and no waits between blocks: bitwise repeatable.  rows == 0 writes dgamma = dbeta = 0.  Limits and
+ * errors as for ln_bwd_*.
+ */
+size_t ln_bwd_ckpt8_workspace_bytes(int64_t rows, int64_t cols);
+
+ln_status ln_bwd_ckpt8_f32(const float* dy, const int8_t* q, const uint8_t* k, const float* gamma,
+                           const float* mean, const float* rstd, float* dx, float* dgamma, float* dbeta,
+                           int64_t rows, int64_t cols, void* workspace, size_t workspace_bytes,
+                           ln_stream_t stream);
+
+ln_status ln_rms_bwd_ckpt8_f32(const float* dy, const int8_t* q, const uint8_t* k, const float* gamma,
+                               const float* rrms, float* dx, float* dgamma, int64_t rows, int64_t cols,
+                               void* workspace, size_t workspace_bytes, ln_stream_t stream);
+
+ln_status ln_bwd_ckpt8_bf16(const ln_bf16* dy, const int8_t* q, const uint8_t* k, const ln_bf16* gamma,
+                           const float* mean, const float* rstd, ln_bf16* dx, ln_bf16* dgamma, ln_bf16* dbeta,
+                           int64_t rows, int64_t cols, void* workspace, size_t workspace_bytes,
+                           ln_stream_t stream);
+
+ln_status ln_rms_bwd_ckpt8_bf16(const ln_bf16* dy, const int8_t* q, const uint8_t* k, const ln_bf16* gamma,
+                               const float* rrms, ln_bf16* dx, ln_bf16* dgamma, int64_t rows, int64_t cols,
+                               void* workspace, size_t workspace_bytes, ln_stream_t stream);
 
 /*
  * LayerNorm forward with the bias + dropout + residual prologue fused in ("Accelerating

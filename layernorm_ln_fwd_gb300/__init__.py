@@ -12,7 +12,10 @@ both x and res), dgamma and dbeta, the latter bitwise reproducible.  ``rms_fwd``
 ``rms_bwd`` do the same for the fused residual-add + RMSNorm ("GPU Performance from First
 Principles", section 6.1).  Over rows of logits, beside ``xent``: ``logprobs`` (token log
 probabilities, entropy, rank, top alternatives), its gradient ``logprobs_bwd`` and ``distill``
-(loss and gradient against a teacher's top logits).  Definitions:
+(loss and gradient against a teacher's top logits).  Over attention scores, beside
+``softmax_fwd``: ``softmax_rel_fwd`` and ``softmax_rel_bwd`` (a learned relative position bias by
+buckets, and its gradient).  ``ckpt8_store`` and ``ckpt8_load`` keep an activation in 8 bits;
+``softmax_rel_bwd``, ``bwd_ckpt8`` and ``rms_bwd_ckpt8`` read it in the backward.  Definitions:
 "Accelerating Transformer on GPU (II): Training with LightSeq2", sections 2.1, 2.2 and 2.4;
 residual fusion as in "llm.c: the llmc/ CUDA kernel layer", section 3.2.
 """
@@ -20,8 +23,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libln.so")
@@ -30,6 +35,8 @@ STATUS = {0: "LN_OK", 1: "LN_EINVAL", 2: "LN_EALIGN", 3: "LN_EUNSUPPORTED", 4: "
           5: "LN_ETIMEOUT", 6: "LN_ENOSPACE"}
 MAX_COLS = 16384
 MAX_TOP = 256
+MAX_REL_SPAN = 16384
+CKPT_BLOCK = 32
 PATH_AUTO, PATH_WARP, PATH_BLOCK, PATH_SCALAR = 0, 1, 2, 3
 
 # Every symbol include/ln.h declares, with its ctypes signature.
@@ -74,6 +81,21 @@ SIGNATURES = {
     "ln_logprobs_bwd_bf16": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, _I64, _P]),
     "ln_distill_f32": (_INT, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _F, _P, _P, _I64, _P]),
     "ln_distill_bf16": (_INT, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _F, _F, _P, _P, _I64, _P]),
+    "ln_softmax_rel_workspace_bytes_f32": (_SZ, [_P]),
+    "ln_softmax_rel_workspace_bytes_bf16": (_SZ, [_P]),
+    "ln_bwd_ckpt8_workspace_bytes": (_SZ, [_I64, _I64]),
+    "ln_softmax_rel_fwd_f32": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
+    "ln_softmax_rel_bwd_f32": (_INT, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "ln_ckpt8_store_f32": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ln_ckpt8_load_f32": (_INT, [_P, _P, _I64, _I64, _P, _I64, _P]),
+    "ln_bwd_ckpt8_f32": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
+    "ln_rms_bwd_ckpt8_f32": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
+    "ln_softmax_rel_fwd_bf16": (_INT, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
+    "ln_softmax_rel_bwd_bf16": (_INT, [_P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "ln_ckpt8_store_bf16": (_INT, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "ln_ckpt8_load_bf16": (_INT, [_P, _P, _I64, _I64, _P, _I64, _P]),
+    "ln_bwd_ckpt8_bf16": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
+    "ln_rms_bwd_ckpt8_bf16": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P, _SZ, _P]),
     "ln_fwd_bias_dropout_f32": (_INT, [_P, _P, _P, _P, _P, _F, _F, _U64, _U64, _I64, _I64, _P, _P,
                                        _P, _P, _P]),
     "ln_fwd_bias_dropout_bf16": (_INT, [_P, _P, _P, _P, _P, _F, _F, _U64, _U64, _I64, _I64, _P,
@@ -590,6 +612,310 @@ def distill(logits, ids, teacher, weights=None, scale: float = 1.0, dloss: float
                         rows, V, K, float(scale), float(dloss), _addr(losses), _addr(dlogits), ldd,
                         raw_stream(dev.index)))
     return losses, dlogits
+
+
+class Ckpt8(NamedTuple):
+    """A [rows, cols] activation kept in 8 bits: ``q``, int8 [rows, 32 * blocks], and ``k``, uint8
+    [rows, blocks], blocks = ceil(cols / 32); column j of a row stands for q[j] * 2 ** (k[j // 32] -
+    127), and a block of k = 255 for NaN."""
+    q: object
+    k: object
+    cols: int
+
+
+def _new_ckpt(rows, cols, dev):
+    import torch
+    blocks = -(-cols // CKPT_BLOCK)
+    return Ckpt8(torch.empty((rows, blocks * CKPT_BLOCK), dtype=torch.int8, device=dev),
+                 torch.empty((rows, blocks), dtype=torch.uint8, device=dev), cols)
+
+
+def _need_ckpt(ck, name, rows, cols, dev):
+    """A checkpoint of [rows, cols] on the device (rows None: as many as it has)."""
+    import torch
+    if not isinstance(ck, Ckpt8):
+        raise TypeError(f"{name} must be a Ckpt8")
+    if ck.cols != cols:
+        raise ValueError(f"{name} has {ck.cols} columns, expected {cols}")
+    if cols < 1:
+        raise ValueError(f"{name} has no columns")
+    if rows is None:
+        rows = ck.q.shape[0]
+    blocks = -(-cols // CKPT_BLOCK)
+    _need(ck.q, f"{name}.q", (rows, blocks * CKPT_BLOCK), torch.int8, dev)
+    _need(ck.k, f"{name}.k", (rows, blocks), torch.uint8, dev)
+    return ck
+
+
+def ckpt8_store(x, out=None, stream=None):
+    """Keeps x, [rows, cols] with contiguous rows, in 8 bits: each 32 columns of a row as integers of
+    -127 .. 127 times the least power of two for which the largest rounds to at most 127 (so off by at
+    most 1/127 of it).  Returns a :class:`Ckpt8` (``out``, if given)."""
+    rows, cols, ld = _rows_of(x, "x")
+    name, fn, raw_stream = _entry("ln_ckpt8_store_", x.dtype)
+    dev = x.device
+    if out is not None:
+        _need_ckpt(out, "out", rows, cols, dev)
+    with _on(dev, stream):
+        ck = _new_ckpt(rows, cols, dev) if out is None else out
+        _check(name, fn(x.data_ptr(), ld, rows, cols, ck.q.data_ptr(), ck.k.data_ptr(), raw_stream(dev.index)))
+    return ck
+
+
+def ckpt8_load(ck, dtype=None, out=None, stream=None):
+    """The activation that a :class:`Ckpt8` stands for, [rows, cols] in float32 or bfloat16 (the
+    default), exact in both; or written into ``out``, whose rows may be padded."""
+    import torch
+    dev = ck.q.device if isinstance(ck, Ckpt8) else None
+    _need_ckpt(ck, "ck", None, getattr(ck, "cols", 0), dev)
+    rows, cols = ck.q.shape[0], ck.cols
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    name, fn, raw_stream = _entry("ln_ckpt8_load_", dtype)
+    ld = cols
+    if out is not None:
+        if out.device != dev or out.dtype != dtype or tuple(out.shape) != (rows, cols):
+            raise ValueError(f"out must be {dtype} [{rows}, {cols}] on {dev}")
+        ld = _rows_of(out, "out")[2]
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _check(name, fn(ck.q.data_ptr(), ck.k.data_ptr(), rows, cols, out.data_ptr(), ld, raw_stream(dev.index)))
+    return out
+
+
+def _workspace(t, nbytes, dev):
+    """(tensor, bytes) of a workspace: the caller's, or a new one, which belongs to the call's stream."""
+    import torch
+    if t is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev), nbytes
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return t, t.numel() * t.element_size()
+
+
+def bwd_ckpt8(dy, ck, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """:func:`bwd` with the forward's res_out (or x) as a :class:`Ckpt8` keeps it; mean and rstd as the
+    forward wrote them.  Returns (dx, dgamma, dbeta).  ``workspace``: at least
+    :func:`ckpt8_workspace_bytes` bytes of any content, by default allocated for the call."""
+    return _norm_bwd_ckpt8(dy, ck, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream, False)
+
+
+def rms_bwd_ckpt8(dy, ck, gamma, rrms, dx=None, dgamma=None, workspace=None, stream=None):
+    """:func:`rms_bwd` with the forward's res_out (or x) as a :class:`Ckpt8` keeps it.  Returns (dx,
+    dgamma); ``workspace`` as for :func:`bwd_ckpt8`."""
+    return _norm_bwd_ckpt8(dy, ck, gamma, None, rrms, dx, dgamma, None, workspace, stream, True)[:2]
+
+
+def _norm_bwd_ckpt8(dy, ck, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream, rms):
+    import torch
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D [rows, cols]")
+    rows, cols = dy.shape
+    dt, dev = dy.dtype, dy.device
+    name, fn, raw_stream = _entry("ln_rms_bwd_ckpt8_" if rms else "ln_bwd_ckpt8_", dt)
+    _need(dy, "dy", (rows, cols), dt, dev)
+    _need_ckpt(ck, "ck", rows, cols, dev)
+    _need(gamma, "gamma", (cols,), dt, dev)
+    if not rms:
+        _need(mean, "mean", (rows,), torch.float32, dev)
+    _need(rstd, "rrms" if rms else "rstd", (rows,), torch.float32, dev)
+    for t, what, shape in ((dx, "dx", (rows, cols)), (dgamma, "dgamma", (cols,)), (dbeta, "dbeta", (cols,))):
+        if t is not None:
+            _need(t, what, shape, dt, dev)
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty((rows, cols), dtype=dt, device=dev)
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=dt, device=dev)
+        if dbeta is None and not rms:
+            dbeta = torch.empty(cols, dtype=dt, device=dev)
+        ws, nbytes = _workspace(workspace, lib().ln_bwd_ckpt8_workspace_bytes(rows, cols), dev)
+        head = (dy.data_ptr(), ck.q.data_ptr(), ck.k.data_ptr(), gamma.data_ptr())
+        tail = (rows, cols, ws.data_ptr(), nbytes, raw_stream(dev.index))
+        if rms:
+            status = fn(*head, rstd.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), *tail)
+        else:
+            status = fn(*head, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+                        *tail)
+        _check(name, status)
+    return dx, dgamma, dbeta
+
+
+def ckpt8_workspace_bytes(rows: int, cols: int) -> int:
+    """Bytes of workspace :func:`bwd_ckpt8` and :func:`rms_bwd_ckpt8` need on the current device."""
+    return int(lib().ln_bwd_ckpt8_workspace_bytes(rows, cols))
+
+
+@functools.lru_cache(maxsize=256)
+def rel_edges(buckets: int, max_distance: int = 128, bidirectional: bool = True) -> tuple:
+    """The distances at which buckets 1, 2, ... of a side begin.  A side has ``buckets`` of them, or half
+    as many where they are ``bidirectional`` (keys behind a query, then keys ahead of it): the first half
+    hold one distance each, the others grow by equal factors up to ``max_distance``, and the last takes
+    all beyond.  Exact: bucket m + k begins at the least n with (n / m)^(s - m) >= (max_distance / m)^k, for a
+    side of s buckets, m = s // 2."""
+    side = buckets // 2 if bidirectional else buckets
+    if bidirectional and buckets % 2:
+        raise ValueError("bidirectional buckets come in pairs")
+    if side < 2 or side > 256:
+        raise ValueError("a side has 2 to 256 buckets")
+    near = side // 2
+    if not near < max_distance <= MAX_REL_SPAN:
+        raise ValueError(f"max_distance must be above {near} and at most {MAX_REL_SPAN}")
+    far = side - near
+    found = list(range(1, near + 1))
+    for k in range(1, far):
+        least = max_distance ** k * near ** far
+        lo, hi = found[-1], max_distance
+        while lo < hi:
+            mid = (lo + hi) // 2
+            if mid ** far * near ** k >= least:
+                hi = mid
+            else:
+                lo = mid + 1
+        found.append(lo)
+    return tuple(found)
+
+
+class _Rel(ctypes.Structure):
+    """ln_rel of include/ln.h."""
+    _fields_ = [("B", _I64), ("H", _I64), ("Lq", _I64), ("Lk", _I64), ("table", _P), ("edges", _P), ("lens", _P),
+                ("q_pos", _P), ("n_edges", ctypes.c_int32), ("table_f32", ctypes.c_int32),
+                ("bidirectional", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", _F)]
+
+
+@functools.lru_cache(maxsize=256)
+def _edge_array(buckets, max_distance, bidirectional):
+    edges = rel_edges(buckets, max_distance, bidirectional)
+    return (ctypes.c_int32 * len(edges))(*edges), len(edges)
+
+
+def _rows4(t, name):
+    """(B, H, Lq, Lk, ld) of a 4-D tensor whose rows are contiguous, ld >= Lk elements apart throughout."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be 4-D [B, H, Lq, Lk]")
+    B, H, Lq, Lk = t.shape
+    if t.is_contiguous():
+        return B, H, Lq, Lk, Lk
+    sb, sh, sq, sk = t.stride()
+    ld, inner = None, 1
+    for n, s in ((Lq, sq), (H, sh), (B, sb)):
+        if n > 1:
+            if ld is None:
+                ld = s
+            if s != ld * inner:
+                raise ValueError(f"{name} must have its rows at equal distances")
+        inner *= n
+    if sk != 1 and Lk > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if ld is None:
+        ld = Lk
+    if ld < Lk:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return B, H, Lq, Lk, ld
+
+
+def _like4(t, name, shape, dtype, dev):
+    """ld of an optional [B, H, Lq, Lk] tensor of the call's type."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _rows4(t, name)[4]
+
+
+def _rel(shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dtype, dev):
+    import torch
+    B, H, Lq, Lk = shape
+    if table.dim() != 2 or table.shape[1] != H:
+        raise ValueError(f"table must be [buckets, {H}]")
+    if table.dtype != torch.float32 and table.dtype != dtype:
+        raise TypeError(f"table has dtype {table.dtype}, expected {dtype} or torch.float32")
+    _need(table, "table", table.shape, table.dtype, dev)
+    for t, what in ((lens, "lens"), (q_pos, "q_pos")):
+        if t is not None:
+            _need(t, what, (B,), torch.int32, dev)
+    edges, n = _edge_array(table.shape[0], max_distance, bool(bidirectional))
+    rel = _Rel(B, H, Lq, Lk, table.data_ptr(), ctypes.addressof(edges), _addr(lens), _addr(q_pos), n,
+               table.dtype == torch.float32, bool(bidirectional), bool(causal), scale)
+    rel.held = edges  # as long as the call reads it
+    return rel
+
+
+def softmax_rel_fwd(x, table, max_distance: int = 128, bidirectional: bool = True, scale: float = 1.0,
+                    causal: bool = False, lens=None, q_pos=None, mask=None, ckpt: bool = False, y=None,
+                    stream=None):
+    """Softmax of attention scores with a learned relative position bias: y = softmax(scale * x +
+    table[bucket(j - p), h] + mask) over keys j, for the query at position p = q_pos[b] + i.
+
+    x: [B, H, Lq, Lk], its rows at equal distances (a view into a wider buffer is fine); table: [buckets,
+    H] in x's type or float32, its buckets as :func:`rel_edges` cuts them up to ``max_distance``;
+    ``causal`` removes keys behind (j > p), lens (int32 [B]) those from lens[b] on, whose scores are not
+    read; q_pos: int32 [B], the position of each sequence's first query (0 by default; a decode step's is
+    lens - 1); mask: additive, [mask_rows, Lk] in x's type, row r % mask_rows of row r = (b H + h) Lq + i,
+    -inf removes a key.  A row with no keys left is 0.  ``y`` may be x.
+
+    Returns (y, ck): ck is a :class:`Ckpt8` of y as [B H Lq, Lk], written in the same pass, with
+    ``ckpt`` (or None), for :func:`softmax_rel_bwd`."""
+    import torch
+    B, H, Lq, Lk, ld = _rows4(x, "x")
+    name, fn, raw_stream = _entry("ln_softmax_rel_fwd_", x.dtype)
+    dt, dev = x.dtype, x.device
+    rel = _rel(x.shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
+    mask_rows = 1
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be 2-D [mask_rows, Lk]")
+        mask_rows = mask.shape[0]
+        _need(mask, "mask", (mask_rows, Lk), dt, dev)
+    ldy = Lk if y is None else _like4(y, "y", x.shape, dt, dev)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
+        ck = _new_ckpt(B * H * Lq, Lk, dev) if ckpt else None
+        _check(name, fn(ctypes.addressof(rel), x.data_ptr(), ld, _addr(mask), mask_rows, y.data_ptr(), ldy,
+                        ck and ck.q.data_ptr(), ck and ck.k.data_ptr(), raw_stream(dev.index)))
+    return y, ck
+
+
+def softmax_rel_bwd(dy, y, table, max_distance: int = 128, bidirectional: bool = True, scale: float = 1.0,
+                    causal: bool = False, lens=None, q_pos=None, want_table: bool = True, dx=None, dtable=None,
+                    workspace=None, stream=None):
+    """Gradients of :func:`softmax_rel_fwd`: dx = scale * dS with dS = y (dy - sum dy y), and dtable, the
+    sum of dS over all pairs of a bucket, in the table's type.  y: the forward's, or its :class:`Ckpt8`;
+    the other arguments as the forward had them (what ``causal`` and lens removed is not read).  ``dx`` may be
+    dy.  Returns (dx, dtable); dtable is None without ``want_table``.  ``workspace``: as many bytes as
+    ``ln_softmax_rel_workspace_bytes_*`` says, of any content, by default allocated for the call."""
+    import torch
+    B, H, Lq, Lk, ld = _rows4(dy, "dy")
+    name, fn, raw_stream = _entry("ln_softmax_rel_bwd_", dy.dtype)
+    dt, dev = dy.dtype, dy.device
+    rel = _rel(dy.shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
+    ldy, probs, q, k = Lk, None, None, None
+    if isinstance(y, Ckpt8):
+        _need_ckpt(y, "y", B * H * Lq, Lk, dev)
+        q, k = y.q.data_ptr(), y.k.data_ptr()
+    else:
+        ldy = _like4(y, "y", dy.shape, dt, dev)
+        probs = y.data_ptr()
+    ldx = Lk if dx is None else _like4(dx, "dx", dy.shape, dt, dev)
+    if dtable is not None:
+        _need(dtable, "dtable", table.shape, table.dtype, dev)
+        want_table = True
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
+        ws, nbytes = None, 0
+        if want_table:
+            if dtable is None:
+                dtable = torch.empty(table.shape, dtype=table.dtype, device=dev)
+            ws, nbytes = _workspace(workspace, _entry("ln_softmax_rel_workspace_bytes_", dt)[1](ctypes.addressof(rel)),
+                                    dev)
+        _check(name, fn(ctypes.addressof(rel), dy.data_ptr(), ld, probs, ldy, q, k, dx.data_ptr(), ldx, _addr(dtable),
+                        _addr(ws), nbytes, raw_stream(dev.index)))
+    return dx, dtable
 
 
 def dropout_keep_bytes(rows: int, cols: int) -> int:

@@ -1,0 +1,122 @@
+// ckpt8.cu -- 8-bit checkpoints of activations: rows to integers and steps (ckpt8.cuh has the format), and back.
+//
+// A warp takes 32 vectors of 16 bytes of a row at a time, several of them in flight; rows of whole blocks that
+// follow one another are taken as one long row.  Bound by memory: each value is read once and written once.
+#include <algorithm>
+
+#include "ckpt8.cuh"
+#include "rel_ops.h"
+#include "row_io.cuh"
+
+namespace lnk {
+namespace {
+
+constexpr int kCkThreads = 256;
+constexpr int kCkFlight = 4;  // a warp's pieces of rows in flight
+
+struct CkParams {
+    const void* x;   // store
+    void* out;       // load
+    int64_t ld, rows, cols, segs, total;
+    int64_t ldq, ldk;
+    int8_t* q;
+    uint8_t* k;
+    Extent ex;
+};
+
+template <typename T, bool STORE>
+__global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
+    constexpr int V = Io<T>::kVec, S = 32 * V;
+    pdl_enter();
+    const int lane = threadIdx.x & 31, col = lane * V;
+    const int64_t warps = (int64_t)gridDim.x * (kCkThreads / 32);
+    const int64_t w0 = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t base = w0; base < p.total; base += warps * kCkFlight) {
+        uint4 u[kCkFlight];
+        CkptRaw<T> raw[kCkFlight];
+        int64_t row[kCkFlight], first[kCkFlight];
+        int n[kCkFlight];
+#pragma unroll
+        for (int f = 0; f < kCkFlight; ++f) {
+            const int64_t at = base + f * warps;
+            n[f] = 0;
+            if (at >= p.total) continue;
+            row[f] = p.segs == p.total ? 0 : at / p.segs;
+            first[f] = (at - row[f] * p.segs) * S;
+            n[f] = (int)min((int64_t)S, p.cols - first[f]);
+            if (col < n[f]) {
+                if constexpr (STORE)
+                    u[f] = load_columns<T>(static_cast<const T*>(p.x) + row[f] * p.ld + first[f], col, n[f], p.ex);
+                else
+                    raw[f].load(p.q + row[f] * p.ldq + first[f], p.k + row[f] * p.ldk + first[f] / kCkptBlock, col);
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < kCkFlight; ++f) {
+            if (n[f] == 0) continue;  // the same in the whole warp
+            if constexpr (STORE) {
+                if (col >= n[f])
+                    u[f] = make_uint4(0, 0, 0, 0);
+                else if (col + V > n[f])
+                    u[f] = first_of<T>(u[f], n[f] - col);
+                ckpt_keep<T>(u[f], col, ckpt_blocks(n[f]) * kCkptBlock, p.q + row[f] * p.ldq + first[f],
+                             p.k + row[f] * p.ldk + first[f] / kCkptBlock);
+            } else {
+                f2 v[Pairs<T>::kPairs];
+                if (col < n[f]) {
+                    raw[f].values(v);
+                    u[f] = Pairs<T>::pack(v);
+                }
+                store_columns<T>(static_cast<T*>(p.out) + row[f] * p.ld + first[f], col, n[f], u[f]);
+            }
+        }
+    }
+}
+
+template <typename T, bool STORE>
+cudaError_t launch_t(CkParams p, cudaStream_t stream) {
+    constexpr int S = 32 * Io<T>::kVec;
+    p.ldk = ckpt_blocks((int)p.cols);
+    p.ldq = p.ldk * kCkptBlock;
+    const char* base = static_cast<const char*>(p.x);
+    p.ex = Extent{base, base ? base + ((p.rows - 1) * p.ld + p.cols) * (int64_t)sizeof(T) : base};
+    if (p.cols == p.ldq && p.ld == p.cols) {
+        p.cols *= p.rows;
+        p.rows = 1;
+    }
+    p.segs = (p.cols + S - 1) / S;
+    p.total = p.segs * p.rows;
+    const void* kern = (const void*)ckpt8_kernel<T, STORE>;
+    const int64_t slots = (int64_t)std::max(1, blocks_per_sm(kern, kCkThreads, 0)) * device_info(-1).sms;
+    const int64_t need = (p.total + kCkThreads / 32 - 1) / (kCkThreads / 32);
+    void* args[] = {&p};
+    return launch_kernel(kern, dim3((unsigned)std::min(slots, need)), dim3(kCkThreads), 0, stream, args, false);
+}
+
+}  // namespace
+
+cudaError_t launch_ckpt8_store(Dtype dt, const void* x, int64_t ld, int64_t rows, int cols, int8_t* q,
+                               uint8_t* k, cudaStream_t stream) {
+    CkParams p = {};
+    p.x = x;
+    p.ld = ld;
+    p.rows = rows;
+    p.cols = cols;
+    p.q = q;
+    p.k = k;
+    return dt == Dtype::F32 ? launch_t<float, true>(p, stream) : launch_t<__nv_bfloat16, true>(p, stream);
+}
+
+cudaError_t launch_ckpt8_load(Dtype dt, const int8_t* q, const uint8_t* k, int64_t rows, int cols, void* x,
+                              int64_t ld, cudaStream_t stream) {
+    CkParams p = {};
+    p.out = x;
+    p.ld = ld;
+    p.rows = rows;
+    p.cols = cols;
+    p.q = const_cast<int8_t*>(q);
+    p.k = const_cast<uint8_t*>(k);
+    return dt == Dtype::F32 ? launch_t<float, false>(p, stream) : launch_t<__nv_bfloat16, false>(p, stream);
+}
+
+}  // namespace lnk

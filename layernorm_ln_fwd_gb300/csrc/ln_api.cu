@@ -12,6 +12,7 @@
 #include "ln.h"
 #include "ln_device.cuh"
 #include "ln_internal.h"
+#include "rel_ops.h"
 #include "vocab_ops.h"
 
 // One status word per device.  Kernels OR kStatusTimeout into it when a bounded wait runs
@@ -609,6 +610,198 @@ ln_status dropout_bwd_impl(Dtype dt, const T* ds, float p, uint64_t seed, uint64
 }  // namespace
 }  // namespace lnk
 
+namespace lnk {
+namespace {
+// The softmax with a relative position bias: sizes, edges and what both directions take.
+ln_status check_rel(const ln_rel* r) {
+    if (!r || r->B < 0 || r->H <= 0 || r->Lq < 0 || r->Lk <= 0) return LN_EINVAL;
+    if (!std::isfinite(r->scale) || r->n_edges < 0 || (r->n_edges > 0 && !r->edges)) return LN_EINVAL;
+    if (r->Lk > LN_REL_MAX_KEYS || r->H > LN_REL_MAX_HEADS || r->n_edges > LN_REL_MAX_EDGES ||
+        r->Lq > LN_MAX_ROWS || r->B > LN_MAX_ROWS)
+        return LN_EUNSUPPORTED;
+    if (r->Lq > 0 && r->B > LN_MAX_ROWS / (r->H * r->Lq)) return LN_EUNSUPPORTED;
+    for (int i = 0; i < r->n_edges; ++i) {
+        if (r->edges[i] < (i ? r->edges[i - 1] : 1)) return LN_EINVAL;
+        if (r->edges[i] > LN_REL_MAX_SPAN) return LN_EUNSUPPORTED;
+    }
+    return LN_OK;
+}
+
+// Rows ld elements apart: they hold Lk, and a row's address stays within 63 bits of byte offset.
+bool rel_rows_ok(const ln_rel* r, int64_t ld) {
+    const int64_t rows = r->B * r->H * r->Lq;
+    return ld >= r->Lk && !(rows > 1 && ld > INT64_MAX / 4 / rows);
+}
+
+bool ckpt_aligned(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+
+void fill_rel(const ln_rel* r, RelBuckets* bk, RelArgs* a) {
+    bk->n = r->n_edges;
+    bk->both = r->bidirectional ? 1 : 0;
+    for (int i = 0; i < r->n_edges; ++i) bk->edge[i] = r->edges[i];
+    a->buckets = bk;
+    a->table = r->table;
+    a->table_f32 = r->table_f32 != 0;
+    a->lens = r->lens;
+    a->q_pos = r->q_pos;
+    a->B = (int)r->B;
+    a->H = (int)r->H;
+    a->Lq = (int)r->Lq;
+    a->Lk = (int)r->Lk;
+    a->causal = r->causal != 0;
+    a->scale = r->scale;
+}
+
+int rel_buckets(const ln_rel* r) { return (r->n_edges + 1) * (r->bidirectional ? 2 : 1); }
+
+size_t rel_workspace(Dtype dt, const ln_rel* r) {
+    if (check_rel(r) != LN_OK || r->B == 0 || r->Lq == 0) return 0;
+    const int dev = current_device();
+    const int sms = dev < 0 ? 0 : device_info(dev).sms;
+    return sms <= 0 ? 0 : rel_workspace_bytes(dt, r->B * r->H, (int)r->Lq, (int)r->Lk, rel_buckets(r), sms);
+}
+
+ln_status rel_fwd_impl(Dtype dt, const ln_rel* r, const void* x, int64_t ldx, const void* mask, int64_t mask_rows,
+                       void* y, int64_t ldy, int8_t* q, uint8_t* k, ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_rel(r);
+    if (st != LN_OK) return st;
+    if (!rel_rows_ok(r, ldx) || !rel_rows_ok(r, ldy) || (mask && mask_rows <= 0) || !q != !k) return LN_EINVAL;
+    if (mask_rows > LN_MAX_ROWS) return LN_EUNSUPPORTED;
+    if (r->B == 0 || r->Lq == 0) return LN_OK;
+    if (!x || !y || !r->table || (x == y && ldx != ldy)) return LN_EINVAL;
+    if (!ckpt_aligned(q)) return LN_EALIGN;
+    st = check_device();
+    if (st != LN_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    RelBuckets bk;
+    RelArgs a = {};
+    fill_rel(r, &bk, &a);
+    a.a = x;
+    a.lda = ldx;
+    a.out = y;
+    a.ldo = ldy;
+    a.q = q;
+    a.k = k;
+    a.mask = mask;
+    a.mask_rows = mask ? mask_rows : 1;
+    const RelPlan plan = rel_plan(dt, r->B * r->H, a.Lq, a.Lk, device_info(-1).sms);
+    int launches = 0;
+    const cudaError_t e = dt == Dtype::F32 ? launch_rel_fwd_f32(a, plan, stream, &launches)
+                                           : launch_rel_fwd_bf16(a, plan, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+
+ln_status rel_bwd_impl(Dtype dt, const ln_rel* r, const void* dy, int64_t ldd, const void* y, int64_t ldy,
+                       const int8_t* q, const uint8_t* k, void* dx, int64_t ldx, void* dtable, void* ws,
+                       size_t ws_bytes, ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_rel(r);
+    if (st != LN_OK) return st;
+    if (!rel_rows_ok(r, ldd) || !rel_rows_ok(r, ldx) || (y && !rel_rows_ok(r, ldy)) || !q != !k) return LN_EINVAL;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int buckets = rel_buckets(r);
+    const size_t tbytes = (size_t)buckets * (size_t)r->H * (r->table_f32 ? 4 : 2);
+    if (r->B == 0 || r->Lq == 0) {  // sums over no rows
+        if (!dtable) return LN_OK;
+        st = check_device();
+        if (st != LN_OK) return st;
+        return finish_call(cudaMemsetAsync(dtable, 0, tbytes, stream), 0, stream);
+    }
+    if (!dy || !dx || !y == !q || (dy == dx && ldd != ldx) || (dtable && !ws)) return LN_EINVAL;
+    if (!ckpt_aligned(q) || (dtable && (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)) return LN_EALIGN;
+    st = check_device();
+    if (st != LN_OK) return st;
+    const int sms = device_info(-1).sms;
+    if (dtable && ws_bytes < rel_workspace_bytes(dt, r->B * r->H, (int)r->Lq, (int)r->Lk, buckets, sms))
+        return LN_ENOSPACE;
+    RelBuckets bk;
+    RelArgs a = {};
+    fill_rel(r, &bk, &a);
+    a.a = dy;
+    a.lda = ldd;
+    a.y = y;
+    a.ldy = ldy;
+    a.q = const_cast<int8_t*>(q);
+    a.k = const_cast<uint8_t*>(k);
+    a.out = dx;
+    a.ldo = ldx;
+    a.mask_rows = 1;
+    a.dtable = dtable;
+    a.part = static_cast<float*>(ws);
+    const RelPlan plan = rel_plan(dt, r->B * r->H, a.Lq, a.Lk, sms);
+    int launches = 0;
+    const cudaError_t e = dt == Dtype::F32 ? launch_rel_bwd_f32(a, plan, stream, &launches)
+                                           : launch_rel_bwd_bf16(a, plan, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+
+// Sizes of an 8-bit checkpoint of [rows, cols], rows of the tensor ld elements apart.
+ln_status check_ckpt(int64_t rows, int64_t cols, int64_t ld) {
+    if (rows < 0 || cols <= 0 || ld < cols) return LN_EINVAL;
+    if (rows > LN_MAX_ROWS || cols > LN_REL_MAX_KEYS) return LN_EUNSUPPORTED;
+    if (rows > 1 && ld > INT64_MAX / 4 / rows) return LN_EINVAL;
+    return LN_OK;
+}
+
+ln_status ckpt8_impl(Dtype dt, bool store, const void* x, int64_t ld, int64_t rows, int64_t cols, const int8_t* q,
+                     const uint8_t* k, ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_ckpt(rows, cols, ld);
+    if (st != LN_OK) return st;
+    if (rows == 0) return LN_OK;
+    if (!x || !q || !k) return LN_EINVAL;
+    if (!ckpt_aligned(q)) return LN_EALIGN;
+    st = check_device();
+    if (st != LN_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const cudaError_t e =
+        store ? launch_ckpt8_store(dt, x, ld, rows, (int)cols, const_cast<int8_t*>(q), const_cast<uint8_t*>(k), stream)
+              : launch_ckpt8_load(dt, q, k, rows, (int)cols, const_cast<void*>(x), ld, stream);
+    return finish_call(e, e == cudaSuccess ? 1 : 0, stream);
+}
+
+ln_status ckpt_norm_impl(Dtype dt, bool rms, const void* dy, const int8_t* q, const uint8_t* k, const void* gamma,
+                         const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta, int64_t rows,
+                         int64_t cols, void* ws, size_t ws_bytes, ln_stream_t stream_) {
+    t_last_launches = 0;
+    ln_status st = check_sizes(rows, cols);
+    if (st != LN_OK) return st;
+    if (!dgamma || (!rms && !dbeta)) return LN_EINVAL;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const size_t bytes = (size_t)cols * (dt == Dtype::F32 ? 4 : 2);
+    if (rows == 0) {  // sums over no rows
+        st = check_device();
+        if (st != LN_OK) return st;
+        cudaError_t e = cudaMemsetAsync(dgamma, 0, bytes, stream);
+        if (e == cudaSuccess && !rms) e = cudaMemsetAsync(dbeta, 0, bytes, stream);
+        return finish_call(e, 0, stream);
+    }
+    if (!dy || !q || !k || !gamma || (!rms && !mean) || !rstd || !dx || !ws) return LN_EINVAL;
+    if (!ckpt_aligned(q) || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LN_EALIGN;
+    st = check_device();
+    if (st != LN_OK) return st;
+    if (ws_bytes < ckpt_norm_workspace_bytes((int)rows, (int)cols, rms, device_info(-1).sms)) return LN_ENOSPACE;
+    CkptNormArgs a;
+    a.dy = dy;
+    a.q = q;
+    a.k = k;
+    a.gamma = gamma;
+    a.mean = rms ? nullptr : mean;
+    a.rstd = rstd;
+    a.dx = dx;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.rows = (int)rows;
+    a.cols = (int)cols;
+    a.part = static_cast<float*>(ws);
+    int launches = 0;
+    const cudaError_t e = launch_ckpt_norm_bwd(dt, a, stream, &launches);
+    return finish_call(e, launches, stream);
+}
+}  // namespace
+}  // namespace lnk
+
 using lnk::Dtype;
 
 extern "C" {
@@ -955,6 +1148,91 @@ ln_status ln_dropout_bwd_keep_bf16_ws(const ln_bf16* ds, float p, const uint8_t*
     return lnk::dropout_bwd_impl<B>(Dtype::BF16, reinterpret_cast<const B*>(ds), p, 0, 0, rows,
                                     cols, reinterpret_cast<B*>(dh), reinterpret_cast<B*>(dbias),
                                     workspace, workspace_bytes, false, stream, keep);
+}
+
+ln_status ln_softmax_rel_fwd_f32(const ln_rel* r, const float* x, int64_t ldx, const float* mask, int64_t mask_rows,
+                                 float* y, int64_t ldy, int8_t* q, uint8_t* k, ln_stream_t stream) {
+    return lnk::rel_fwd_impl(Dtype::F32, r, x, ldx, mask, mask_rows, y, ldy, q, k, stream);
+}
+
+ln_status ln_softmax_rel_bwd_f32(const ln_rel* r, const float* dy, int64_t ldd, const float* y, int64_t ldy,
+                                 const int8_t* q, const uint8_t* k, float* dx, int64_t ldx, void* dtable,
+                                 void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::rel_bwd_impl(Dtype::F32, r, dy, ldd, y, ldy, q, k, dx, ldx, dtable, workspace, workspace_bytes, stream);
+}
+
+size_t ln_softmax_rel_workspace_bytes_f32(const ln_rel* r) {
+    return lnk::rel_workspace(Dtype::F32, r);
+}
+
+ln_status ln_ckpt8_store_f32(const float* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,
+                             ln_stream_t stream) {
+    return lnk::ckpt8_impl(Dtype::F32, true, x, ld, rows, cols, q, k, stream);
+}
+
+ln_status ln_ckpt8_load_f32(const int8_t* q, const uint8_t* k, int64_t rows, int64_t cols, float* x, int64_t ld,
+                            ln_stream_t stream) {
+    return lnk::ckpt8_impl(Dtype::F32, false, x, ld, rows, cols, q, k, stream);
+}
+
+ln_status ln_bwd_ckpt8_f32(const float* dy, const int8_t* q, const uint8_t* k, const float* gamma, const float* mean,
+                           const float* rstd, float* dx, float* dgamma, float* dbeta, int64_t rows, int64_t cols,
+                           void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::ckpt_norm_impl(Dtype::F32, false, dy, q, k, gamma, mean, rstd, dx, dgamma, dbeta, rows, cols, workspace,
+                               workspace_bytes, stream);
+}
+
+ln_status ln_rms_bwd_ckpt8_f32(const float* dy, const int8_t* q, const uint8_t* k, const float* gamma,
+                               const float* rrms, float* dx, float* dgamma, int64_t rows, int64_t cols,
+                               void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::ckpt_norm_impl(Dtype::F32, true, dy, q, k, gamma, nullptr, rrms, dx, dgamma, nullptr, rows, cols,
+                               workspace, workspace_bytes, stream);
+}
+
+ln_status ln_softmax_rel_fwd_bf16(const ln_rel* r, const ln_bf16* x, int64_t ldx, const ln_bf16* mask, int64_t mask_rows,
+                                 ln_bf16* y, int64_t ldy, int8_t* q, uint8_t* k, ln_stream_t stream) {
+    return lnk::rel_fwd_impl(Dtype::BF16, r, x, ldx, mask, mask_rows, y, ldy, q, k, stream);
+}
+
+ln_status ln_softmax_rel_bwd_bf16(const ln_rel* r, const ln_bf16* dy, int64_t ldd, const ln_bf16* y, int64_t ldy,
+                                 const int8_t* q, const uint8_t* k, ln_bf16* dx, int64_t ldx, void* dtable,
+                                 void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::rel_bwd_impl(Dtype::BF16, r, dy, ldd, y, ldy, q, k, dx, ldx, dtable, workspace, workspace_bytes, stream);
+}
+
+size_t ln_softmax_rel_workspace_bytes_bf16(const ln_rel* r) {
+    return lnk::rel_workspace(Dtype::BF16, r);
+}
+
+ln_status ln_ckpt8_store_bf16(const ln_bf16* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,
+                             ln_stream_t stream) {
+    return lnk::ckpt8_impl(Dtype::BF16, true, x, ld, rows, cols, q, k, stream);
+}
+
+ln_status ln_ckpt8_load_bf16(const int8_t* q, const uint8_t* k, int64_t rows, int64_t cols, ln_bf16* x, int64_t ld,
+                            ln_stream_t stream) {
+    return lnk::ckpt8_impl(Dtype::BF16, false, x, ld, rows, cols, q, k, stream);
+}
+
+ln_status ln_bwd_ckpt8_bf16(const ln_bf16* dy, const int8_t* q, const uint8_t* k, const ln_bf16* gamma, const float* mean,
+                           const float* rstd, ln_bf16* dx, ln_bf16* dgamma, ln_bf16* dbeta, int64_t rows, int64_t cols,
+                           void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::ckpt_norm_impl(Dtype::BF16, false, dy, q, k, gamma, mean, rstd, dx, dgamma, dbeta, rows, cols, workspace,
+                               workspace_bytes, stream);
+}
+
+ln_status ln_rms_bwd_ckpt8_bf16(const ln_bf16* dy, const int8_t* q, const uint8_t* k, const ln_bf16* gamma,
+                               const float* rrms, ln_bf16* dx, ln_bf16* dgamma, int64_t rows, int64_t cols,
+                               void* workspace, size_t workspace_bytes, ln_stream_t stream) {
+    return lnk::ckpt_norm_impl(Dtype::BF16, true, dy, q, k, gamma, nullptr, rrms, dx, dgamma, nullptr, rows, cols,
+                               workspace, workspace_bytes, stream);
+}
+
+size_t ln_bwd_ckpt8_workspace_bytes(int64_t rows, int64_t cols) {
+    if (lnk::check_sizes(rows, cols) != LN_OK) return 0;
+    const int dev = lnk::current_device();
+    const int sms = dev < 0 ? 0 : lnk::device_info(dev).sms;
+    return sms <= 0 ? 0 : lnk::ckpt_norm_workspace_bytes((int)rows, (int)cols, false, sms);
 }
 
 ln_status ln_device_check(ln_stream_t stream_) {

@@ -1,0 +1,80 @@
+// rel_ops.h -- host-side declarations of the softmax with a relative position bias (rel_*.cu) and of the
+// 8-bit checkpoints (ckpt8.cu, ckpt8_norm.cu).
+#pragma once
+
+#include "vocab_ops.h"
+
+namespace lnk {
+
+constexpr int kRelMaxEdges = 255;
+
+// The bias's buckets: bucket(d) for d = key - query is the number of edges at or below |d| (0 for a key behind
+// its query where `both` is false), plus edges + 1 for d > 0 where it is true.
+struct RelBuckets {
+    int n;      // edges
+    int both;
+    int edge[kRelMaxEdges];
+};
+
+struct RelArgs {
+    const void* a;            // scores (forward) or dy (backward)
+    const void* y;            // backward: probabilities, or null with q and k
+    void* out;                // y (forward) or dx (backward)
+    int64_t lda, ldy, ldo;    // elements between rows
+    int8_t* q;                // checkpoint: integers [rows, whole blocks] and bytes [rows, blocks], or null
+    uint8_t* k;
+    const void* mask;         // additive [mask_rows, Lk], or null
+    int64_t mask_rows;
+    const void* table;        // [buckets, H]
+    bool table_f32;           // fp32, or bf16
+    const int* lens;          // [B] keys of each sequence, or null
+    const int* q_pos;         // [B] position of each sequence's first query, or null
+    int B, H, Lq, Lk;
+    bool causal;
+    float scale;
+    const RelBuckets* buckets;
+    void* dtable;             // backward: [buckets, H] of the table's type, or null
+    float* part;              // its partial sums (rel_workspace_bytes)
+};
+
+// How a call's rows are cut: `chunks` of `rows` queries for each sequence and head, one block each.
+struct RelPlan {
+    int shape = 0;
+    int rows = 0;
+    int chunks = 0;
+};
+
+RelPlan rel_plan(Dtype dt, int64_t matrices, int Lq, int Lk, int sms);
+size_t rel_workspace_bytes(Dtype dt, int64_t matrices, int Lq, int Lk, int buckets, int sms);
+
+cudaError_t launch_rel_fwd_f32(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_fwd_bf16(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_bwd_f32(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_bwd_bf16(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
+// The second stage of the table's gradient.
+cudaError_t launch_rel_table(const RelArgs& a, const RelPlan& plan, cudaStream_t stream);
+
+// x [rows, cols], rows ld elements apart, to integers and bytes, and back (into rows ld apart).
+cudaError_t launch_ckpt8_store(Dtype dt, const void* x, int64_t ld, int64_t rows, int cols, int8_t* q,
+                               uint8_t* k, cudaStream_t stream);
+cudaError_t launch_ckpt8_load(Dtype dt, const int8_t* q, const uint8_t* k, int64_t rows, int cols, void* x,
+                              int64_t ld, cudaStream_t stream);
+
+// The LayerNorm's (mean given) or RMSNorm's backward from a checkpoint of its input.
+struct CkptNormArgs {
+    const void* dy;
+    const int8_t* q;
+    const uint8_t* k;
+    const void* gamma;
+    const float* mean;   // null: RMSNorm
+    const float* rstd;
+    void* dx;
+    void* dgamma;
+    void* dbeta;
+    int rows, cols;
+    float* part;         // ckpt_norm_workspace_bytes
+};
+size_t ckpt_norm_workspace_bytes(int rows, int cols, bool rms, int sms);
+cudaError_t launch_ckpt_norm_bwd(Dtype dt, const CkptNormArgs& a, cudaStream_t stream, int* launches);
+
+}  // namespace lnk

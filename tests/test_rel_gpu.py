@@ -1,0 +1,312 @@
+"""The softmax with a learned relative position bias on the GPU, against 64 bits (relref has the reference and
+where the tolerances come from)."""
+import numpy as np
+import pytest
+import torch
+
+import layernorm_ln_fwd_gb300 as ln
+import relref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def to64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rows_of(shape, dtype, g, spread=1.0, pad=0, offset=0):
+    """A CUDA tensor of that shape, rows `pad` elements wider, `offset` elements behind an aligned address."""
+    B, H, Lq, Lk = shape
+    ld = Lk + pad
+    flat = torch.randn(offset + B * H * Lq * ld, generator=g) * spread
+    return flat.to(TYPES[dtype]).cuda()[offset:].view(B, H, Lq, ld)[..., :Lk]
+
+
+class Case:
+    def __init__(self, dtype, shape, buckets=32, span=128, both=True, scale=0.7, causal=False, lens=None, q_pos=None,
+                 mask=None, table_f32=False, pad=0, offset=0, spread=2.0, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        self.dtype, self.shape, self.buckets = dtype, shape, buckets
+        self.x = rows_of(shape, dtype, g, spread, pad, offset)
+        self.dy = rows_of(shape, dtype, g, 1.0, pad, offset)
+        self.table = torch.randn(buckets, shape[1], generator=g).to(torch.float32 if table_f32 else TYPES[dtype]).cuda()
+        ints = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+        self.how = dict(max_distance=span, bidirectional=both, scale=scale, causal=causal, lens=ints(lens), q_pos=ints(q_pos))
+        self.mask = None if mask is None else mask.to(TYPES[dtype]).cuda()
+        scale = float(np.float32(scale))
+        edges = relref.edges_of(buckets, span, both)
+        self.y64, self.tol, self.bk, self.kept = relref.fwd(
+            to64(self.x), to64(self.table), edges, both, scale, causal, lens, q_pos,
+            None if mask is None else to64(self.mask))
+        self.scale = scale
+
+    def check_fwd(self, y):
+        want = self.y64
+        relref.close("y", to64(y), want, relref.stored(self.tol, want, self.dtype))
+        assert (to64(y)[~self.kept] == 0).all()
+
+    def check_bwd(self, out, y64, name=""):
+        dx, tdx, dt, tdt = relref.bwd(to64(self.dy), y64, self.bk, self.kept, self.buckets, self.scale)
+        relref.close(name + "dx", to64(out[0]), dx, relref.stored(tdx, dx, self.dtype))
+        ttype = "f32" if self.table.dtype == torch.float32 else self.dtype
+        relref.close(name + "dtable", to64(out[1]), dt, relref.stored(tdt, dt, ttype))
+        assert (to64(out[0])[~self.kept] == 0).all()
+
+    def check(self):
+        y, ck = ln.softmax_rel_fwd(self.x, self.table, mask=self.mask, ckpt=True, **self.how)
+        self.check_fwd(y)
+        plain = ln.softmax_rel_fwd(self.x, self.table, mask=self.mask, **self.how)
+        assert plain[1] is None and torch.equal(plain[0], y)
+        rows = y.reshape(-1, self.shape[3])
+        q, k, values = relref.quantise(to64(rows))
+        np.testing.assert_array_equal(ck.q.cpu().numpy(), q)
+        np.testing.assert_array_equal(ck.k.cpu().numpy(), k)
+        self.check_bwd(ln.softmax_rel_bwd(self.dy, y, self.table, **self.how), to64(y))
+        out = ln.softmax_rel_bwd(self.dy, ck, self.table, **self.how)
+        self.check_bwd(out, values.reshape(self.shape), "kept ")
+        dx, none = ln.softmax_rel_bwd(self.dy, ck, self.table, want_table=False, **self.how)
+        assert none is None and torch.equal(dx, out[0])
+
+
+SHAPES = [(1, 1, 1, 1), (2, 3, 1, 77), (2, 2, 5, 8), (1, 2, 33, 33), (2, 3, 17, 100), (1, 2, 40, 256), (1, 2, 24, 333),
+          (1, 1, 9, 513), (2, 1, 7, 1000), (1, 2, 5, 1032), (1, 2, 6, 2500), (1, 1, 3, 5001), (1, 1, 5, 8192),
+          (1, 1, 4, 16384), (2, 1, 1, 4099), (1, 3, 130, 40)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("both", [True, False])
+def test_shapes(dtype, shape, both):
+    Case(dtype, shape, both=both, seed=shape[3]).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 2, 1, 1), (2, 2, 37, 37), (1, 2, 128, 128), (1, 1, 65, 301), (1, 1, 4, 1100),
+                                   (1, 1, 300, 520)])
+def test_causal(dtype, shape):
+    Case(dtype, shape, both=False, causal=True, seed=3).check()
+    Case(dtype, shape, both=False, causal=True, q_pos=[shape[3] - shape[2]] * shape[0], seed=4).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lq,Lk", [(1, 200), (6, 200), (1, 2000), (1, 5000), (20, 61)])
+def test_sequences_of_their_own_lengths_and_positions(dtype, Lq, Lk):
+    lens = [0, 1, Lk, Lk // 2 + 1, Lk + 7, -3]
+    Case(dtype, (6, 2, Lq, Lk), lens=lens, q_pos=[max(0, n - Lq) for n in lens], both=False, seed=5).check()
+    Case(dtype, (6, 2, Lq, Lk), lens=lens, q_pos=[-Lk, -1, 3 * Lk, 2**31 - 1, -2**31, 40], seed=6).check()
+    Case(dtype, (6, 2, Lq, Lk), lens=lens, q_pos=[-Lk, -1, 3 * Lk, 2**31 - 1 - Lq, -2**31, 40], both=False, causal=True,
+         seed=7).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lk", [16385, 20000, 33001])
+def test_rows_longer_than_the_registers_hold(dtype, Lk):
+    Case(dtype, (1, 1, 2, Lk), span=800, seed=8).check()
+    Case(dtype, (2, 1, 1, Lk), both=False, lens=[Lk - 5, 3], q_pos=[Lk - 6, 2], seed=9).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("buckets,span,both", [(4, 2, True), (2, 5, False), (16, 64, True), (64, 800, False),
+                                               (256, 16384, False), (512, 16384, True), (32, 17, True), (3, 2, False)])
+def test_buckets(dtype, buckets, span, both):
+    Case(dtype, (1, 2, 70, 230), buckets, span, both, seed=10).check()
+    Case(dtype, (1, 1, 3, 6000), buckets, span, both, q_pos=[2500], seed=11).check()
+    Case(dtype, (1, 1, 1, 17001), buckets, span, both, q_pos=[16999], seed=12).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 1), (3, 5), (13, 2), (64, 7)])
+@pytest.mark.parametrize("Lk", [40, 333, 1500])
+def test_rows_at_any_distance_and_address(dtype, pad, offset, Lk):
+    c = Case(dtype, (2, 2, 5, Lk), pad=pad, offset=offset, seed=13)
+    c.check()
+    # Outputs into such rows, what lies between them left as it was.
+    whole = torch.full((2, 2, 5, Lk + 11), 7.0, dtype=TYPES[dtype], device="cuda")
+    y, _ = ln.softmax_rel_fwd(c.x, c.table, y=whole[..., 3:3 + Lk], **c.how)
+    c.check_fwd(y)
+    dx = torch.full((2, 2, 5, Lk + 11), 7.0, dtype=TYPES[dtype], device="cuda")
+    c.check_bwd(ln.softmax_rel_bwd(c.dy, y, c.table, dx=dx[..., 5:5 + Lk], **c.how), to64(y))
+    assert (whole[..., :3] == 7).all() and (whole[..., 3 + Lk:] == 7).all()
+    assert (dx[..., :5] == 7).all() and (dx[..., 5 + Lk:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 2, 9, 96), (1, 2, 7, 333), (1, 1, 3, 3001), (1, 1, 2, 17001)])
+def test_in_place(dtype, shape):
+    c = Case(dtype, shape, seed=14)
+    y, _ = ln.softmax_rel_fwd(c.x, c.table, **c.how)
+    want = ln.softmax_rel_bwd(c.dy, y, c.table, **c.how)
+    x, dy = c.x.clone(), c.dy.clone()
+    assert ln.softmax_rel_fwd(x, c.table, y=x, **c.how)[0] is x and torch.equal(x, y)
+    got = ln.softmax_rel_bwd(dy, x, c.table, dx=dy, **c.how)
+    assert got[0] is dy and torch.equal(dy, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_table_of_fp32_beside_bf16():
+    Case("bf16", (2, 3, 50, 120), table_f32=True, seed=15).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lk", [64, 77, 1500])
+def test_masks(dtype, Lk):
+    g = torch.Generator().manual_seed(16)
+    mask = torch.randn(3, Lk, generator=g)
+    mask[:, ::3] = -np.inf
+    mask[1] = -np.inf  # a row with nothing left
+    Case(dtype, (1, 2, 6, Lk), mask=mask, seed=17).check()
+    # The type's lowest value throughout: a softmax of equal scores; in half the row: nothing of that half.
+    low = torch.zeros(2, Lk)
+    low[0] = torch.finfo(TYPES[dtype]).min
+    low[1, ::2] = torch.finfo(TYPES[dtype]).min
+    c = Case(dtype, (1, 1, 4, Lk), mask=low, seed=18)
+    c.check()
+    np.testing.assert_allclose(c.y64[0, 0, 0], 1 / Lk, rtol=1e-12)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lk", [48, 99, 1200, 20001])
+def test_what_takes_no_part_is_not_used(dtype, Lk):
+    lens = [Lk - 9]
+    c = Case(dtype, (1, 2, 3, Lk), lens=lens, seed=19)
+    x, dy = c.x.clone(), c.dy.clone()
+    x[..., Lk - 9:] = float("nan")
+    dy[..., Lk - 9:] = float("inf")
+    y, ck = ln.softmax_rel_fwd(x, c.table, ckpt=True, **c.how)
+    c.check_fwd(y)
+    c.check_bwd(ln.softmax_rel_bwd(dy, y, c.table, **c.how), to64(y))
+    # A mask of -inf, whatever the score; a probability of 0, whatever dy.
+    mask = torch.zeros(1, Lk, dtype=TYPES[dtype], device="cuda")
+    mask[:, 5::7] = -float("inf")
+    how = dict(c.how, lens=None)
+    m = Case(dtype, (1, 2, 3, Lk), mask=mask.cpu(), seed=19)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        x, dy = c.x.clone(), c.dy.clone()
+        x[..., 5::7] = value
+        dy[..., 5::7] = value
+        y, ck = ln.softmax_rel_fwd(x, c.table, mask=mask, ckpt=True, **how)
+        m.check_fwd(y)
+        m.check_bwd(ln.softmax_rel_bwd(dy, y, c.table, **how), to64(y))
+        m.check_bwd(ln.softmax_rel_bwd(dy, ck, c.table, **how), to64(ln.ckpt8_load(ck, torch.float32)).reshape(m.shape))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lk", [40, 1500, 20001])
+def test_rows_that_are_not_finite(dtype, Lk):
+    c = Case(dtype, (1, 1, 4, Lk), seed=20)
+    x = c.x.clone()
+    x[0, 0, 0, 3] = float("nan")
+    x[0, 0, 1, 5] = float("inf")
+    x[0, 0, 2] = -float("inf")
+    y, ck = ln.softmax_rel_fwd(x, c.table, ckpt=True, **c.how)
+    assert y[0, 0, :2].isnan().all() and (y[0, 0, 2] == 0).all()
+    relref.close("y", to64(y)[0, 0, 3], c.y64[0, 0, 3], relref.stored(c.tol, c.y64, dtype)[0, 0, 3])
+    x[0, 0, 0] = float("nan")
+    assert ln.softmax_rel_fwd(x, c.table, **c.how)[0][0, 0, 0].isnan().all()
+    back = ln.ckpt8_load(ck, torch.float32)
+    assert back[:2].isnan().all() and (back[2] == 0).all()
+    for p in (y, ck):
+        dx, dt = ln.softmax_rel_bwd(c.dy, p, c.table, **c.how)
+        assert dx[0, 0, :2].isnan().all() and (dx[0, 0, 2] == 0).all() and dx[0, 0, 3].isfinite().all()
+
+
+def test_a_table_that_removes_a_bucket():
+    c = Case("f32", (1, 2, 20, 50), seed=21)
+    c.table[3, 0] = -float("inf")
+    y, _ = ln.softmax_rel_fwd(c.x, c.table, **c.how)
+    gone = (c.bk[0] == 3)
+    assert (to64(y)[0, 0][gone] == 0).all() and y.isfinite().all()
+    dx, dt = ln.softmax_rel_bwd(c.dy, y, c.table, **c.how)
+    assert dt[3, 0] == 0 and dt.isfinite().all()
+
+
+def test_gradients_against_differences():
+    """Central differences of the kernel's own forward in fp32: its y errs by at most `tol`, so that a quotient over
+    2 eps errs by sum |dy| tol / eps, and by eps^2 / 6 of a third derivative of at most 8 times sum |dy| y."""
+    c = Case("f32", (1, 2, 6, 23), buckets=8, span=7, scale=1.0, seed=22)
+    y, _ = ln.softmax_rel_fwd(c.x, c.table, **c.how)
+    dx, dt = ln.softmax_rel_bwd(c.dy, y, c.table, **c.how)
+    eps = 2.0 ** -7
+    dy64 = to64(c.dy)
+    noise = (np.abs(dy64) * relref.stored(c.tol, c.y64, "f32") * 1.1).sum() / eps + 8 * eps**2 / 6 * np.abs(dy64).sum()
+    for grad, t, at in [(dx, c.x, (0, 0, 2, 4)), (dx, c.x, (0, 1, 5, 22)), (dt, c.table, (0, 0)), (dt, c.table, (5, 1))]:
+        old = t[at].item()
+        ends = []
+        for step in (eps, -eps):
+            t[at] = old + step
+            ends.append((to64(ln.softmax_rel_fwd(c.x, c.table, **c.how)[0]) * dy64).sum())
+            width = t[at].item() - old if step > 0 else width - (t[at].item() - old)
+        t[at] = old
+        assert abs((ends[0] - ends[1]) / width - grad[at].item()) <= noise
+
+
+def test_no_rows():
+    table = torch.randn(32, 2).cuda()
+    for shape in ((0, 2, 4, 8), (2, 2, 0, 8)):
+        x = torch.empty(shape, device="cuda")
+        y, ck = ln.softmax_rel_fwd(x, table, ckpt=True)
+        assert y.shape == shape and ck.q.shape == (0, 32)
+        dx, dt = ln.softmax_rel_bwd(x, ck, table)
+        assert dx.shape == shape and (dt == 0).all()
+
+
+def test_bitwise_repeatable_whatever_the_workspace_holds():
+    c = Case("bf16", (3, 4, 200, 700), lens=[700, 300, 1], seed=23)
+    y, ck = ln.softmax_rel_fwd(c.x, c.table, ckpt=True, **c.how)
+    want = ln.softmax_rel_bwd(c.dy, ck, c.table, **c.how)
+    for fill in (0, 255):
+        ws = torch.full((1 << 20,), fill, dtype=torch.uint8, device="cuda")
+        got = ln.softmax_rel_bwd(c.dy, ck, c.table, workspace=ws, **c.how)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ln.LnError, match="ENOSPACE"):
+        ln.softmax_rel_bwd(c.dy, ck, c.table, workspace=ws[:256], **c.how)
+    with pytest.raises(ln.LnError, match="EALIGN"):
+        ln.softmax_rel_bwd(c.dy, ck, c.table, workspace=ws[16:], **c.how)
+
+
+def test_given_streams_and_graphs():
+    """A step captured and replayed with new inputs, another on a stream of its own meanwhile."""
+    c, d = (Case("bf16", (2, 3, 90, 161), both=False, causal=True, seed=s) for s in (24, 25))
+
+    def step(x, dy, stream=None):
+        y, ck = ln.softmax_rel_fwd(x, c.table, ckpt=True, stream=stream, **c.how)
+        return (y, *ln.softmax_rel_bwd(dy, ck, c.table, stream=stream, **c.how))
+    want_c, want_d = step(c.x, c.dy), step(d.x, d.dy)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    x, dy = c.x.clone(), c.dy.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step(x, dy)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    for inputs, want in ((c, want_c), (d, want_d), (c, want_c)):
+        x.copy_(inputs.x)
+        dy.copy_(inputs.dy)
+        graph.replay()
+        eager = step(d.x, d.dy, other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want_d))
+
+
+def test_rows_past_two_to_the_thirty_two_bytes():
+    """The last rows of a call whose scores end behind 4 GB are those of a call of their own."""
+    B, H, Lq, Lk = 9, 4, 2048, 16384 + 8
+    x = torch.empty((B, H, Lq, Lk), dtype=torch.bfloat16, device="cuda")
+    x.view(-1)[:1 << 20].normal_()
+    for b in range(B):
+        x[b] = x.view(-1)[:1 << 20].repeat(H * Lq * Lk // (1 << 20) + 1)[:H * Lq * Lk].view(H, Lq, Lk)
+    x[-1, -1, -3:].normal_()
+    table = torch.randn(32, H).bfloat16().cuda()
+    last = x[-1:, -1:, -3:].clone()
+    at = torch.tensor([Lq - 3], dtype=torch.int32, device="cuda")
+    want, kept = ln.softmax_rel_fwd(last, table[:, -1:].contiguous(), q_pos=at, ckpt=True)
+    wdx, _ = ln.softmax_rel_bwd(last, kept, table[:, -1:].contiguous(), q_pos=at)
+    y, ck = ln.softmax_rel_fwd(x, table, y=x, ckpt=True)
+    assert torch.equal(y[-1:, -1:, -3:], want) and torch.equal(ck.q[-3:], kept.q)
+    y[-1, -1, -3:] = last[0, 0]
+    dx, _ = ln.softmax_rel_bwd(y, ck, table, dx=y)
+    assert torch.equal(dx[-1:, -1:, -3:], wdx)
