@@ -453,7 +453,7 @@ ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
  *
  * y may be x itself, and dx may be dy itself, with the same ld; otherwise outputs overlap nothing.  Columns
  * Lk .. ld of a row are left as they are.  Pointers and ld need no alignment (q: 16 bytes).  Limits: Lk <=
- * LN_REL_MAX_KEYS, H <= LN_REL_MAX_HEADS, n_edges <= LN_REL_MAX_EDGES, edges <= LN_REL_MAX_SPAN, B H Lq <=
+ * LN_REL_MAX_KEYS, ld <= LN_REL_MAX_LD, H <= LN_REL_MAX_HEADS, n_edges <= LN_REL_MAX_EDGES, edges <= LN_REL_MAX_SPAN, B H Lq <=
  * LN_MAX_ROWS.  No rows: the forward does nothing, the backward zeroes dtable.
  *
  * The workspace (the backward with dtable) is the caller's, of ln_softmax_rel_workspace_bytes_* bytes; what it
@@ -465,6 +465,7 @@ ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
 #define LN_REL_MAX_HEADS 65536
 #define LN_REL_MAX_EDGES 255
 #define LN_REL_MAX_SPAN 16384
+#define LN_REL_MAX_LD (1 << 29)
 
 typedef struct ln_rel {
     int64_t B, H, Lq, Lk;

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
             n[f] = (int)min((int64_t)S, p.cols - first[f]);
             if (col < n[f]) {
                 if constexpr (STORE)
-                    u[f] = load_columns<T>(static_cast<const T*>(p.x) + row[f] * p.ld + first[f], col, n[f], p.ex);
+                    u[f] = load_columns<T>(RowIn<T>(static_cast<const T*>(p.x) + row[f] * p.ld + first[f], n[f], p.ex), col, n[f], p.ex);
                 else
                     raw[f].load(p.q + row[f] * p.ldq + first[f], p.k + row[f] * p.ldk + first[f] / kCkptBlock, col);
             }

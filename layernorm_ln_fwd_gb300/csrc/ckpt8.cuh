@@ -122,8 +122,14 @@ struct CkptRaw {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) ckpt_unpack4(w[i], step, v[2 * i], v[2 * i + 1]);
     }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+        k = 0;
+    }
     // Zeros from the count-th column on.
     __device__ __forceinline__ void first(int count) {
+        if (count <= 0) k = 0;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             const int left = count - 4 * i;

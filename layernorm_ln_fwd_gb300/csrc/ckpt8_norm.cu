@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(W * TEAMS * 32) ckpt_norm_kernel(const CnParam
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int col = column(v);
-        gm[v] = col < cols ? load_columns<T>(static_cast<const T*>(p.gamma), col, cols, p.eg) : make_uint4(0, 0, 0, 0);
+        gm[v] = col < cols ? load_columns<T>(RowIn<T>(static_cast<const T*>(p.gamma), cols, p.eg), col, cols, p.eg) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             sg[v][h] = f2_splat(0.f);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(W * TEAMS * 32) ckpt_norm_kernel(const CnParam
         for (int v = 0; v < NV; ++v) {
             const int col = column(v);
             if (col < cols) {
-                dn[v] = load_columns<T>(DY + row * cols, col, cols, p.ed);
+                dn[v] = load_columns<T>(RowIn<T>(DY + row * cols, cols, p.ed), col, cols, p.ed);
                 qn[v].load(p.q + row * blocks * kCkptBlock, p.k + row * blocks, col);
             }
         }

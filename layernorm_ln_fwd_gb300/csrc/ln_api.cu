@@ -627,10 +627,9 @@ ln_status check_rel(const ln_rel* r) {
     return LN_OK;
 }
 
-// Rows ld elements apart: they hold Lk, and a row's address stays within 63 bits of byte offset.
-bool rel_rows_ok(const ln_rel* r, int64_t ld) {
-    const int64_t rows = r->B * r->H * r->Lq;
-    return ld >= r->Lk && !(rows > 1 && ld > INT64_MAX / 4 / rows);
+// Rows ld elements apart: they hold Lk, and a distance is within 31 bits of bytes.
+ln_status check_rel_rows(const ln_rel* r, int64_t ld) {
+    return ld < r->Lk ? LN_EINVAL : ld > LN_REL_MAX_LD ? LN_EUNSUPPORTED : LN_OK;
 }
 
 bool ckpt_aligned(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
@@ -654,11 +653,11 @@ void fill_rel(const ln_rel* r, RelBuckets* bk, RelArgs* a) {
 
 int rel_buckets(const ln_rel* r) { return (r->n_edges + 1) * (r->bidirectional ? 2 : 1); }
 
-size_t rel_workspace(Dtype dt, const ln_rel* r) {
+size_t rel_workspace(const ln_rel* r) {
     if (check_rel(r) != LN_OK || r->B == 0 || r->Lq == 0) return 0;
     const int dev = current_device();
     const int sms = dev < 0 ? 0 : device_info(dev).sms;
-    return sms <= 0 ? 0 : rel_workspace_bytes(dt, r->B * r->H, (int)r->Lq, (int)r->Lk, rel_buckets(r), sms);
+    return sms <= 0 ? 0 : rel_workspace_bytes((int)r->H, rel_buckets(r), sms);
 }
 
 ln_status rel_fwd_impl(Dtype dt, const ln_rel* r, const void* x, int64_t ldx, const void* mask, int64_t mask_rows,
@@ -666,7 +665,10 @@ ln_status rel_fwd_impl(Dtype dt, const ln_rel* r, const void* x, int64_t ldx, co
     t_last_launches = 0;
     ln_status st = check_rel(r);
     if (st != LN_OK) return st;
-    if (!rel_rows_ok(r, ldx) || !rel_rows_ok(r, ldy) || (mask && mask_rows <= 0) || !q != !k) return LN_EINVAL;
+    st = check_rel_rows(r, ldx);
+    if (st == LN_OK) st = check_rel_rows(r, ldy);
+    if (st != LN_OK) return st;
+    if ((mask && mask_rows <= 0) || !q != !k) return LN_EINVAL;
     if (mask_rows > LN_MAX_ROWS) return LN_EUNSUPPORTED;
     if (r->B == 0 || r->Lq == 0) return LN_OK;
     if (!x || !y || !r->table || (x == y && ldx != ldy)) return LN_EINVAL;
@@ -685,10 +687,9 @@ ln_status rel_fwd_impl(Dtype dt, const ln_rel* r, const void* x, int64_t ldx, co
     a.k = k;
     a.mask = mask;
     a.mask_rows = mask ? mask_rows : 1;
-    const RelPlan plan = rel_plan(dt, r->B * r->H, a.Lq, a.Lk, device_info(-1).sms);
     int launches = 0;
-    const cudaError_t e = dt == Dtype::F32 ? launch_rel_fwd_f32(a, plan, stream, &launches)
-                                           : launch_rel_fwd_bf16(a, plan, stream, &launches);
+    const cudaError_t e = dt == Dtype::F32 ? launch_rel_fwd_f32(a, stream, &launches)
+                                           : launch_rel_fwd_bf16(a, stream, &launches);
     return finish_call(e, launches, stream);
 }
 
@@ -698,7 +699,11 @@ ln_status rel_bwd_impl(Dtype dt, const ln_rel* r, const void* dy, int64_t ldd, c
     t_last_launches = 0;
     ln_status st = check_rel(r);
     if (st != LN_OK) return st;
-    if (!rel_rows_ok(r, ldd) || !rel_rows_ok(r, ldx) || (y && !rel_rows_ok(r, ldy)) || !q != !k) return LN_EINVAL;
+    st = check_rel_rows(r, ldd);
+    if (st == LN_OK) st = check_rel_rows(r, ldx);
+    if (st == LN_OK && y) st = check_rel_rows(r, ldy);
+    if (st != LN_OK) return st;
+    if (!q != !k) return LN_EINVAL;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int buckets = rel_buckets(r);
     const size_t tbytes = (size_t)buckets * (size_t)r->H * (r->table_f32 ? 4 : 2);
@@ -713,7 +718,7 @@ ln_status rel_bwd_impl(Dtype dt, const ln_rel* r, const void* dy, int64_t ldd, c
     st = check_device();
     if (st != LN_OK) return st;
     const int sms = device_info(-1).sms;
-    if (dtable && ws_bytes < rel_workspace_bytes(dt, r->B * r->H, (int)r->Lq, (int)r->Lk, buckets, sms))
+    if (dtable && ws_bytes < rel_workspace_bytes((int)r->H, buckets, sms))
         return LN_ENOSPACE;
     RelBuckets bk;
     RelArgs a = {};
@@ -729,10 +734,9 @@ ln_status rel_bwd_impl(Dtype dt, const ln_rel* r, const void* dy, int64_t ldd, c
     a.mask_rows = 1;
     a.dtable = dtable;
     a.part = static_cast<float*>(ws);
-    const RelPlan plan = rel_plan(dt, r->B * r->H, a.Lq, a.Lk, sms);
     int launches = 0;
-    const cudaError_t e = dt == Dtype::F32 ? launch_rel_bwd_f32(a, plan, stream, &launches)
-                                           : launch_rel_bwd_bf16(a, plan, stream, &launches);
+    const cudaError_t e = dt == Dtype::F32 ? launch_rel_bwd_f32(a, stream, &launches)
+                                           : launch_rel_bwd_bf16(a, stream, &launches);
     return finish_call(e, launches, stream);
 }
 
@@ -1162,7 +1166,7 @@ ln_status ln_softmax_rel_bwd_f32(const ln_rel* r, const float* dy, int64_t ldd, 
 }
 
 size_t ln_softmax_rel_workspace_bytes_f32(const ln_rel* r) {
-    return lnk::rel_workspace(Dtype::F32, r);
+    return lnk::rel_workspace(r);
 }
 
 ln_status ln_ckpt8_store_f32(const float* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,
@@ -1201,7 +1205,7 @@ ln_status ln_softmax_rel_bwd_bf16(const ln_rel* r, const ln_bf16* dy, int64_t ld
 }
 
 size_t ln_softmax_rel_workspace_bytes_bf16(const ln_rel* r) {
-    return lnk::rel_workspace(Dtype::BF16, r);
+    return lnk::rel_workspace(r);
 }
 
 ln_status ln_ckpt8_store_bf16(const ln_bf16* x, int64_t ld, int64_t rows, int64_t cols, int8_t* q, uint8_t* k,

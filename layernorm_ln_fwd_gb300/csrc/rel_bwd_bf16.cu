@@ -3,8 +3,8 @@
 
 namespace lnk {
 
-cudaError_t launch_rel_bwd_bf16(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches) {
-    return launch_rel_t<__nv_bfloat16, true>(a, plan, stream, launches);
+cudaError_t launch_rel_bwd_bf16(const RelArgs& a, cudaStream_t stream, int* launches) {
+    return launch_rel_t<__nv_bfloat16, true>(a, stream, launches);
 }
 
 }  // namespace lnk

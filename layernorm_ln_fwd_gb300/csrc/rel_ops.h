@@ -37,22 +37,40 @@ struct RelArgs {
     float* part;              // its partial sums (rel_workspace_bytes)
 };
 
-// How a call's rows are cut: `chunks` of `rows` queries for each sequence and head, one block each.
-struct RelPlan {
-    int shape = 0;
-    int rows = 0;
-    int chunks = 0;
+constexpr int kRelFar = 1 << 30;  // positions are held to this: every bucket ends long before
+
+// Lanes of a row, rows of a block at a time, vectors a lane; rows of any length in tiles, twice.
+struct RelShape {
+    int lanes, teams, nv;
+    bool loop;
 };
+constexpr RelShape kRelShapes[] = {{256, 1, 1, false}, {256, 1, 2, false}, {256, 1, 4, false}, {512, 1, 4, false},
+                                   {512, 1, 4, true}, {32, 8, 1, false}, {32, 8, 2, false}, {32, 8, 4, false},
+                                   {64, 4, 4, false}, {32, 1, 2, false}, {8, 32, 1, false}, {8, 32, 2, false},
+                                   {16, 16, 2, false}, {16, 16, 4, false}};
+constexpr int kRelShapeCount = sizeof(kRelShapes) / sizeof(kRelShapes[0]);
 
-RelPlan rel_plan(Dtype dt, int64_t matrices, int Lq, int Lk, int sms);
-size_t rel_workspace_bytes(Dtype dt, int64_t matrices, int Lq, int Lk, int buckets, int sms);
+// The window in shared memory as slots (rel_softmax.cuh): how many, and groups of V entries of each.
+__host__ __device__ constexpr int rel_slot_count(int teams) { return teams > 8 ? teams : 8; }
+__host__ __device__ constexpr int rel_groups(int span, int V) { return (span - 1 + 2 * V - 1 + V - 1) / V + 1; }
+constexpr int kRelSlotBytes = 48 * 1024;  // of all slots at most
 
-cudaError_t launch_rel_fwd_f32(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
-cudaError_t launch_rel_fwd_bf16(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
-cudaError_t launch_rel_bwd_f32(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
-cudaError_t launch_rel_bwd_bf16(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches);
-// The second stage of the table's gradient.
-cudaError_t launch_rel_table(const RelArgs& a, const RelPlan& plan, cudaStream_t stream);
+constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch uses
+
+// The distances a call's window has to hold.
+void rel_span(const RelArgs& a, int* dlo, int* dhi);
+// The kernel's shape, and whether its window is in slots, for vectors of V elements.
+int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots);
+
+// Bytes of partial sums: a row of buckets for each block and head that it works on.
+size_t rel_workspace_bytes(int H, int buckets, int sms);
+
+cudaError_t launch_rel_fwd_f32(const RelArgs& a, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_fwd_bf16(const RelArgs& a, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_bwd_f32(const RelArgs& a, cudaStream_t stream, int* launches);
+cudaError_t launch_rel_bwd_bf16(const RelArgs& a, cudaStream_t stream, int* launches);
+// The second stage of the table's gradient, behind `blocks` blocks of the first.
+cudaError_t launch_rel_table(const RelArgs& a, int blocks, int64_t per_head, cudaStream_t stream);
 
 // x [rows, cols], rows ld elements apart, to integers and bytes, and back (into rows ld apart).
 cudaError_t launch_ckpt8_store(Dtype dt, const void* x, int64_t ld, int64_t rows, int cols, int8_t* q,

@@ -6,26 +6,25 @@
 // A key of lens[b] or more, or behind its query where the call is causal, takes no part, and nor does one
 // whose z is -inf: y = 0 there, and a row with nothing left is 0 throughout.
 //
-// Buckets.  Beyond the last edge every distance of a side has one bucket, so that a block needs the table
-// at a window of distances only, spread out in shared memory once for the block's queries (all of one
-// sequence and head): 2 * 91 + 1 entries for 32 buckets up to 128, whatever the row's length.  Columns
-// outside the window take its end value from a register.  The gradient goes the same way back: each
-// warp adds dS into a window of its own by distance, with loads and stores (a row meets each distance once,
-// rows follow one another), sums both far ends in registers, and the block adds the windows up and cuts them
-// into buckets at its end.  Nothing is atomic; the order of all sums is fixed by the sizes.
+// Buckets.  Beyond the last edge every distance of a side has one bucket, so that a head needs its column of the
+// table at a window of distances only (183 of them for 32 buckets up to 128), whatever the rows' length, spread
+// out in shared memory.  The gradient goes the same way back: dS is added into a window by distance with loads
+// and stores (a row meets each distance once), both far ends in registers, and a head's window is cut into buckets
+// when the block is through with the head.  Nothing is atomic; the order of all sums is fixed by the sizes.
 //
-// Entry t of a window is at t + t / V: lanes read V consecutive entries each, V apart, and the spare word
-// behind every V moves them to different banks.
-//
-// A row is held in registers by 1 to 16 warps (a team), read once and written once; what a causal row or a
-// short sequence leaves out is not read.  Rows of more columns than 16 warps hold are gone through twice.
-// Bound by memory: see the figures at the kernels.
+// Blocks.  A row is held in registers by 1 to 16 warps (a team), read once and written once; what a causal
+// row or a short sequence leaves out is not read.  The grid is one wave of resident blocks; a block has an equal,
+// contiguous share of the units (one row for each of its teams), which are ordered by head (so that a block fills
+// its window once or twice), then by query from both ends inwards (a causal row's work grows with its query:
+// neighbours average), then by sequence.  Its teams meet only where the head changes.
+// Rows of more columns than 16 warps hold are gone through twice.
 #pragma once
 
 #include <limits.h>
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "ckpt8.cuh"
 #include "rel_ops.h"
@@ -35,37 +34,28 @@ namespace lnk {
 namespace {
 
 constexpr float kRelLog2e = 1.4426950408889634f;
-constexpr int kRelFar = 1 << 30;  // positions are held to this: every bucket ends long before
 
 struct RelParams {
     const void* a;
     const void* y;
     void* out;
-    int64_t lda, ldy, ldo, ldm;
+    unsigned lda, ldy, ldo, ldm;  // bytes between rows
     int8_t* q;
     uint8_t* k;
     const void* mask;
-    int64_t mask_rows;
+    unsigned mask_rows;
     const void* table;
     int table_f32;
     const int* lens;
     const int* q_pos;
-    int H, Lq, Lk, rows, chunks, causal;
+    int B, H, Lq, Lk, causal;
+    int dlo, dhi;        // the window's distances
+    int per_matrix;      // units of a sequence and head
+    int64_t per_head, units;
     float scale;
     Extent ea, ey, em;
     float* part;
     RelBuckets bk;
-};
-
-// What a block works on.
-struct RelBlock {
-    int64_t row0;    // its first row in the call
-    int b, h;
-    int i0, i1;      // queries
-    int len;         // the sequence's keys
-    int at;          // position of the sequence's query 0
-    int dlo, dhi;    // the window's distances
-    int wlen;        // its entries: V more at either end
 };
 
 __device__ __forceinline__ int rel_bucket(const RelBuckets& bk, const int* edge, int d) {
@@ -81,53 +71,108 @@ __device__ __forceinline__ int rel_bucket(const RelBuckets& bk, const int* edge,
     return d > 0 && bk.both ? lo + bk.n + 1 : lo;
 }
 
-template <int V>
-__device__ __forceinline__ RelBlock rel_block(const RelParams& p) {
-    RelBlock r;
-    const int m = (int)blockIdx.x / p.chunks, c = (int)blockIdx.x - m * p.chunks;
-    r.b = m / p.H;
-    r.h = m - r.b * p.H;
-    r.i0 = c * p.rows;
-    r.i1 = min(p.Lq, r.i0 + p.rows);
-    r.row0 = (int64_t)m * p.Lq + r.i0;
-    r.len = p.lens ? min(max(__ldg(p.lens + r.b), 0), p.Lk) : p.Lk;
-    r.at = p.q_pos ? min(max(__ldg(p.q_pos + r.b), -kRelFar), kRelFar) : 0;
-    const int last = p.bk.n ? p.bk.edge[p.bk.n - 1] : 1;  // at least 1: d > 0 and d <= 0 have two ends
-    const int hi = p.bk.both ? last : 0;
-    r.dlo = min(max(-(r.at + r.i1 - 1), -last), hi);
-    r.dhi = min(max(p.Lk - 1 - (r.at + r.i0), r.dlo), hi);
-    r.wlen = r.dhi - r.dlo + 1 + 2 * V;
+// The distances a .. b of bucket k.
+__device__ __forceinline__ void rel_distances(const RelBuckets& bk, const int* edge, int k, int& a, int& b) {
+    const int side = bk.n + 1, j = k < side ? k : k - side;
+    const int near = j ? edge[j - 1] : 0, far = j < bk.n ? edge[j] - 1 : INT_MAX;
+    if (k < side) {
+        a = far == INT_MAX ? INT_MIN : -far;
+        b = j == 0 && !bk.both ? INT_MAX : -near;
+    } else {
+        a = max(near, 1);
+        b = far;
+    }
+}
+
+// The bias of head h at distance d.
+__device__ __forceinline__ float rel_bias(const RelParams& p, const int* edge, int h, int d) {
+    const int at = rel_bucket(p.bk, edge, d) * p.H + h;
+    return p.table_f32 ? __ldg(static_cast<const float*>(p.table) + at)
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.table)[at]);
+}
+
+// The block's units of a head, one after another: `c`-th of it is row group j (from both ends inwards)
+// of sequence b.
+struct RelWalk {
+    int j, b;
+    __device__ __forceinline__ RelWalk(const RelParams& p, int64_t c) : j((int)(c / p.B)), b((int)(c - (int64_t)j * p.B)) {}
+    __device__ __forceinline__ void next(const RelParams& p) {
+        if (++b == p.B) {
+            b = 0;
+            ++j;
+        }
+    }
+    __device__ __forceinline__ int group(const RelParams& p) const {
+        return j & 1 ? p.per_matrix - 1 - (j >> 1) : j >> 1;
+    }
+};
+
+// A team's row of a unit.  Teams take the unit's rows by their positions, so that a team meets the same
+// positions modulo TEAMS whatever q_pos is.
+struct RelRow {
+    bool ok = false;
+    int n = 0;         // keys that take part: the first n columns
+    int at = 0;        // the query's position
+    unsigned row = 0;  // in the call
+};
+
+template <int TEAMS>
+__device__ __forceinline__ RelRow rel_row(const RelParams& p, const RelWalk& w, int h, int team) {
+    RelRow r;
+    const int start = p.q_pos ? min(max(__ldg(p.q_pos + w.b), -kRelFar), kRelFar) : 0;
+    const int len = p.lens ? min(max(__ldg(p.lens + w.b), 0), p.Lk) : p.Lk;
+    const int i = w.group(p) * TEAMS + ((team - start) & (TEAMS - 1));
+    r.ok = i < p.Lq;
+    r.at = start + i;
+    r.n = r.ok ? (p.causal ? min(len, max(r.at + 1, 0)) : len) : 0;
+    r.row = (unsigned)(w.b * p.H + h) * (unsigned)p.Lq + (unsigned)i;
     return r;
 }
 
-template <int V>
-__device__ __forceinline__ int spread(int t) {
-    return t + (int)((unsigned)t / V);  // t >= 0
-}
-
-// Keys of query i that take part: the first n columns.
-__device__ __forceinline__ int rel_keys(const RelParams& p, const RelBlock& r, int i) {
-    return p.causal ? min(r.len, max(r.at + i + 1, 0)) : r.len;
+// Row `row` of a tensor whose rows are `ld` bytes apart.
+template <typename T>
+__device__ __forceinline__ T* rel_at(const void* t, unsigned row, unsigned ld) {
+    return reinterpret_cast<T*>(static_cast<char*>(const_cast<void*>(t)) + (unsigned long long)row * ld);
 }
 
 template <int W, int TEAMS>
 __device__ __forceinline__ void team_sync(int team) {
-    if constexpr (TEAMS == 1) {
+    if constexpr (TEAMS == 1)
         __syncthreads();
-    } else {
+    else
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
-    }
 }
 
+// The largest of three (one instruction of sm_100-family SMs).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Blocks an SM that the registers are to allow.
+constexpr int rel_resident(int threads, int nv, bool whole) {
+    return threads == 256 && whole ? (nv == 4 ? 3 : 4) : 1;
+}
+
+// Over groups of L lanes.
+template <int L>
 __device__ __forceinline__ float rel_warp_max(float a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
+    for (int o = L / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFullMask, a, o));
     return a;
 }
+template <int L>
 __device__ __forceinline__ float rel_warp_sum(float a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(kFullMask, a, o);
+    for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFullMask, a, o);
     return a;
+}
+
+// 1 / s to one unit in the last place (s >= 1 but for what is infinite or NaN).
+__device__ __forceinline__ float rcp_fast(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
 }
 
 // exp2((m - M) log2 e), the factor from sums taken against m to those against M >= m; 1 for a sum that
@@ -137,189 +182,348 @@ __device__ __forceinline__ float rel_factor(float m, float M) {
 }
 
 // ---------------------------------------------------------------------------------------
+// The window in shared memory.
+//
+// Slots: for windows of up to kRelSlotBytes.  A row at position p meets distance d in column d + p, so that its
+// vectors of V columns start at one residue of V throughout, and rows 8 positions apart at the same.  The window
+// is kept 8 times (a row has slot p % 8), each moved so that its rows' vectors are groups of V consecutive
+// entries: a vector is V / 4 loads of 128 bits, one after another over the lanes, at a group held between the
+// first and the last, which are the far ends' throughout.  A team's rows come every TEAMS positions, and TEAMS
+// divides 8: in the backward each slot is added to by one team alone.
+//
+// Entry t of a slot stands for distance dlo + t + residue - (2 V - 1): group 0 ends before dlo whatever the
+// residue, and the last group begins at dhi or behind.  The groups' first halves come first, then their second
+// halves (V = 8), so that 32 lanes read 512 consecutive bytes.
+//
+// One window (any size; blocks of one team): entry t, for distance dlo + t - V, is at t + t / V: lanes read V
+// consecutive entries each, V apart, and the spare word behind every V moves them to different banks.
+// ---------------------------------------------------------------------------------------
+__host__ __device__ constexpr int rel_entries(int span, int V) { return span + 2 * V; }
+__host__ __device__ constexpr int rel_spread(int t, int V) { return t + (int)((unsigned)t / (unsigned)V); }
+
+template <typename T, int SLOTS>
+struct RelWindow {
+    static constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
+    float* win;
+    int size;    // groups of a slot, or entries
+    int dlo, dhi;
+
+    __device__ __forceinline__ RelWindow(const RelParams& p, float* w)
+        : win(w), size(SLOTS ? rel_groups(p.dhi - p.dlo + 1, V) : rel_entries(p.dhi - p.dlo + 1, V)), dlo(p.dlo), dhi(p.dhi) {}
+    __device__ __forceinline__ int words() const { return SLOTS ? SLOTS * size * V : rel_spread(size - 1, V) + 1; }
+
+    // Position p's slot, the shift of its entries, and the group (entry) of its column 0.
+    __device__ __forceinline__ static int slot(int p) { return p & (SLOTS - 1); }
+    __device__ __forceinline__ int residue(int s) const { return (2 * V - 1 - dlo - s) & (V - 1); }
+    __device__ __forceinline__ int first(int p) const {
+        return SLOTS ? (2 * V - 1 - dlo - p) >> (V == 8 ? 3 : 2) : V - dlo - p;
+    }
+    // Where entry u of slot s is.
+    __device__ __forceinline__ int place(int s, int u) const {
+        return s * size * V + ((u % V / 4) * size + u / V) * 4 + u % 4;
+    }
+
+    // The bias of head h; all threads, between two barriers of the caller's.
+    __device__ void fill(const RelParams& p, const int* edge, int h, int threads) {
+        if constexpr (SLOTS) {
+            const int span = dhi - dlo + 1, per = size * V;
+            float* one = win + words();
+            for (int t = threadIdx.x; t < span; t += threads) one[t] = rel_bias(p, edge, h, dlo + t);
+            __syncthreads();
+            for (int u = threadIdx.x; u < per; u += threads)
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+                    win[place(s, u)] = one[min(max(u + residue(s) - (2 * V - 1), 0), span - 1)];
+        } else {
+            for (int t = threadIdx.x; t < size; t += threads)
+                win[rel_spread(t, V)] = rel_bias(p, edge, h, min(max(dlo + t - V, dlo), dhi));
+        }
+    }
+    __device__ void clear(int threads) {
+        for (int t = threadIdx.x; t < words(); t += threads) win[t] = 0.f;
+    }
+
+    // -1, 0, 1: the vector of column col (vector v) lies below the window, meets it, or lies above.
+    __device__ __forceinline__ int side(int first, int col) const {
+        if constexpr (SLOTS) {
+            const int g = first + col / V;
+            return g <= 0 ? -1 : g >= size - 1 ? 1 : 0;
+        } else {
+            const int t = first + col;
+            return t <= 1 ? -1 : t >= size - V ? 1 : 0;
+        }
+    }
+    __device__ __forceinline__ void read(int at, int first, int col, f2 (&b)[H]) const {
+        if constexpr (SLOTS) {
+            const float4* q = reinterpret_cast<const float4*>(win) + slot(at) * size * (V / 4) +
+                              min(max(first + col / V, 0), size - 1);
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) {
+                const float4 f = q[j * size];
+                b[2 * j] = f2_make(f.x, f.y);
+                b[2 * j + 1] = f2_make(f.z, f.w);
+            }
+        } else {
+            const int t = min(max(first + col, 0), size - V), c = t & (V - 1);
+            const float* w = win + rel_spread(t, V);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                b[h] = f2_make(w[2 * h + (c + 2 * h >= V)], w[2 * h + 1 + (c + 2 * h + 1 >= V)]);
+        }
+    }
+    // Adds a vector that meets the window.
+    __device__ __forceinline__ void add(int at, int first, int col, const f2 (&d)[H]) {
+        if constexpr (SLOTS) {
+            float4* q = reinterpret_cast<float4*>(win) + slot(at) * size * (V / 4) + first + col / V;
+            float4 f[V / 4];
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) f[j] = q[j * size];
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) {
+                const f2 a = f2_add(f2_make(f[j].x, f[j].y), d[2 * j]);
+                const f2 b = f2_add(f2_make(f[j].z, f[j].w), d[2 * j + 1]);
+                q[j * size] = make_float4(f2_lo(a), f2_hi(a), f2_lo(b), f2_hi(b));
+            }
+        } else {
+            const int t = first + col, c = t & (V - 1);
+            float* w = win + rel_spread(t, V);
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = w[e + (c + e >= V)];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                v[2 * h] += f2_lo(d[h]);
+                v[2 * h + 1] += f2_hi(d[h]);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e + (c + e >= V)] = v[e];
+        }
+    }
+    // (one window) Into the entries beyond its ends.
+    __device__ __forceinline__ void add_far(float below, float above) {
+        win[0] += below;
+        win[rel_spread(size - 1, V)] += above;
+    }
+    // What was added at distance dlo + t, at the window's ends with what is held to them.
+    __device__ __forceinline__ float sum_at(int t) const {
+        const int span = dhi - dlo + 1;
+        float sum = 0.f;
+        if constexpr (SLOTS) {
+            for (int s = 0; s < SLOTS; ++s) {
+                const int u = t + 2 * V - 1 - residue(s), last = (size - 1) * V - 1;
+                for (int e = t == 0 ? V : max(u, V); e <= (t == span - 1 ? last : min(u, last)); ++e)
+                    sum += win[place(s, e)];
+            }
+        } else {
+            for (int e = t == 0 ? 0 : t + V; e <= (t == span - 1 ? size - 1 : t + V); ++e) sum += win[rel_spread(e, V)];
+        }
+        return sum;
+    }
+};
+
+// ---------------------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------------------
 
-// The scores z of vector `col` of a row with n keys that take part: -inf elsewhere.  win: the bias's window
-// (lo, hi: its end values), t0: the entry of column 0.
-template <typename T>
-__device__ __forceinline__ void rel_scores(const uint4& raw, const T* mrow, const Extent& em, int col, int n,
-                                           int t0, int wlen, const float* win, float lo, float hi, f2 scale,
-                                           f2 (&z)[Pairs<T>::kPairs]) {
+// LPR lanes (of 1 to 16 warps, or a part of one) hold a row, NV vectors each (lane l: vectors l, l + LPR, ...);
+// TEAMS rows at a time.  WHOLE: rows of whole
+// vectors at vectors' distance, the next row's loads under way during the current one's arithmetic.  LOOP: rows
+// of any length, in tiles of that size, twice.
+template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, bool WHOLE, bool SLOTS>
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOLE)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
-    f2 x[H];
-    Pairs<T>::unpack(raw, x);
-    const int t = t0 + col;  // entries t .. t + V - 1; those below 1 and from wlen - V on are the ends
-    if (t <= 1) {
-        const f2 b = f2_splat(lo);
-#pragma unroll
-        for (int h = 0; h < H; ++h) z[h] = f2_fma(scale, x[h], b);
-    } else if (t >= wlen - V) {
-        const f2 b = f2_splat(hi);
-#pragma unroll
-        for (int h = 0; h < H; ++h) z[h] = f2_fma(scale, x[h], b);
-    } else {
-        const int c = t & (V - 1);
-        const float* w = win + spread<V>(t);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const float b0 = w[2 * h + (c + 2 * h >= V)], b1 = w[2 * h + 1 + (c + 2 * h + 1 >= V)];
-            z[h] = f2_fma(scale, x[h], f2_make(b0, b1));
-        }
-    }
-    if (mrow) {
-        f2 mv[H];
-        Pairs<T>::unpack(load_columns<T>(mrow, col, n, em), mv);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {  // a mask of -inf removes a key whatever its score is
-            const f2 s = f2_add(z[h], mv[h]);
-            z[h] = f2_make(f2_lo(mv[h]) == -INFINITY ? -INFINITY : f2_lo(s),
-                           f2_hi(mv[h]) == -INFINITY ? -INFINITY : f2_hi(s));
-        }
-    }
-    if (col + V > n) {
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-            z[h] = f2_make(col + 2 * h < n ? f2_lo(z[h]) : -INFINITY,
-                           col + 2 * h + 1 < n ? f2_hi(z[h]) : -INFINITY);
-    }
-}
-
-// y of a vector: e c, zeros from column n on, stored (and kept in 8 bits).  Called by all lanes.
-template <typename T, bool CKPT>
-__device__ __forceinline__ void rel_put(const RelParams& p, T* yrow, int8_t* qrow, uint8_t* krow, int col, int n,
-                                        const f2 (&e)[Pairs<T>::kPairs], float c) {
-    constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (col < n) {
-        f2 o[H];
-        const f2 c2 = f2_splat(c);
-#pragma unroll
-        for (int h = 0; h < H; ++h) o[h] = f2_mul(e[h], c2);
-        u = Pairs<T>::pack(o);
-        if (col + V > n) u = first_of<T>(u, n - col);
-    }
-    store_columns<T>(yrow, col, p.Lk, u);
-    if constexpr (CKPT) ckpt_keep<T>(u, col, ckpt_blocks(p.Lk) * kCkptBlock, qrow, krow);
-}
-
-// W warps hold a row, NV vectors a lane (vector (k W + w) 32 + l); TEAMS rows at a time.  LOOP: rows of any
-// length, in tiles of that size, twice.
-template <typename T, int W, int TEAMS, int NV, bool LOOP, bool CKPT>
-__global__ void __launch_bounds__(W * TEAMS * 32) rel_fwd_kernel(const __grid_constant__ RelParams p) {
-    constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
-    constexpr int kThreads = W * TEAMS * 32;
-    constexpr int kTile = W * NV * 32 * V;
-    extern __shared__ float win[];
+    constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
+    constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
+    constexpr int kTile = LPR * NV * V, kPiece = L * V;
+    static_assert(SLOTS || TEAMS == 1, "one window has one team");
+    extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][2][W];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / W, wt = warp - team * W;
+    const int tid = threadIdx.x, lane = tid & (L - 1), warp = tid >> 5;
+    const int team = tid / LPR, wt = (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
-    const RelBlock r = rel_block<V>(p);
-    __syncthreads();
-    for (int t = tid; t < r.wlen; t += kThreads) {
-        const int d = min(max(r.dlo + t - V, r.dlo), r.dhi);
-        const int at = rel_bucket(p.bk, edge, d) * p.H + r.h;
-        win[spread<V>(t)] = p.table_f32 ? __ldg(static_cast<const float*>(p.table) + at)
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.table)[at]);
-    }
-    __syncthreads();
-    const float lo = win[0], hi = win[spread<V>(r.wlen - 1)];
+    RelWindow<T, SLOTS ? rel_slot_count(TEAMS) : 0> win(p, smem);
     const f2 scale = f2_splat(p.scale), l2 = f2_splat(kRelLog2e);
-    const int padded = CKPT ? ckpt_blocks(p.Lk) * kCkptBlock : p.Lk;
+    const int blocks = ckpt_blocks(p.Lk);
+    const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
     int parity = 0;
-    for (int i = r.i0 + team; i < r.i1; i += TEAMS, parity ^= 1) {
-        const int64_t row = r.row0 + (i - r.i0);
-        const int n = rel_keys(p, r, i);
-        const T* x = static_cast<const T*>(p.a) + row * p.lda;
-        T* y = static_cast<T*>(p.out) + row * p.ldo;
-        const T* mrow = p.mask ? static_cast<const T*>(p.mask) + (row % p.mask_rows) * p.ldm : nullptr;
-        int8_t* qrow = CKPT ? p.q + row * padded : nullptr;
-        uint8_t* krow = CKPT ? p.k + row * (padded / kCkptBlock) : nullptr;
-        const int t0 = V - r.dlo - (r.at + i);  // window entry of column 0
-        f2 z[NV][H];
-        float m = -INFINITY, s = 0.f;
-        const int tiles = LOOP ? (n + kTile - 1) / kTile : 1;
-        auto scores = [&](int base) {
-            uint4 raw[NV];
+    for (int64_t unit = p.units * blockIdx.x / gridDim.x; unit < end;) {
+        const int h = (int)(unit / p.per_head);
+        const int64_t c0 = unit - (int64_t)h * p.per_head;
+        const int count = (int)(min(p.per_head, c0 + (end - unit)) - c0);
+        unit += count;
+        __syncthreads();
+        win.fill(p, edge, h, kThreads);
+        __syncthreads();
+        uint4 raw[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) raw[k] = make_uint4(0, 0, 0, 0);
+        auto load = [&](const RelRow& r, int base) {
+            const T* x = rel_at<const T>(p.a, r.row, p.lda);
+            const RowIn<T> in(x, p.Lk, p.ea);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = base + ((k * W + wt) * 32 + lane) * V;
-                if (col < n) raw[k] = load_columns<T>(x, col, n, p.ea);
-            }
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = base + ((k * W + wt) * 32 + lane) * V;
-                if (col < n) {
-                    rel_scores<T>(raw[k], mrow, p.em, col, n, t0, r.wlen, win, lo, hi, scale, z[k]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < H; ++h) z[k][h] = f2_splat(-INFINITY);
+                const int col = base + (k * LPR + wt * 32 + lane) * V;
+                if (col < r.n) {
+                    if constexpr (WHOLE)
+                        raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + col));
+                    else
+                        raw[k] = load_columns<T>(in, col, r.n, p.ea);
                 }
             }
         };
-        // z becomes exp(z - ref).
-        auto weights = [&](float ref) {
-            const f2 nr = f2_splat(-ref);
+        RelWalk walk(p, c0);
+        RelRow r = rel_row<TEAMS>(p, walk, h, team);
+        if (!LOOP) load(r, 0);
+        for (int c = 0; c < count; ++c) {
+            f2 z[NV][H];
+            const int n = r.n, first = win.first(r.at), at = r.at;
+            const int most = L < 32 ? __reduce_max_sync(kFullMask, n) : n;   // of the warp's rows
+            const int least = L < 32 ? __reduce_min_sync(kFullMask, n) : n;
+            const unsigned row = r.row;
+            const bool ok = r.ok;
+            const T* mrow = p.mask ? rel_at<const T>(p.mask, row % p.mask_rows, p.ldm) : nullptr;
+            // The scores of a tile, where the warp's 32 vectors have keys that take part (elsewhere z is
+            // left as it is, and not used): -inf at the others among them.  Returns the largest.
+            auto scores = [&](int base) {
+                float m = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+                for (int k = 0; k < NV; ++k) {
+                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    if (from >= most) continue;
+                    f2 b[H];
+                    win.read(at, first, col, b);
+                    Pairs<T>::unpack(raw[k], z[k]);
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const f2 t = f2_mul(f2_add(z[k][h], nr), l2);
-                    z[k][h] = f2_make(ex2_fast(f2_lo(t)), ex2_fast(f2_hi(t)));
+                    for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_fma(scale, z[k][h2], b[h2]);
+                    if (mrow && col < n) {
+                        f2 mv[H];
+                        if constexpr (WHOLE)
+                            Pairs<T>::unpack(ld_keep(mrow + col), mv);
+                        else
+                            Pairs<T>::unpack(load_columns<T>(RowIn<T>(mrow, p.Lk, p.em), col, n, p.em), mv);
+#pragma unroll
+                        for (int h2 = 0; h2 < H; ++h2) {  // a mask of -inf removes a key whatever its score is
+                            const f2 s = f2_add(z[k][h2], mv[h2]);
+                            z[k][h2] = f2_make(f2_lo(mv[h2]) == -INFINITY ? -INFINITY : f2_lo(s),
+                                               f2_hi(mv[h2]) == -INFINITY ? -INFINITY : f2_hi(s));
+                        }
+                    }
+                    if (from + kPiece > least) {
+                        const int left = n - col;
+#pragma unroll
+                        for (int h2 = 0; h2 < H; ++h2)
+                            z[k][h2] = f2_make(2 * h2 < left ? f2_lo(z[k][h2]) : -INFINITY,
+                                               2 * h2 + 1 < left ? f2_hi(z[k][h2]) : -INFINITY);
+                    }
+#pragma unroll
+                    for (int h2 = 0; h2 < H; ++h2) m = max3(m, f2_lo(z[k][h2]), f2_hi(z[k][h2]));
                 }
-        };
-        for (int tile = 0; tile < tiles; ++tile) {
-            scores(tile * kTile);
-            float mt = -INFINITY;
+                return m;
+            };
+            // z becomes exp(z - m); returns its sum.  exp2(z log2 e - m log2 e): the last product's rounding
+            // is the same for the whole row and cancels.  For an m whose rounding could pass fp32's exponents,
+            // z - m first.
+            auto weights = [&](float m, int base) {
+                float ref = m == -INFINITY ? 0.f : m;
+                if (!(fabsf(ref) < 16777216.f)) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+                    for (int k = 0; k < NV; ++k) {
+                        if (base + (k * LPR + wt * 32) * V >= most) continue;
 #pragma unroll
-                for (int h = 0; h < H; ++h) mt = fmaxf(mt, fmaxf(f2_lo(z[k][h]), f2_hi(z[k][h])));
-            mt = rel_warp_max(mt);
+                        for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_add(z[k][h2], f2_splat(-ref));
+                    }
+                    ref = 0.f;
+                }
+                const f2 nr = f2_splat(-ref * kRelLog2e);
+                f2 acc = f2_splat(0.f);
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    if (base + (k * LPR + wt * 32) * V >= most) continue;
+#pragma unroll
+                    for (int h2 = 0; h2 < H; ++h2) {
+                        const f2 t = f2_fma(z[k][h2], l2, nr);
+                        z[k][h2] = f2_make(ex2_fast(f2_lo(t)), ex2_fast(f2_hi(t)));
+                        acc = f2_add(acc, z[k][h2]);
+                    }
+                }
+                return f2_lo(acc) + f2_hi(acc);
+            };
+            float m = -INFINITY, s = 0.f;
             if constexpr (LOOP) {
-                mt = fmaxf(mt, m);
-                s = s * rel_factor(m, mt);
+                for (int base = 0; base < n; base += kTile) {
+                    load(r, base);
+                    const float mt = fmaxf(m, rel_warp_max<L>(scores(base)));
+                    s *= rel_factor(m, mt);
+                    m = mt;
+                    s += weights(m, base);
+                }
+            } else {
+                m = scores(0);
+                walk.next(p);
+                r = c + 1 < count ? rel_row<TEAMS>(p, walk, h, team) : RelRow();
+                if (WHOLE) load(r, 0);
+                if (L == 32 && !ok) {  // (the same in the whole team)
+                    if (!WHOLE) load(r, 0);
+                    continue;
+                }
+                m = rel_warp_max<L>(m);
+                s = weights(m, 0);
             }
-            m = mt;
-            weights(m == -INFINITY ? 0.f : m);
-            f2 acc = f2_splat(0.f);
+            s = rel_warp_sum<L>(s);
+            float inv;
+            if constexpr (W == 1) {
+                inv = s == 0.f ? 0.f : rcp_fast(s);
+            } else {  // the warps' (max, sum) meet once
+                if (lane == 0) {
+                    red[parity][team][0][wt] = m;
+                    red[parity][team][1][wt] = s;
+                }
+                team_sync<W, TEAMS>(team);
+                float M = -INFINITY, S = 0.f;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+                for (int w = 0; w < W; ++w) M = fmaxf(M, red[parity][team][0][w]);
 #pragma unroll
-                for (int h = 0; h < H; ++h) acc = f2_add(acc, z[k][h]);
-            s += f2_lo(acc) + f2_hi(acc);
-        }
-        s = rel_warp_sum(s);
-        float c;
-        if constexpr (W == 1) {
-            c = s == 0.f ? 0.f : 1.f / s;
-        } else {  // the warps' (max, sum) meet once
-            if (lane == 0) {
-                red[parity][team][0][wt] = m;
-                red[parity][team][1][wt] = s;
+                for (int w = 0; w < W; ++w) S += red[parity][team][1][w] * rel_factor(red[parity][team][0][w], M);
+                inv = S == 0.f ? 0.f : rel_factor(m, M) / S;
+                parity ^= 1;
             }
-            team_sync<W, TEAMS>(team);
-            float M = -INFINITY, S = 0.f;
+            const f2 c2 = f2_splat(inv);
+            T* y = rel_at<T>(p.out, row, p.ldo);
+            const int stored = L == 32 || ok ? p.Lk : 0;
+            for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
+                if constexpr (LOOP) {
+                    load(r, base);
+                    scores(base);
+                    weights(m, base);
+                }
 #pragma unroll
-            for (int w = 0; w < W; ++w) M = fmaxf(M, red[parity][team][0][w]);
+                for (int k = 0; k < NV; ++k) {
+                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    if (from >= p.Lk) continue;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (from < most) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) S += red[parity][team][1][w] * rel_factor(red[parity][team][0][w], M);
-            c = S == 0.f ? 0.f : rel_factor(m, M) / S;
-        }
-        const int out_tiles = LOOP ? (padded + kTile - 1) / kTile : 1;
-        for (int tile = 0; tile < out_tiles; ++tile) {
-            const int base = tile * kTile;
+                        for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_mul(z[k][h2], c2);
+                        u = Pairs<T>::pack(z[k]);
+                        if (inv != inv) u = first_of<T>(u, n - col);  // (0 times NaN)
+                    }
+                    if constexpr (WHOLE) {
+                        if (col < stored) st_stream(y + col, u);
+                    } else {
+                        store_columns<T, L>(y, col, stored, u);
+                    }
+                    if constexpr (CKPT)
+                        ckpt_keep<T>(u, col, L == 32 || ok ? blocks * kCkptBlock : 0, p.q + (unsigned long long)row * (blocks * kCkptBlock),
+                                     p.k + (unsigned long long)row * blocks);
+                }
+            }
             if constexpr (LOOP) {
-                scores(base);
-                weights(m == -INFINITY ? 0.f : m);
-            }
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int first = base + (k * W + wt) * 32 * V;
-                if (first < p.Lk) rel_put<T, CKPT>(p, y, qrow, krow, first + lane * V, n, z[k], c);
+                walk.next(p);
+                if (c + 1 < count) r = rel_row<TEAMS>(p, walk, h, team);
+            } else if (!WHOLE) {
+                load(r, 0);
             }
         }
     }
@@ -333,20 +537,14 @@ __global__ void __launch_bounds__(W * TEAMS * 32) rel_fwd_kernel(const __grid_co
 template <typename T, bool CKPT>
 struct Probs {
     uint4 u;
-    __device__ __forceinline__ void load(const RelParams& p, const T* yrow, const int8_t*, const uint8_t*, int col,
-                                         int n) {
-        u = load_columns<T>(yrow, col, n, p.ey);
-    }
+    __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void first(int count) { u = first_of<T>(u, count); }
     __device__ __forceinline__ void values(f2 (&v)[Pairs<T>::kPairs]) const { Pairs<T>::unpack(u, v); }
 };
 template <typename T>
 struct Probs<T, true> {
     CkptRaw<T> r;
-    __device__ __forceinline__ void load(const RelParams&, const T*, const int8_t* qrow, const uint8_t* krow, int col,
-                                         int) {
-        r.load(qrow, krow, col);
-    }
+    __device__ __forceinline__ void clear() { r.clear(); }
     __device__ __forceinline__ void first(int count) { r.first(count); }
     __device__ __forceinline__ void values(f2 (&v)[Pairs<T>::kPairs]) const { r.values(v); }
 };
@@ -356,234 +554,248 @@ __device__ __forceinline__ f2 where_weight(f2 y, f2 g) {
     return f2_make(f2_lo(y) == 0.f ? 0.f : f2_lo(g), f2_hi(y) == 0.f ? 0.f : f2_hi(g));
 }
 
-template <typename T, int W, int TEAMS, int NV, bool LOOP, bool CKPT>
-__global__ void __launch_bounds__(W * TEAMS * 32) rel_bwd_kernel(const __grid_constant__ RelParams p) {
+template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, bool WHOLE, bool SLOTS>
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOLE)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
-    constexpr int kThreads = W * TEAMS * 32;
-    constexpr int kTile = W * NV * 32 * V;
-    extern __shared__ float win[];
+    constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
+    constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
+    constexpr int kTile = LPR * NV * V, kPiece = L * V;
+    static_assert(SLOTS || TEAMS == 1, "one window has one team");
+    extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][W];
-    __shared__ float far_sums[W * TEAMS][2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / W, wt = warp - team * W;
+    __shared__ float far_sums[kWarps][2];
+    const int tid = threadIdx.x, lane = tid & (L - 1), warp = tid >> 5;
+    const int team = tid / LPR, wt = (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
-    const RelBlock r = rel_block<V>(p);
-    const int stride = spread<V>(r.wlen - 1) + 1;
-    float* mine = win + team * stride;
+    RelWindow<T, SLOTS ? rel_slot_count(TEAMS) : 0> win(p, smem);
     const bool sums = p.part != nullptr;
-    if (sums)
-        for (int t = tid; t < TEAMS * stride; t += kThreads) win[t] = 0.f;
-    __syncthreads();
     const f2 scale = f2_splat(p.scale);
-    f2 below = f2_splat(0.f), above = f2_splat(0.f);  // dS of the far ends
-    const int padded = ckpt_blocks(p.Lk) * kCkptBlock;
+    const int blocks = ckpt_blocks(p.Lk);
+    const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
     int parity = 0;
-    for (int i = r.i0 + team; i < r.i1; i += TEAMS) {
-        const int64_t row = r.row0 + (i - r.i0);
-        const int n = rel_keys(p, r, i);
-        const T* dy = static_cast<const T*>(p.a) + row * p.lda;
-        const T* yrow = CKPT ? nullptr : static_cast<const T*>(p.y) + row * p.ldy;
-        const int8_t* qrow = CKPT ? p.q + row * padded : nullptr;
-        const uint8_t* krow = CKPT ? p.k + row * (padded / kCkptBlock) : nullptr;
-        T* dx = static_cast<T*>(p.out) + row * p.ldo;
-        const int t0 = V - r.dlo - (r.at + i);
+    for (int64_t unit = p.units * blockIdx.x / gridDim.x; unit < end;) {
+        const int h = (int)(unit / p.per_head);
+        const int64_t c0 = unit - (int64_t)h * p.per_head;
+        const int count = (int)(min(p.per_head, c0 + (end - unit)) - c0);
+        unit += count;
+        if (sums) {
+            __syncthreads();
+            win.clear(kThreads);
+            __syncthreads();
+        }
+        f2 below = f2_splat(0.f), above = f2_splat(0.f);  // dS of the far ends
         uint4 g[NV];
         Probs<T, CKPT> pr[NV];
-        const int tiles = LOOP ? (n + kTile - 1) / kTile : 1;
-        auto load = [&](int base) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = base + ((k * W + wt) * 32 + lane) * V;
-                if (col < n) {
-                    g[k] = load_columns<T>(dy, col, n, p.ea);
-                    pr[k].load(p, yrow, qrow, krow, col, n);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = base + ((k * W + wt) * 32 + lane) * V;
-                if (col < n && col + V > n) {
-                    g[k] = first_of<T>(g[k], n - col);
-                    pr[k].first(n - col);
-                }
-            }
-        };
-        // sum dy y over the row; `careful`: without what a weight of 0 meets.
-        auto row_sum = [&](auto careful) {
-            float s = 0.f;
-            for (int tile = 0; tile < tiles; ++tile) {
-                if constexpr (LOOP) load(tile * kTile);
-                f2 acc = f2_splat(0.f);
+        for (int k = 0; k < NV; ++k) {
+            g[k] = make_uint4(0, 0, 0, 0);
+            pr[k].clear();
+        }
+        RelWalk walk(p, c0);
+        for (int c = 0; c < count; ++c, walk.next(p)) {
+            const RelRow r = rel_row<TEAMS>(p, walk, h, team);
+            if (L == 32 && !r.ok) continue;  // (the same in the whole team)
+            const int n = r.n, first = win.first(r.at);
+            const int most = L < 32 ? __reduce_max_sync(kFullMask, n) : n;   // of the warp's rows
+            const int least = L < 32 ? __reduce_min_sync(kFullMask, n) : n;
+            const int stored = L == 32 || r.ok ? p.Lk : 0;
+            const T* dy = rel_at<const T>(p.a, r.row, p.lda);
+            const T* py = rel_at<const T>(p.y, r.row, p.ldy);
+            const int8_t* pq = p.q + (unsigned long long)r.row * (blocks * kCkptBlock);
+            const uint8_t* pk = p.k + (unsigned long long)r.row * blocks;
+            T* dx = rel_at<T>(p.out, r.row, p.ldo);
+            auto load = [&](int base) {
+                const RowIn<T> in(dy, p.Lk, p.ea), iy(py, p.Lk, p.ey);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int col = tile * kTile + ((k * W + wt) * 32 + lane) * V;
-                    if (col >= n) continue;
-                    f2 d[H], y[H];
-                    Pairs<T>::unpack(g[k], d);
-                    pr[k].values(y);
-#pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        acc = f2_fma(decltype(careful)::value ? where_weight(y[h], d[h]) : d[h], y[h], acc);
-                }
-                s += f2_lo(acc) + f2_hi(acc);
-            }
-            s = rel_warp_sum(s);
-            if constexpr (W > 1) {
-                if (lane == 0) red[parity][team][wt] = s;
-                team_sync<W, TEAMS>(team);
-                s = 0.f;
-#pragma unroll
-                for (int w = 0; w < W; ++w) s += red[parity][team][w];
-                parity ^= 1;
-            }
-            return s;
-        };
-        if constexpr (!LOOP) load(0);
-        float s = row_sum(std::false_type{});
-        // A sum that is not finite (an infinite or NaN dy, perhaps at a key of weight 0, where it must
-        // not count) is formed again without such keys.
-        const bool careful = !(fabsf(s) < INFINITY);
-        if (careful) s = row_sum(std::true_type{});
-        const f2 s2 = f2_splat(s);
-        const int out_tiles = LOOP ? (p.Lk + kTile - 1) / kTile : 1;
-        for (int tile = 0; tile < out_tiles; ++tile) {
-            const int base = tile * kTile;
-            if constexpr (LOOP) load(base);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int first = base + (k * W + wt) * 32 * V, col = first + lane * V;
-                if (first >= p.Lk) continue;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (col < n) {
-                    f2 d[H], y[H], o[H];
-                    Pairs<T>::unpack(g[k], d);
-                    pr[k].values(y);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        d[h] = f2_mul(y[h], f2_sub(d[h], s2));
-                        if (careful) d[h] = where_weight(y[h], d[h]);
-                        o[h] = f2_mul(scale, d[h]);
+                    const int col = base + (k * LPR + wt * 32 + lane) * V;
+                    if (col < n) {
+                        if constexpr (WHOLE)
+                            g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + col));
+                        else
+                            g[k] = load_columns<T>(in, col, n, p.ea);
+                        if constexpr (CKPT)
+                            pr[k].r.load(pq, pk, col);
+                        else if constexpr (WHOLE)
+                            pr[k].u = __ldcs(reinterpret_cast<const uint4*>(py + col));
+                        else
+                            pr[k].u = load_columns<T>(iy, col, n, p.ey);
                     }
-                    u = Pairs<T>::pack(o);
-                    if (col + V > n) u = first_of<T>(u, n - col);
-                    if (sums) {
-                        const int t = t0 + col;
-                        if (t <= 1) {
+                }
 #pragma unroll
-                            for (int h = 0; h < H; ++h) below = f2_add(below, d[h]);
-                        } else if (t >= r.wlen - V) {
+                for (int k = 0; k < NV; ++k) {  // zeros where a key takes no part
+                    const int from = base + (k * LPR + wt * 32) * V;
+                    if (from < most && from + kPiece > least) {
+                        g[k] = first_of<T>(g[k], n - from - lane * V);
+                        pr[k].first(n - from - lane * V);
+                    }
+                }
+            };
+            // sum dy y over the row; `careful`: without what a weight of 0 meets.
+            auto row_sum = [&](auto careful) {
+                float s = 0.f;
+                for (int base = 0; base < (LOOP ? n : 1); base += kTile) {
+                    if constexpr (LOOP) load(base);
+                    f2 acc = f2_splat(0.f);
 #pragma unroll
-                            for (int h = 0; h < H; ++h) above = f2_add(above, d[h]);
-                        } else {
-                            const int c = t & (V - 1);
-                            float* w = mine + spread<V>(t);
-                            float v[V];
+                    for (int k = 0; k < NV; ++k) {
+                        if (base + (k * LPR + wt * 32) * V >= most) continue;
+                        f2 d[H], y[H];
+                        Pairs<T>::unpack(g[k], d);
+                        pr[k].values(y);
 #pragma unroll
-                            for (int e = 0; e < V; ++e) v[e] = w[e + (c + e >= V)];
+                        for (int h2 = 0; h2 < H; ++h2)
+                            acc = f2_fma(decltype(careful)::value ? where_weight(y[h2], d[h2]) : d[h2], y[h2], acc);
+                    }
+                    s += f2_lo(acc) + f2_hi(acc);
+                }
+                s = rel_warp_sum<L>(s);
+                if constexpr (W > 1) {
+                    if (lane == 0) red[parity][team][wt] = s;
+                    team_sync<W, TEAMS>(team);
+                    s = 0.f;
 #pragma unroll
-                            for (int h = 0; h < H; ++h) {
-                                v[2 * h] += f2_lo(d[h]);
-                                v[2 * h + 1] += f2_hi(d[h]);
+                    for (int w = 0; w < W; ++w) s += red[parity][team][w];
+                    parity ^= 1;
+                }
+                return s;
+            };
+            if constexpr (!LOOP) load(0);
+            float s = row_sum(std::false_type{});
+            // A sum that is not finite (an infinite or NaN dy, perhaps at a key of weight 0, where it must
+            // not count) is formed again without such keys.
+            const bool careful = L < 32 ? __any_sync(kFullMask, !(fabsf(s) < INFINITY)) : !(fabsf(s) < INFINITY);
+            if (careful) s = row_sum(std::true_type{});
+            const f2 s2 = f2_splat(s);
+            for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
+                if constexpr (LOOP) load(base);
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    if (from >= p.Lk) continue;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (from < most) {
+                        f2 d[H], y[H], o[H];
+                        Pairs<T>::unpack(g[k], d);
+                        pr[k].values(y);
+#pragma unroll
+                        for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_mul(y[h2], f2_sub(d[h2], s2));
+                        if (careful) {
+#pragma unroll
+                            for (int h2 = 0; h2 < H; ++h2) {
+                                d[h2] = where_weight(y[h2], d[h2]);
+                                d[h2] = f2_make(col + 2 * h2 < n ? f2_lo(d[h2]) : 0.f,
+                                                col + 2 * h2 + 1 < n ? f2_hi(d[h2]) : 0.f);
                             }
+                        }
 #pragma unroll
-                            for (int e = 0; e < V; ++e) w[e + (c + e >= V)] = v[e];
+                        for (int h2 = 0; h2 < H; ++h2) o[h2] = f2_mul(scale, d[h2]);
+                        u = Pairs<T>::pack(o);
+                        if (sums) {
+                            const int side = win.side(first, col);
+                            if (side == 0) {
+                                win.add(r.at, first, col, d);
+                            } else {
+                                f2 sum = f2_add(d[0], d[1]);
+#pragma unroll
+                                for (int h2 = 2; h2 < H; ++h2) sum = f2_add(sum, d[h2]);
+                                if (side < 0)
+                                    below = f2_add(below, sum);
+                                else
+                                    above = f2_add(above, sum);
+                            }
                         }
                     }
+                    if constexpr (WHOLE) {
+                        if (col < stored) st_stream(dx + col, u);
+                    } else {
+                        store_columns<T, L>(dx, col, stored, u);
+                    }
                 }
-                store_columns<T>(dx, col, p.Lk, u);
             }
+            if constexpr (W == 1) __syncwarp();  // the next row's entries are other lanes'
         }
-        if constexpr (W == 1) __syncwarp();  // the next row's entries are other lanes'
-    }
-    if (!sums) return;
-    const float fb = rel_warp_sum(f2_lo(below) + f2_hi(below)), fa = rel_warp_sum(f2_lo(above) + f2_hi(above));
-    if (lane == 0) {
-        far_sums[warp][0] = fb;
-        far_sums[warp][1] = fa;
-    }
-    __syncthreads();
-    for (int t = tid; t < r.wlen; t += kThreads) {  // the teams' windows, and the far ends into the ends
-        float v = 0.f;
-        for (int k = 0; k < TEAMS; ++k) v += win[k * stride + spread<V>(t)];
-        if (t == 0)
-            for (int w = 0; w < W * TEAMS; ++w) v += far_sums[w][0];
-        if (t == r.wlen - 1)
-            for (int w = 0; w < W * TEAMS; ++w) v += far_sums[w][1];
-        win[spread<V>(t)] = v;
-    }
-    __syncthreads();
-    const int side = p.bk.n + 1, total = side * (p.bk.both ? 2 : 1);
-    for (int k = warp; k < total; k += W * TEAMS) {
-        // The bucket's distances a .. b, then the window's entries: with an end go the entries beyond it.
-        const int j = k < side ? k : k - side;
-        const int near = j ? edge[j - 1] : 0, far = j < p.bk.n ? edge[j] - 1 : INT_MAX;
-        int a, b;
-        if (k < side) {
-            a = far == INT_MAX ? INT_MIN : -far;
-            b = j == 0 && !p.bk.both ? INT_MAX : -near;
-        } else {
-            a = max(near, 1);
-            b = far;
+        if (!sums) continue;
+        // The head is through with: its window by distance, then by bucket.
+        const float fb = rel_warp_sum<32>(f2_lo(below) + f2_hi(below)), fa = rel_warp_sum<32>(f2_lo(above) + f2_hi(above));
+        if ((tid & 31) == 0) {
+            far_sums[warp][0] = fb;
+            far_sums[warp][1] = fa;
         }
-        float v = 0.f;
-        a = max(a, r.dlo);
-        b = min(b, r.dhi);
-        if (a <= b) {
-            const int ta = a == r.dlo ? 0 : a - r.dlo + V, tb = b == r.dhi ? r.wlen - 1 : b - r.dlo + V;
-            for (int t = ta + lane; t <= tb; t += 32) v += win[spread<V>(t)];
+        __syncthreads();
+        const int span = p.dhi - p.dlo + 1;
+        float* one = smem + win.words();  // slots: their sum by distance
+        if constexpr (SLOTS) {
+            for (int t = tid; t < span; t += kThreads) {
+                float v = win.sum_at(t);
+                if (t == 0)
+                    for (int w = 0; w < kWarps; ++w) v += far_sums[w][0];
+                if (t == span - 1)
+                    for (int w = 0; w < kWarps; ++w) v += far_sums[w][1];
+                one[t] = v;
+            }
+        } else if (tid == 0) {
+            for (int w = 0; w < kWarps; ++w) win.add_far(far_sums[w][0], far_sums[w][1]);
         }
-        v = rel_warp_sum(v);
-        if (lane == 0) p.part[(int64_t)blockIdx.x * total + k] = v;
+        __syncthreads();
+        const int total = (p.bk.n + 1) * (p.bk.both ? 2 : 1);
+        float* part = p.part + ((int64_t)blockIdx.x + h) * total;
+        for (int k = warp; k < total; k += kWarps) {
+            int a, b;
+            rel_distances(p.bk, edge, k, a, b);
+            // (distances beyond the window have been added to its ends)
+            if (a < p.dlo && b >= p.dlo) a = p.dlo;
+            if (b > p.dhi && a <= p.dhi) b = p.dhi;
+            float v = 0.f;
+            if (a >= p.dlo && b <= p.dhi)
+                for (int d = a + (tid & 31); d <= b; d += 32) v += SLOTS ? one[d - p.dlo] : win.sum_at(d - p.dlo);
+            v = rel_warp_sum<32>(v);
+            if ((tid & 31) == 0) part[k] = v;
+        }
     }
 }
 
 // ---------------------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------------------
-struct RelShape {
-    int W, teams, nv;
-    bool loop;
-};
-// By capacity: 32 W nv vectors a row.
-constexpr RelShape kRelShapes[] = {{1, 8, 1, false}, {1, 8, 2, false}, {1, 8, 4, false}, {2, 4, 4, false},
-                                   {4, 2, 4, false}, {8, 1, 4, false}, {16, 1, 4, false}, {16, 1, 4, true},
-                                   {1, 1, 2, false}, {8, 1, 1, false}, {8, 1, 2, false}};
-
-template <typename T, bool BWD, bool CKPT, int W, int TEAMS, int NV, bool LOOP>
+template <typename T, bool BWD, bool CKPT, bool WHOLE, bool SLOTS, int I>
 const void* rel_kernel_of() {
-    if constexpr (BWD)
-        return (const void*)rel_bwd_kernel<T, W, TEAMS, NV, LOOP, CKPT>;
+    constexpr RelShape s = kRelShapes[I];
+    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1))
+        return nullptr;  // rows in tiles have one window, and one window one team
+    else if constexpr (BWD)
+        return (const void*)rel_bwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, WHOLE, SLOTS>;
     else
-        return (const void*)rel_fwd_kernel<T, W, TEAMS, NV, LOOP, CKPT>;
+        return (const void*)rel_fwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, WHOLE, SLOTS>;
+}
+
+template <typename T, bool BWD, bool CKPT, bool WHOLE, bool SLOTS, int... I>
+const void* rel_kernel(int shape, std::integer_sequence<int, I...>) {
+    const void* found = nullptr;
+    ((void)(shape == I && (found = rel_kernel_of<T, BWD, CKPT, WHOLE, SLOTS, I>())), ...);
+    return found;
 }
 
 template <typename T, bool BWD, bool CKPT>
-const void* rel_kernel(int shape) {
-    switch (shape) {
-        case 0: return rel_kernel_of<T, BWD, CKPT, 1, 8, 1, false>();
-        case 1: return rel_kernel_of<T, BWD, CKPT, 1, 8, 2, false>();
-        case 2: return rel_kernel_of<T, BWD, CKPT, 1, 8, 4, false>();
-        case 3: return rel_kernel_of<T, BWD, CKPT, 2, 4, 4, false>();
-        case 4: return rel_kernel_of<T, BWD, CKPT, 4, 2, 4, false>();
-        case 5: return rel_kernel_of<T, BWD, CKPT, 8, 1, 4, false>();
-        case 6: return rel_kernel_of<T, BWD, CKPT, 16, 1, 4, false>();
-        case 7: return rel_kernel_of<T, BWD, CKPT, 16, 1, 4, true>();
-        case 8: return rel_kernel_of<T, BWD, CKPT, 1, 1, 2, false>();
-        case 9: return rel_kernel_of<T, BWD, CKPT, 8, 1, 1, false>();
-        case 10: return rel_kernel_of<T, BWD, CKPT, 8, 1, 2, false>();
-        default: return nullptr;
-    }
+const void* rel_kernel(int shape, bool whole, bool slots) {
+    constexpr auto all = std::make_integer_sequence<int, kRelShapeCount>();
+    return !slots  ? rel_kernel<T, BWD, CKPT, false, false>(shape, all)
+           : whole ? rel_kernel<T, BWD, CKPT, true, true>(shape, all)
+                   : rel_kernel<T, BWD, CKPT, false, true>(shape, all);
+}
+
+// Whether rows of n elements, ld apart, are whole vectors at vectors' distance.
+template <typename T>
+bool rel_whole(const void* t, int64_t ld, int64_t n) {
+    return !t || ((reinterpret_cast<uintptr_t>(t) & 15u) == 0 && ld % Io<T>::kVec == 0 && n % Io<T>::kVec == 0);
 }
 
 template <typename T, bool BWD>
-cudaError_t launch_rel_t(const RelArgs& a, const RelPlan& plan, cudaStream_t stream, int* launches) {
+cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
     constexpr int V = Io<T>::kVec;
     *launches = 0;
-    const RelShape& sh = kRelShapes[plan.shape];
-    const bool ckpt = a.q != nullptr;
-    const void* kern = ckpt ? rel_kernel<T, BWD, true>(plan.shape) : rel_kernel<T, BWD, false>(plan.shape);
     RelParams p;
     const int64_t rows = (int64_t)a.B * a.H * a.Lq;
     auto extent = [&](const void* t, int64_t n, int64_t ld) {
@@ -593,23 +805,22 @@ cudaError_t launch_rel_t(const RelArgs& a, const RelPlan& plan, cudaStream_t str
     p.a = a.a;
     p.y = a.y;
     p.out = a.out;
-    p.lda = a.lda;
-    p.ldy = a.ldy;
-    p.ldo = a.ldo;
-    p.ldm = a.Lk;
+    p.lda = (unsigned)(a.lda * (int64_t)sizeof(T));
+    p.ldy = (unsigned)(a.ldy * (int64_t)sizeof(T));
+    p.ldo = (unsigned)(a.ldo * (int64_t)sizeof(T));
+    p.ldm = (unsigned)(a.Lk * sizeof(T));
     p.q = a.q;
     p.k = a.k;
     p.mask = a.mask;
-    p.mask_rows = a.mask_rows;
+    p.mask_rows = (unsigned)a.mask_rows;
     p.table = a.table;
     p.table_f32 = a.table_f32;
     p.lens = a.lens;
     p.q_pos = a.q_pos;
+    p.B = a.B;
     p.H = a.H;
     p.Lq = a.Lq;
     p.Lk = a.Lk;
-    p.rows = plan.rows;
-    p.chunks = plan.chunks;
     p.causal = a.causal;
     p.scale = a.scale;
     p.ea = extent(a.a, rows, a.lda);
@@ -617,21 +828,35 @@ cudaError_t launch_rel_t(const RelArgs& a, const RelPlan& plan, cudaStream_t str
     p.em = extent(a.mask, a.mask_rows, a.Lk);
     p.part = BWD && a.dtable ? a.part : nullptr;
     p.bk = *a.buckets;
-    // Distances a block can meet, or the buckets' span: whichever is less.
-    const int last = p.bk.n ? p.bk.edge[p.bk.n - 1] : 1;
-    const int64_t span = std::min<int64_t>((int64_t)last * (p.bk.both ? 2 : 1) + 1, (int64_t)a.Lk + plan.rows);
-    const int64_t entries = span + 2 * V;
-    const size_t words = (size_t)(entries + entries / V + 1) * (BWD ? (p.part ? sh.teams : 0) : 1);
+    rel_span(a, &p.dlo, &p.dhi);
+    const int span = p.dhi - p.dlo + 1;
+    const bool whole = rel_whole<T>(a.a, a.lda, a.Lk) && rel_whole<T>(a.y, a.ldy, a.Lk) &&
+                       rel_whole<T>(a.out, a.ldo, a.Lk) && rel_whole<T>(a.mask, a.Lk, a.Lk);
+    bool slots;
+    const int shape = rel_shape(V, rows, a.Lq, a.Lk, span, &slots);
+    const RelShape& sh = kRelShapes[shape];
+    p.per_matrix = (a.Lq + sh.teams - 1) / sh.teams;
+    p.per_head = (int64_t)p.per_matrix * a.B;
+    p.units = p.per_head * a.H;
+    // The forward's one copy by distance (slots), and the backward's sums by distance.
+    const size_t words = BWD && !p.part ? 0
+                         : slots        ? (size_t)rel_slot_count(sh.teams) * rel_groups(span, V) * V + span
+                                        : (size_t)rel_spread(rel_entries(span, V) - 1, V) + 1;
     const size_t smem = words * sizeof(float);
+    const bool ckpt = a.q != nullptr;
+    const void* kern = ckpt ? rel_kernel<T, BWD, true>(shape, whole, slots) : rel_kernel<T, BWD, false>(shape, whole, slots);
+    if (!kern) return cudaErrorInvalidValue;
     cudaError_t e = smem > 40 * 1024 ? allow_smem(kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
+    const int threads = sh.lanes * sh.teams;
+    const int per_sm = std::min(kRelMaxPerSm, std::max(1, blocks_per_sm(kern, threads, smem)));
+    const int grid = (int)std::min<int64_t>(p.units, (int64_t)per_sm * device_info(-1).sms);
     void* args[] = {&p};
-    e = launch_kernel(kern, dim3((unsigned)((int64_t)a.B * a.H * plan.chunks)), dim3(sh.W * sh.teams * 32), smem, stream,
-                      args, false);
+    e = launch_kernel(kern, dim3(grid), dim3(threads), smem, stream, args, false);
     if (e != cudaSuccess) return e;
     *launches = 1;
     if (p.part) {
-        e = launch_rel_table(a, plan, stream);
+        e = launch_rel_table(a, grid, p.per_head, stream);
         if (e == cudaSuccess) *launches = 2;
     }
     return e;

@@ -1,7 +1,8 @@
-// rel_table.cu -- the softmax with a relative position bias: how a call's rows are cut, and the second stage
-// of the table's gradient: each block of the backward left its dS by bucket, one row of partial sums; here
-// those of a head are added, 16 interleaved groups of rows and then the groups, in a fixed order, with the
-// rounding errors of the additions carried along (their number grows with the batch).
+// rel_table.cu -- the softmax with a relative position bias: which kernel takes a call, and the second stage of
+// the table's gradient.  Each block of the backward left its dS by bucket, a row of partial sums for each head
+// that it worked on; block k's of head h is row k + h, since either grows by one at a time along the blocks' units.
+// Here a head's rows are added: 16 interleaved groups, then the groups, in order, with the rounding errors of the
+// additions carried along.
 #include <algorithm>
 
 #include "ln_finish.cuh"
@@ -13,20 +14,23 @@ namespace {
 constexpr int kTabX = 32, kTabY = 16;
 
 template <typename T>
-__global__ void __launch_bounds__(kTabX * kTabY) rel_table_kernel(const float* part, T* dtable, int H, int B,
-                                                                  int chunks, int total) {
+__global__ void __launch_bounds__(kTabX * kTabY) rel_table_kernel(const float* part, T* dtable, int H, int blocks,
+                                                                  int64_t per_head, int total) {
     __shared__ float2 fold[kTabY][kTabX];
     pdl_enter();
     const int h = blockIdx.x, k = (int)blockIdx.y * kTabX + (int)threadIdx.x;
+    // The blocks that have units of the head: block b has those from units b / blocks on.
+    const int64_t units = per_head * H, u0 = per_head * h, u1 = u0 + per_head;
+    auto block_of = [&](int64_t u) {  // the last block that begins at unit u or before
+        int64_t b = min(u * blocks / units, (int64_t)blocks - 1);
+        while (b + 1 < blocks && units * (b + 1) / blocks <= u) ++b;
+        return (int)b;
+    };
+    const int b0 = block_of(u0), b1 = block_of(u1 - 1);
     float s = 0.f, c = 0.f;
-    if (k < total) {
-        const int64_t n = (int64_t)B * chunks;
+    if (k < total)
 #pragma unroll 4
-        for (int64_t i = threadIdx.y; i < n; i += kTabY) {
-            const int64_t b = i / chunks;
-            comp_add(s, c, part[((b * H + h) * chunks + (i - b * chunks)) * total + k], 0.f);
-        }
-    }
+        for (int b = b0 + (int)threadIdx.y; b <= b1; b += kTabY) comp_add(s, c, part[(int64_t)(b + h) * total + k], 0.f);
     fold[threadIdx.y][threadIdx.x] = make_float2(s, c);
     __syncthreads();
     if (threadIdx.y == 0 && k < total) {
@@ -38,44 +42,41 @@ __global__ void __launch_bounds__(kTabX * kTabY) rel_table_kernel(const float* p
 
 }  // namespace
 
-RelPlan rel_plan(Dtype dt, int64_t matrices, int Lq, int Lk, int sms) {
-    // Shapes of kRelShapes (rel_softmax.cuh) by the vectors of a row.
-    const int nvec = (Lk + (dt == Dtype::F32 ? 4 : 8) - 1) / (dt == Dtype::F32 ? 4 : 8);
-    RelPlan p;
-    int teams = 1;
-    if (Lq < 4 && nvec <= 512) {  // single queries: a block each, no teams to fill
-        p.shape = nvec <= 64 ? 8 : nvec <= 256 ? 9 : 10;
-    } else if (nvec <= 128) {
-        p.shape = nvec <= 32 ? 0 : nvec <= 64 ? 1 : 2;
-        teams = 8;
-    } else if (nvec <= 512) {
-        p.shape = nvec <= 256 ? 3 : 4;
-        teams = nvec <= 256 ? 4 : 2;
-    } else {
-        p.shape = nvec <= 1024 ? 5 : nvec <= 2048 ? 6 : 7;
+void rel_span(const RelArgs& a, int* dlo, int* dhi) {
+    // At least one distance on each side that has buckets of its own, so that each has its far end.
+    const int last = a.buckets->n ? a.buckets->edge[a.buckets->n - 1] : 1;
+    *dlo = -last;
+    *dhi = a.buckets->both ? last : 0;
+    if (!a.q_pos) {  // positions 0 .. Lq - 1: distances beyond these do not occur
+        *dlo = std::max(*dlo, -(a.Lq - 1));
+        *dhi = std::min(*dhi, a.Lk - 1);
     }
-    // Enough blocks to even out their ends, rows enough for a block to pay for its window.
-    int64_t rows = matrices * Lq / ((int64_t)sms * 16);
-    rows = std::min<int64_t>(std::max<int64_t>(rows, 1), 128);
-    rows = (rows + teams - 1) / teams * teams;
-    p.chunks = (int)((Lq + rows - 1) / rows);
-    p.rows = (Lq + p.chunks - 1) / p.chunks;
-    p.rows = (p.rows + teams - 1) / teams * teams;
-    p.chunks = (Lq + p.rows - 1) / p.rows;
-    return p;
 }
 
-size_t rel_workspace_bytes(Dtype dt, int64_t matrices, int Lq, int Lk, int buckets, int sms) {
-    return (size_t)matrices * (size_t)rel_plan(dt, matrices, Lq, Lk, sms).chunks * (size_t)buckets * sizeof(float);
+int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots) {
+    const int nvec = (Lk + V - 1) / V;
+    auto fits = [&](int teams) { return rel_slot_count(teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes; };
+    *slots = nvec <= 2048 && fits(8);
+    if (*slots && Lq < 4 && nvec <= 64) return 9;  // single queries: no teams to fill
+    if (*slots && Lq >= 4 && nvec <= 256) {
+        if (nvec <= 16 && fits(32)) return nvec <= 8 ? 10 : 11;
+        if (nvec <= 64 && fits(16)) return nvec <= 32 ? 12 : 13;
+        return nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : 8;
+    }
+    return nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : 4;
 }
 
-cudaError_t launch_rel_table(const RelArgs& a, const RelPlan& plan, cudaStream_t stream) {
+size_t rel_workspace_bytes(int H, int buckets, int sms) {
+    return ((size_t)kRelMaxPerSm * sms + (size_t)H) * (size_t)buckets * sizeof(float);
+}
+
+cudaError_t launch_rel_table(const RelArgs& a, int blocks, int64_t per_head, cudaStream_t stream) {
     int total = (a.buckets->n + 1) * (a.buckets->both ? 2 : 1);
     const float* part = a.part;
-    int H = a.H, B = a.B, chunks = plan.chunks;
+    int H = a.H;
     const dim3 grid(H, (total + kTabX - 1) / kTabX), block(kTabX, kTabY);
     void* out = a.dtable;
-    void* args[] = {&part, &out, &H, &B, &chunks, &total};
+    void* args[] = {&part, &out, &H, &blocks, &per_head, &total};
     const void* kern = a.table_f32 ? (const void*)rel_table_kernel<float> : (const void*)rel_table_kernel<__nv_bfloat16>;
     return launch_kernel(kern, grid, block, 0, stream, args, false);
 }

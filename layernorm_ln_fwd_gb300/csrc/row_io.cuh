@@ -80,19 +80,34 @@ __device__ __forceinline__ uint4 chunk_at(const char* c, const Extent& t) {
     return u;
 }
 
+// A row to read: whether the chunks at its ends are the tensor's as well.
+template <typename T>
+struct RowIn {
+    const T* row;
+    bool inside;
+    __device__ __forceinline__ RowIn(const T* r, int n, const Extent& t)
+        : row(r),
+          inside(reinterpret_cast<const char*>(r) - 15 >= t.lo && reinterpret_cast<const char*>(r + n) + 15 <= t.hi) {}
+};
+
 // Columns col .. col + V - 1 of a row whose first n > col columns are wanted; those behind them come
 // as anything.
 template <typename T>
-__device__ __forceinline__ uint4 load_columns(const T* row, int col, int n, const Extent& t) {
+__device__ __forceinline__ uint4 load_columns(const RowIn<T>& r, int col, int n, const Extent& t) {
     constexpr int V = Io<T>::kVec;
-    const char* p = reinterpret_cast<const char*>(row + col);
-    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
-    if (s == 0 && col + V <= n) return __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint4 a = chunk_at<T>(p - s, t);
-    if (s == 0) return a;
+    const char* p = reinterpret_cast<const char*>(r.row + col);
+    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane
+    if (s == 0 && (r.inside || col + V <= n)) return __ldcs(reinterpret_cast<const uint4*>(p));
     const int in_a = (16 - (int)s) / (int)sizeof(T);  // elements of the first chunk
-    const uint4 b = col + in_a < n ? chunk_at<T>(p - s + 16, t) : make_uint4(0, 0, 0, 0);
-    return join_at(a, b, s);
+    uint4 a, b = make_uint4(0, 0, 0, 0);
+    if (r.inside) {
+        a = *reinterpret_cast<const uint4*>(p - s);
+        if (col + in_a < n) b = *reinterpret_cast<const uint4*>(p - s + 16);
+    } else {
+        a = chunk_at<T>(p - s, t);
+        if (s != 0 && col + in_a < n) b = chunk_at<T>(p - s + 16, t);
+    }
+    return s == 0 ? a : join_at(a, b, s);
 }
 
 // One element of a vector, as it is stored.
@@ -105,14 +120,15 @@ __device__ __forceinline__ void store_element(T* p, const uint4& u, int e) {
         *reinterpret_cast<uint32_t*>(p) = w[e];
 }
 
-// A warp stores 32 vectors that follow one another: lane l has columns col .. col + V - 1, col = first +
-// l V, of a row of n columns (those of n and more are not stored; first < n).  Called by all lanes.
-template <typename T>
+// Groups of L lanes store L vectors each that follow one another: lane l of a group has columns col ..
+// col + V - 1, col = first + l V, of a row of n columns (those of n and more are not stored; rows may differ from
+// group to group).  Called by all lanes of the warp.
+template <typename T, int L = 32>
 __device__ __forceinline__ void store_columns(T* row, int col, int n, const uint4& u) {
     constexpr int V = Io<T>::kVec;
     T* p = row + col;
-    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane
-    if (s == 0) {
+    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane of a group
+    if (L == 32 ? s == 0 : __all_sync(kFullMask, s == 0)) {
         if (col + V <= n) {
             __stcs(reinterpret_cast<uint4*>(p), u);
         } else {
@@ -122,15 +138,15 @@ __device__ __forceinline__ void store_columns(T* row, int col, int n, const uint
         }
         return;
     }
-    const int lane = threadIdx.x & 31;
-    const int over = (int)s / (int)sizeof(T);  // elements of mine that belong to the next lane's chunk: over
+    const int lane = threadIdx.x & (L - 1);
+    const int over = (int)s / (int)sizeof(T);  // elements of mine that belong to the next lane's chunk
     uint4 before;
-    before.x = __shfl_up_sync(kFullMask, u.x, 1);
-    before.y = __shfl_up_sync(kFullMask, u.y, 1);
-    before.z = __shfl_up_sync(kFullMask, u.z, 1);
-    before.w = __shfl_up_sync(kFullMask, u.w, 1);
-    if (lane > 0) {  // the chunk that holds the last `over` elements before mine and my first V - over
-        const uint4 c = join_at(before, u, 16 - s);
+    before.x = __shfl_up_sync(kFullMask, u.x, 1, L);
+    before.y = __shfl_up_sync(kFullMask, u.y, 1, L);
+    before.z = __shfl_up_sync(kFullMask, u.z, 1, L);
+    before.w = __shfl_up_sync(kFullMask, u.w, 1, L);
+    if (lane > 0 || s == 0) {  // the chunk that holds the last `over` elements before mine and my first V - over
+        const uint4 c = s == 0 ? u : join_at(before, u, 16 - s);
         if (col - over + V <= n) {
             *reinterpret_cast<uint4*>(p - over) = c;
         } else {
@@ -139,10 +155,10 @@ __device__ __forceinline__ void store_columns(T* row, int col, int n, const uint
                 if (col - over + e < n) store_element(p - over + e, c, e);
         }
     }
-    // The warp's first V - over and last `over` elements lie in chunks shared with others.
+    // The group's first V - over and last `over` elements lie in chunks shared with others.
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const bool mine = (lane == 0 && e < V - over) || (lane == 31 && e >= V - over);
+        const bool mine = s != 0 && ((lane == 0 && e < V - over) || (lane == L - 1 && e >= V - over));
         if (mine && col + e < n) store_element(p + e, u, e);
     }
 }

@@ -120,7 +120,7 @@ def test_rel_fwd_arguments(lib):
         def call(r=rel, x=P, ldx=8, mask=N, mask_rows=1, y=other, ldy=8, q=N, k=N):
             return f(r and ctypes.addressof(r), x, ldx, mask, mask_rows, y, ldy, q, k, N)
         assert call(r=None) == 1 and call(x=N) == 1 and call(y=N) == 1
-        assert call(ldx=7) == 1 and call(ldy=7) == 1 and call(ldx=2**62) == 1
+        assert call(ldx=7) == 1 and call(ldy=7) == 1 and call(ldx=2**29 + 1) == 3 and call(ldy=2**62) == 3
         assert call(mask=P, mask_rows=0) == 1 and call(q=P) == 1 and call(k=P) == 1
         assert call(y=P, ldy=9) == 1  # in place, but rows elsewhere
         assert call(r=_rel(table=0)) == 1
@@ -137,6 +137,7 @@ def test_rel_bwd_arguments(lib):
             return f(r and ctypes.addressof(r), dy, ldd, y, ldy, q, k, dx, ldx, dt, ws, n, N)
         assert call(r=None) == 1 and call(dy=N) == 1 and call(y=N) == 1 and call(dx=N) == 1
         assert call(ldd=7) == 1 and call(ldy=7) == 1 and call(ldx=7) == 1
+        assert call(ldd=2**30) == 3 and call(ldy=2**30) == 3 and call(ldx=2**30) == 3
         assert call(q=P, k=P) == 1 and call(y=N, q=P) == 1  # both, or half a checkpoint
         assert call(y=N, q=ctypes.c_void_p(264), k=P) == 2
         assert call(dt=P) == 1 and call(dt=P, ws=ctypes.c_void_p(272), n=1 << 20) == 2
