@@ -25,6 +25,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -623,6 +624,41 @@ class Ckpt8(NamedTuple):
     cols: int
 
 
+_binding = None
+
+
+def _load_binding():
+    """The extension module ``_binding.so`` (csrc/binding.cpp) with the library's entry points handed over."""
+    global _binding
+    import importlib.util
+
+    import torch  # noqa: F401  (the module's symbols are torch's)
+    cdll = lib()
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m layernorm_ln_fwd_gb300.build`")
+    spec = importlib.util.spec_from_file_location("layernorm_ln_fwd_gb300._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.init({name: ctypes.cast(getattr(cdll, name), _P).value for name in SIGNATURES
+                 if "softmax_rel" in name or "ckpt8" in name})
+    _binding = module
+    return module
+
+
+def _done(name, dtype, out):
+    """A result of the extension module: an int is the status of a call that failed."""
+    if out.__class__ is int:
+        _check(name + _suffix(dtype), out)
+    return out
+
+
+def _is(t, shape, dtype, index):
+    """Whether a tensor is a contiguous one of that shape and dtype on CUDA device ``index`` (what
+    :func:`_need` asks, in a third of the time; the index of a tensor elsewhere is -1)."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
 def _new_ckpt(rows, cols, dev):
     import torch
     blocks = -(-cols // CKPT_BLOCK)
@@ -642,8 +678,11 @@ def _need_ckpt(ck, name, rows, cols, dev):
     if rows is None:
         rows = ck.q.shape[0]
     blocks = -(-cols // CKPT_BLOCK)
-    _need(ck.q, f"{name}.q", (rows, blocks * CKPT_BLOCK), torch.int8, dev)
-    _need(ck.k, f"{name}.k", (rows, blocks), torch.uint8, dev)
+    q, k = ck.q, ck.k
+    index = dev.index if dev.type == "cuda" else -1
+    if not (_is(q, (rows, blocks * CKPT_BLOCK), torch.int8, index) and _is(k, (rows, blocks), torch.uint8, index)):
+        _need(q, f"{name}.q", (rows, blocks * CKPT_BLOCK), torch.int8, dev)
+        _need(k, f"{name}.k", (rows, blocks), torch.uint8, dev)
     return ck
 
 
@@ -651,6 +690,11 @@ def ckpt8_store(x, out=None, stream=None):
     """Keeps x, [rows, cols] with contiguous rows, in 8 bits: each 32 columns of a row as integers of
     -127 .. 127 times the least power of two for which the largest rounds to at most 127 (so off by at
     most 1/127 of it).  Returns a :class:`Ckpt8` (``out``, if given)."""
+    if out is None and stream is None:
+        got = (_binding or _load_binding()).store(x)
+        if got is not None:
+            q, k = _done("ln_ckpt8_store_", x.dtype, got)
+            return Ckpt8(q, k, x.shape[1])
     rows, cols, ld = _rows_of(x, "x")
     name, fn, raw_stream = _entry("ln_ckpt8_store_", x.dtype)
     dev = x.device
@@ -666,6 +710,10 @@ def ckpt8_load(ck, dtype=None, out=None, stream=None):
     """The activation that a :class:`Ckpt8` stands for, [rows, cols] in float32 or bfloat16 (the
     default), exact in both; or written into ``out``, whose rows may be padded."""
     import torch
+    if out is None and stream is None and ck.__class__ is Ckpt8 and dtype in (None, torch.bfloat16, torch.float32):
+        got = (_binding or _load_binding()).load(ck.q, ck.k, ck.cols, dtype is torch.float32)
+        if got is not None:
+            return _done("ln_ckpt8_load_", dtype or torch.bfloat16, got)
     dev = ck.q.device if isinstance(ck, Ckpt8) else None
     _need_ckpt(ck, "ck", None, getattr(ck, "cols", 0), dev)
     rows, cols = ck.q.shape[0], ck.cols
@@ -698,12 +746,20 @@ def bwd_ckpt8(dy, ck, gamma, mean, rstd, dx=None, dgamma=None, dbeta=None, works
     """:func:`bwd` with the forward's res_out (or x) as a :class:`Ckpt8` keeps it; mean and rstd as the
     forward wrote them.  Returns (dx, dgamma, dbeta).  ``workspace``: at least
     :func:`ckpt8_workspace_bytes` bytes of any content, by default allocated for the call."""
+    if dx is dgamma is dbeta is workspace is stream is None and mean is not None and ck.__class__ is Ckpt8:
+        got = (_binding or _load_binding()).norm_bwd(dy, ck.q, ck.k, ck.cols, gamma, mean, rstd)
+        if got is not None:
+            return _done("ln_bwd_ckpt8_", dy.dtype, got)
     return _norm_bwd_ckpt8(dy, ck, gamma, mean, rstd, dx, dgamma, dbeta, workspace, stream, False)
 
 
 def rms_bwd_ckpt8(dy, ck, gamma, rrms, dx=None, dgamma=None, workspace=None, stream=None):
     """:func:`rms_bwd` with the forward's res_out (or x) as a :class:`Ckpt8` keeps it.  Returns (dx,
     dgamma); ``workspace`` as for :func:`bwd_ckpt8`."""
+    if dx is dgamma is workspace is stream is None and ck.__class__ is Ckpt8:
+        got = (_binding or _load_binding()).norm_bwd(dy, ck.q, ck.k, ck.cols, gamma, None, rrms)
+        if got is not None:
+            return _done("ln_rms_bwd_ckpt8_", dy.dtype, got)[:2]
     return _norm_bwd_ckpt8(dy, ck, gamma, None, rrms, dx, dgamma, None, workspace, stream, True)[:2]
 
 
@@ -711,34 +767,37 @@ def _norm_bwd_ckpt8(dy, ck, gamma, mean, rstd, dx, dgamma, dbeta, workspace, str
     import torch
     if dy.dim() != 2:
         raise ValueError("dy must be 2-D [rows, cols]")
-    rows, cols = dy.shape
+    shape = dy.shape
+    rows, cols = shape
     dt, dev = dy.dtype, dy.device
     name, fn, raw_stream = _entry("ln_rms_bwd_ckpt8_" if rms else "ln_bwd_ckpt8_", dt)
-    _need(dy, "dy", (rows, cols), dt, dev)
+    f32, index = torch.float32, dev.index
     _need_ckpt(ck, "ck", rows, cols, dev)
-    _need(gamma, "gamma", (cols,), dt, dev)
-    if not rms:
-        _need(mean, "mean", (rows,), torch.float32, dev)
-    _need(rstd, "rrms" if rms else "rstd", (rows,), torch.float32, dev)
-    for t, what, shape in ((dx, "dx", (rows, cols)), (dgamma, "dgamma", (cols,)), (dbeta, "dbeta", (cols,))):
-        if t is not None:
-            _need(t, what, shape, dt, dev)
+    for t, what, want, dtype in ((dy, "dy", shape, dt), (gamma, "gamma", (cols,), dt), (mean, "mean", (rows,), f32),
+                                 (rstd, "rrms" if rms else "rstd", (rows,), f32), (dx, "dx", shape, dt),
+                                 (dgamma, "dgamma", (cols,), dt), (dbeta, "dbeta", (cols,), dt)):
+        if t is None:
+            if what == "gamma" or what[0] == "r" or (what == "mean" and not rms):
+                _need(t, what, want, dtype, dev)
+        elif not _is(t, want, dtype, index):
+            _need(t, what, want, dtype, dev)
     with _on(dev, stream):
         if dx is None:
-            dx = torch.empty((rows, cols), dtype=dt, device=dev)
+            dx = torch.empty_like(dy)
         if dgamma is None:
-            dgamma = torch.empty(cols, dtype=dt, device=dev)
+            dgamma = torch.empty_like(gamma)
         if dbeta is None and not rms:
-            dbeta = torch.empty(cols, dtype=dt, device=dev)
+            dbeta = torch.empty_like(gamma)
         ws, nbytes = _workspace(workspace, lib().ln_bwd_ckpt8_workspace_bytes(rows, cols), dev)
-        head = (dy.data_ptr(), ck.q.data_ptr(), ck.k.data_ptr(), gamma.data_ptr())
-        tail = (rows, cols, ws.data_ptr(), nbytes, raw_stream(dev.index))
         if rms:
-            status = fn(*head, rstd.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), *tail)
+            status = fn(dy.data_ptr(), ck.q.data_ptr(), ck.k.data_ptr(), gamma.data_ptr(), rstd.data_ptr(),
+                        dx.data_ptr(), dgamma.data_ptr(), rows, cols, ws.data_ptr(), nbytes, raw_stream(index))
         else:
-            status = fn(*head, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
-                        *tail)
-        _check(name, status)
+            status = fn(dy.data_ptr(), ck.q.data_ptr(), ck.k.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
+                        rstd.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), rows, cols,
+                        ws.data_ptr(), nbytes, raw_stream(index))
+        if status:
+            _check(name, status)
     return dx, dgamma, dbeta
 
 
@@ -777,17 +836,18 @@ def rel_edges(buckets: int, max_distance: int = 128, bidirectional: bool = True)
     return tuple(found)
 
 
-class _Rel(ctypes.Structure):
-    """ln_rel of include/ln.h."""
-    _fields_ = [("B", _I64), ("H", _I64), ("Lq", _I64), ("Lk", _I64), ("table", _P), ("edges", _P), ("lens", _P),
-                ("q_pos", _P), ("n_edges", ctypes.c_int32), ("table_f32", ctypes.c_int32),
-                ("bidirectional", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", _F)]
+# ln_rel of include/ln.h: B, H, Lq, Lk, table, edges, lens, q_pos, n_edges, table_f32, bidirectional, causal, scale.
+_REL = struct.Struct("@4q4P4if")
 
 
 @functools.lru_cache(maxsize=256)
 def _edge_array(buckets, max_distance, bidirectional):
+    """(array, its address, its length), kept as long as its address is in use: the cache's entries go only when
+    others take their place, so the caller holds the array meanwhile."""
     edges = rel_edges(buckets, max_distance, bidirectional)
-    return (ctypes.c_int32 * len(edges))(*edges), len(edges)
+    array = (ctypes.c_int32 * len(edges))(*edges)
+    (_binding or _load_binding()).edges(buckets, max_distance, bidirectional, edges)
+    return array, ctypes.addressof(array), len(edges)
 
 
 def _rows4(t, name):
@@ -826,22 +886,28 @@ def _like4(t, name, shape, dtype, dev):
     return _rows4(t, name)[4]
 
 
-def _rel(shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dtype, dev):
+def _rel(B, H, Lq, Lk, table, max_distance, bidirectional, scale, causal, lens, q_pos, dtype, dev):
+    """(the packed ln_rel, what it points to that nobody else holds)."""
     import torch
-    B, H, Lq, Lk = shape
-    if table.dim() != 2 or table.shape[1] != H:
+    shape, ttype = table.shape, table.dtype
+    if len(shape) != 2 or shape[1] != H:
         raise ValueError(f"table must be [buckets, {H}]")
-    if table.dtype != torch.float32 and table.dtype != dtype:
-        raise TypeError(f"table has dtype {table.dtype}, expected {dtype} or torch.float32")
-    _need(table, "table", table.shape, table.dtype, dev)
-    for t, what in ((lens, "lens"), (q_pos, "q_pos")):
-        if t is not None:
-            _need(t, what, (B,), torch.int32, dev)
-    edges, n = _edge_array(table.shape[0], max_distance, bool(bidirectional))
-    rel = _Rel(B, H, Lq, Lk, table.data_ptr(), ctypes.addressof(edges), _addr(lens), _addr(q_pos), n,
-               table.dtype == torch.float32, bool(bidirectional), bool(causal), scale)
-    rel.held = edges  # as long as the call reads it
-    return rel
+    if ttype is not torch.float32 and ttype is not dtype:
+        raise TypeError(f"table has dtype {ttype}, expected {dtype} or torch.float32")
+    if table.get_device() != dev.index or not table.is_contiguous():
+        _need(table, "table", shape, ttype, dev)
+    l = p = 0
+    if lens is not None:
+        if not _is(lens, (B,), torch.int32, dev.index):
+            _need(lens, "lens", (B,), torch.int32, dev)
+        l = lens.data_ptr()
+    if q_pos is not None:
+        if not _is(q_pos, (B,), torch.int32, dev.index):
+            _need(q_pos, "q_pos", (B,), torch.int32, dev)
+        p = q_pos.data_ptr()
+    array, edges, n = _edge_array(shape[0], max_distance, bool(bidirectional))
+    return _REL.pack(B, H, Lq, Lk, table.data_ptr(), edges, l, p, n, ttype is torch.float32, bool(bidirectional),
+                     bool(causal), scale), array
 
 
 def softmax_rel_fwd(x, table, max_distance: int = 128, bidirectional: bool = True, scale: float = 1.0,
@@ -860,10 +926,16 @@ def softmax_rel_fwd(x, table, max_distance: int = 128, bidirectional: bool = Tru
     Returns (y, ck): ck is a :class:`Ckpt8` of y as [B H Lq, Lk], written in the same pass, with
     ``ckpt`` (or None), for :func:`softmax_rel_bwd`."""
     import torch
+    if y is stream is None:
+        got = (_binding or _load_binding()).rel_fwd(x, table, max_distance, bidirectional, scale, causal, lens, q_pos, mask,
+                                                    ckpt)
+        if got is not None:
+            y, q, k = _done("ln_softmax_rel_fwd_", x.dtype, got)
+            return y, Ckpt8(q, k, x.shape[3]) if ckpt else None
     B, H, Lq, Lk, ld = _rows4(x, "x")
-    name, fn, raw_stream = _entry("ln_softmax_rel_fwd_", x.dtype)
     dt, dev = x.dtype, x.device
-    rel = _rel(x.shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
+    name, fn, raw_stream = _entry("ln_softmax_rel_fwd_", dt)
+    rel, _held = _rel(B, H, Lq, Lk, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
     mask_rows = 1
     if mask is not None:
         if mask.dim() != 2:
@@ -873,10 +945,14 @@ def softmax_rel_fwd(x, table, max_distance: int = 128, bidirectional: bool = Tru
     ldy = Lk if y is None else _like4(y, "y", x.shape, dt, dev)
     with _on(dev, stream):
         if y is None:
-            y = torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
-        ck = _new_ckpt(B * H * Lq, Lk, dev) if ckpt else None
-        _check(name, fn(ctypes.addressof(rel), x.data_ptr(), ld, _addr(mask), mask_rows, y.data_ptr(), ldy,
-                        ck and ck.q.data_ptr(), ck and ck.k.data_ptr(), raw_stream(dev.index)))
+            y = torch.empty_like(x) if ld == Lk else torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
+        ck = q = k = None
+        if ckpt:
+            ck = _new_ckpt(B * H * Lq, Lk, dev)
+            q, k = ck.q.data_ptr(), ck.k.data_ptr()
+        status = fn(rel, x.data_ptr(), ld, _addr(mask), mask_rows, y.data_ptr(), ldy, q, k, raw_stream(dev.index))
+        if status:
+            _check(name, status)
     return y, ck
 
 
@@ -889,10 +965,16 @@ def softmax_rel_bwd(dy, y, table, max_distance: int = 128, bidirectional: bool =
     dy.  Returns (dx, dtable); dtable is None without ``want_table``.  ``workspace``: as many bytes as
     ``ln_softmax_rel_workspace_bytes_*`` says, of any content, by default allocated for the call."""
     import torch
+    if dx is dtable is workspace is stream is None:
+        q, k, cols = y if y.__class__ is Ckpt8 else (y, None, None)
+        got = (_binding or _load_binding()).rel_bwd(dy, q, k, cols, table, max_distance, bidirectional, scale, causal, lens,
+                                                    q_pos, want_table)
+        if got is not None:
+            return _done("ln_softmax_rel_bwd_", dy.dtype, got)
     B, H, Lq, Lk, ld = _rows4(dy, "dy")
-    name, fn, raw_stream = _entry("ln_softmax_rel_bwd_", dy.dtype)
     dt, dev = dy.dtype, dy.device
-    rel = _rel(dy.shape, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
+    name, fn, raw_stream = _entry("ln_softmax_rel_bwd_", dt)
+    rel, _held = _rel(B, H, Lq, Lk, table, max_distance, bidirectional, scale, causal, lens, q_pos, dt, dev)
     ldy, probs, q, k = Lk, None, None, None
     if isinstance(y, Ckpt8):
         _need_ckpt(y, "y", B * H * Lq, Lk, dev)
@@ -906,15 +988,16 @@ def softmax_rel_bwd(dy, y, table, max_distance: int = 128, bidirectional: bool =
         want_table = True
     with _on(dev, stream):
         if dx is None:
-            dx = torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
+            dx = torch.empty_like(dy) if ld == Lk else torch.empty((B, H, Lq, Lk), dtype=dt, device=dev)
         ws, nbytes = None, 0
         if want_table:
             if dtable is None:
-                dtable = torch.empty(table.shape, dtype=table.dtype, device=dev)
-            ws, nbytes = _workspace(workspace, _entry("ln_softmax_rel_workspace_bytes_", dt)[1](ctypes.addressof(rel)),
-                                    dev)
-        _check(name, fn(ctypes.addressof(rel), dy.data_ptr(), ld, probs, ldy, q, k, dx.data_ptr(), ldx, _addr(dtable),
-                        _addr(ws), nbytes, raw_stream(dev.index)))
+                dtable = torch.empty_like(table)
+            ws, nbytes = _workspace(workspace, _entry("ln_softmax_rel_workspace_bytes_", dt)[1](rel), dev)
+        status = fn(rel, dy.data_ptr(), ld, probs, ldy, q, k, dx.data_ptr(), ldx, _addr(dtable), _addr(ws), nbytes,
+                    raw_stream(dev.index))
+        if status:
+            _check(name, status)
     return dx, dtable
 
 

@@ -2,7 +2,8 @@
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then the objects are linked
 into ``layernorm_ln_fwd_gb300/libln.so`` (CUDA runtime linked statically).  Register and
-shared-memory usage reported by ptxas is kept in ``_build/ptxas.log``.
+shared-memory usage reported by ptxas is kept in ``_build/ptxas.log``.  Beside it ``csrc/binding.cpp``
+becomes the extension module ``_binding.so`` (g++, torch's headers).
 
 Usage: ``python -m layernorm_ln_fwd_gb300.build [--force]``.
 """
@@ -21,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libln.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -39,14 +41,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
+    return _sources() + [os.path.join(CSRC, "binding.cpp")] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(
         glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "ln.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -59,13 +61,35 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _compile_binding() -> str:
+    """The extension module, against the torch that is here; returns its temporary name."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", libs, f"-Wl,-rpath,{libs}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return tmp
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, srcs))
+        binding = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log) in results:
             f.write(f"==== {os.path.basename(obj)}\n{log}\n")
@@ -75,6 +99,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(binding, BINDING)
     if verbose:
         print(f"built {LIB}")
     return LIB

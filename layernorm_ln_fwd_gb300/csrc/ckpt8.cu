@@ -24,6 +24,43 @@ struct CkParams {
     Extent ex;
 };
 
+// Aligned rows of whole blocks that follow one another, as one: piece `at` of 32 vectors, of `cols` in all.
+template <typename T, bool STORE>
+__global__ void __launch_bounds__(kCkThreads) ckpt8_flat_kernel(const CkParams p) {
+    constexpr int V = Io<T>::kVec, S = 32 * V, F = STORE ? kCkFlight : 2 * kCkFlight;
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kCkThreads / 32);
+    const int64_t w0 = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t base = w0; base < p.total; base += warps * F) {
+        uint4 u[STORE ? F : 1];
+        CkptRaw<T> raw[STORE ? 1 : F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int64_t col = (base + f * warps) * S + lane * V;
+            if (col >= p.cols) continue;
+            if constexpr (STORE)
+                u[f] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + col));
+            else
+                raw[f].load(p.q + (col - lane * V), p.k + (col - lane * V) / kCkptBlock, lane * V);
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int64_t from = (base + f * warps) * S;
+            if (from >= p.cols) break;  // the same in the whole warp
+            const bool mine = from + lane * V < p.cols;
+            if constexpr (STORE) {
+                if (!mine) u[f] = make_uint4(0, 0, 0, 0);
+                ckpt_keep<T>(u[f], lane * V, (int)min((int64_t)S, p.cols - from), p.q + from, p.k + from / kCkptBlock);
+            } else if (mine) {
+                f2 v[Pairs<T>::kPairs];
+                raw[f].values(v);
+                st_stream(static_cast<T*>(p.out) + from + lane * V, Pairs<T>::pack(v));
+            }
+        }
+    }
+}
+
 template <typename T, bool STORE>
 __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
     constexpr int V = Io<T>::kVec, S = 32 * V;
@@ -41,7 +78,7 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
             const int64_t at = base + f * warps;
             n[f] = 0;
             if (at >= p.total) continue;
-            row[f] = p.segs == p.total ? 0 : at / p.segs;
+            row[f] = at / p.segs;
             first[f] = (at - row[f] * p.segs) * S;
             n[f] = (int)min((int64_t)S, p.cols - first[f]);
             if (col < n[f]) {
@@ -80,13 +117,15 @@ cudaError_t launch_t(CkParams p, cudaStream_t stream) {
     p.ldq = p.ldk * kCkptBlock;
     const char* base = static_cast<const char*>(p.x);
     p.ex = Extent{base, base ? base + ((p.rows - 1) * p.ld + p.cols) * (int64_t)sizeof(T) : base};
-    if (p.cols == p.ldq && p.ld == p.cols) {
+    const void* t = STORE ? p.x : p.out;
+    const bool flat = p.cols == p.ldq && p.ld == p.cols && (reinterpret_cast<uintptr_t>(t) & 15u) == 0;
+    if (flat) {
         p.cols *= p.rows;
         p.rows = 1;
     }
     p.segs = (p.cols + S - 1) / S;
     p.total = p.segs * p.rows;
-    const void* kern = (const void*)ckpt8_kernel<T, STORE>;
+    const void* kern = flat ? (const void*)ckpt8_flat_kernel<T, STORE> : (const void*)ckpt8_kernel<T, STORE>;
     const int64_t slots = (int64_t)std::max(1, blocks_per_sm(kern, kCkThreads, 0)) * device_info(-1).sms;
     const int64_t need = (p.total + kCkThreads / 32 - 1) / (kCkThreads / 32);
     void* args[] = {&p};

@@ -42,31 +42,38 @@ __device__ __forceinline__ uint32_t ckpt_pack4(f2 a, f2 b, f2 inv) {
     return __byte_perm(lo, hi, 0x5410);
 }
 
-// Four integers as the values they stand for.  q + 128 in the low byte of 2^23 is 2^23 + 128 + q.
-__device__ __forceinline__ void ckpt_unpack4(uint32_t w, f2 step, f2& a, f2& b) {
+// Four integers as floats: q + 128 in the low byte of 2^23 is 2^23 + 128 + q.
+__device__ __forceinline__ void ckpt_integers4(uint32_t w, f2& a, f2& b) {
     w ^= 0x80808080u;
     const f2 off = f2_splat(-8388736.0f);
-    const f2 p = f2_make(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
-                         __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)));
-    const f2 q = f2_make(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)),
-                         __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)));
-    a = f2_mul(f2_add(p, off), step);
-    b = f2_mul(f2_add(q, off), step);
+    a = f2_add(f2_make(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)),
+                       __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441))), off);
+    b = f2_add(f2_make(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)),
+                       __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443))), off);
 }
 
-// The largest magnitude's bits of a vector of T.
-template <typename T>
+// As the values they stand for.
+__device__ __forceinline__ void ckpt_unpack4(uint32_t w, f2 step, f2& a, f2& b) {
+    ckpt_integers4(w, a, b);
+    a = f2_mul(a, step);
+    b = f2_mul(b, step);
+}
+
+// The largest magnitude's bits over groups of LANES lanes' vectors of T (bf16: two columns of maxima at a time).
+template <typename T, int LANES>
 __device__ __forceinline__ uint32_t magnitude(const uint4& u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t m = 0;
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                              __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 2)
-            m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-        else
-            m = max(m, w[i] & 0x7fffffffu);
+        for (int o = 1; o < LANES; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, o));
+        return max(m << 16, m & 0xffff0000u);
+    } else {
+        uint32_t m = max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
+        return m;
     }
-    return m;
 }
 
 // A warp keeps 32 vectors of 16 bytes of a row: lane l has columns col .. col + V - 1 (col = first + l V,
@@ -75,10 +82,7 @@ __device__ __forceinline__ uint32_t magnitude(const uint4& u) {
 template <typename T>
 __device__ __forceinline__ void ckpt_keep(const uint4& u, int col, int past, int8_t* q, uint8_t* k) {
     constexpr int V = Io<T>::kVec;
-    uint32_t m = magnitude<T>(u);
-#pragma unroll
-    for (int o = 1; o < kCkptBlock / V; o <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
-    uint32_t byte = ckpt_byte(m);
+    uint32_t byte = ckpt_byte(magnitude<T, kCkptBlock / V>(u));
     if (col >= past) return;
     f2 v[Pairs<T>::kPairs];
     Pairs<T>::unpack(u, v);
@@ -121,6 +125,26 @@ struct CkptRaw {
         const f2 step = f2_splat(ckpt_step(k));
 #pragma unroll
         for (int i = 0; i < kWords; ++i) ckpt_unpack4(w[i], step, v[2 * i], v[2 * i + 1]);
+    }
+    // The integers, from where they start (shared memory, or global).
+    __device__ __forceinline__ void take(const void* q) {
+        if constexpr (kWords == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(q);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(q);
+        }
+    }
+    // The values plus c, each rounded once (the product is exact).
+    __device__ __forceinline__ void values(f2 (&v)[Pairs<T>::kPairs], f2 c) const {
+        const f2 step = f2_splat(ckpt_step(k));
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            ckpt_integers4(w[i], v[2 * i], v[2 * i + 1]);
+            v[2 * i] = f2_fma(v[2 * i], step, c);
+            v[2 * i + 1] = f2_fma(v[2 * i + 1], step, c);
+        }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll

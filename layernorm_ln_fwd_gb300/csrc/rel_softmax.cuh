@@ -151,7 +151,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // Blocks an SM that the registers are to allow.
 constexpr int rel_resident(int threads, int nv, bool whole) {
-    return threads == 256 && whole ? (nv == 4 ? 3 : 4) : 1;
+    return threads == 256 ? (nv == 4 ? 3 : 4) : 1;
 }
 
 // Over groups of L lanes.

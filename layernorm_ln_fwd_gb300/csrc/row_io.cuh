@@ -90,6 +90,14 @@ struct RowIn {
           inside(reinterpret_cast<const char*>(r) - 15 >= t.lo && reinterpret_cast<const char*>(r + n) + 15 <= t.hi) {}
 };
 
+// The vector of load_columns in a tensor's first or last row (a call: rare, and too large to have in line).
+template <typename T>
+__device__ __noinline__ uint4 load_at_end(const char* p, bool two, Extent t) {
+    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint4 a = chunk_at<T>(p - s, t);
+    return s == 0 ? a : join_at(a, two ? chunk_at<T>(p - s + 16, t) : make_uint4(0, 0, 0, 0), s);
+}
+
 // Columns col .. col + V - 1 of a row whose first n > col columns are wanted; those behind them come
 // as anything.
 template <typename T>
@@ -97,17 +105,11 @@ __device__ __forceinline__ uint4 load_columns(const RowIn<T>& r, int col, int n,
     constexpr int V = Io<T>::kVec;
     const char* p = reinterpret_cast<const char*>(r.row + col);
     const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane
-    if (s == 0 && (r.inside || col + V <= n)) return __ldcs(reinterpret_cast<const uint4*>(p));
-    const int in_a = (16 - (int)s) / (int)sizeof(T);  // elements of the first chunk
-    uint4 a, b = make_uint4(0, 0, 0, 0);
-    if (r.inside) {
-        a = *reinterpret_cast<const uint4*>(p - s);
-        if (col + in_a < n) b = *reinterpret_cast<const uint4*>(p - s + 16);
-    } else {
-        a = chunk_at<T>(p - s, t);
-        if (s != 0 && col + in_a < n) b = chunk_at<T>(p - s + 16, t);
-    }
-    return s == 0 ? a : join_at(a, b, s);
+    const bool two = s != 0 && col + (16 - (int)s) / (int)sizeof(T) < n;  // the second chunk has columns
+    if (!r.inside && (s != 0 || col + V > n)) return load_at_end<T>(p, two, t);
+    const uint4 a = *reinterpret_cast<const uint4*>(p - s);
+    if (s == 0) return a;
+    return join_at(a, two ? *reinterpret_cast<const uint4*>(p - s + 16) : make_uint4(0, 0, 0, 0), s);
 }
 
 // One element of a vector, as it is stored.

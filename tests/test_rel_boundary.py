@@ -85,15 +85,17 @@ def test_reference_checkpoint():
     assert (relref.quantise(np.array([[2.0 ** -126, 2.0 ** -128]]))[2] == [[2.0 ** -126, 0]]).all()
 
 
-def _rel(**over):
-    e = over.pop("edge", (1, 2, 4))
-    arr = (ctypes.c_int32 * max(len(e), 1))(*e)
-    a = dict(B=2, H=2, Lq=3, Lk=8, table=256, edges=ctypes.addressof(arr), lens=0, q_pos=0, n_edges=len(e), table_f32=0,
-             bidirectional=0, causal=0, scale=1.0)
-    a.update(over)
-    r = ln._Rel(**a)
-    r.held = arr
-    return r
+class Packed:
+    """The binding's ln_rel with some of its fields changed."""
+    names = ("B", "H", "Lq", "Lk", "table", "edges", "lens", "q_pos", "n_edges", "table_f32", "bidirectional", "causal",
+             "scale")
+
+    def __init__(self, edge=(1, 2, 4), **over):
+        self.held = (ctypes.c_int32 * max(len(edge), 1))(*edge)
+        a = dict(B=2, H=2, Lq=3, Lk=8, table=256, edges=ctypes.addressof(self.held), lens=0, q_pos=0, n_edges=len(edge),
+                 table_f32=0, bidirectional=0, causal=0, scale=1.0)
+        a.update(over)
+        self.bytes = ln._REL.pack(*(a[n] for n in self.names))
 
 
 BAD = [(dict(B=-1), 1), (dict(H=0), 1), (dict(Lq=-1), 1), (dict(Lk=0), 1), (dict(scale=float("nan")), 1),
@@ -104,37 +106,37 @@ BAD = [(dict(B=-1), 1), (dict(H=0), 1), (dict(Lq=-1), 1), (dict(Lk=0), 1), (dict
 
 @pytest.mark.parametrize("over,status", BAD)
 def test_rel_sizes(lib, over, status):
-    r = ctypes.addressof(rel := _rel(**over))
+    rel = Packed(**over)
+    r = rel.bytes
     ld = 1 << 21
     for s in ("f32", "bf16"):
         assert getattr(lib, f"ln_softmax_rel_fwd_{s}")(r, P, ld, N, 1, P, ld, N, N, N) == status
         assert getattr(lib, f"ln_softmax_rel_bwd_{s}")(r, P, ld, P, ld, N, N, P, ld, P, P, 1 << 30, N) == status
         assert getattr(lib, f"ln_softmax_rel_workspace_bytes_{s}")(r) == 0
-    del rel
 
 
 def test_rel_fwd_arguments(lib):
-    rel = _rel()
+    rel = Packed()
     other = ctypes.c_void_p(512)
     for f in (lib.ln_softmax_rel_fwd_f32, lib.ln_softmax_rel_fwd_bf16):
         def call(r=rel, x=P, ldx=8, mask=N, mask_rows=1, y=other, ldy=8, q=N, k=N):
-            return f(r and ctypes.addressof(r), x, ldx, mask, mask_rows, y, ldy, q, k, N)
+            return f(r and r.bytes, x, ldx, mask, mask_rows, y, ldy, q, k, N)
         assert call(r=None) == 1 and call(x=N) == 1 and call(y=N) == 1
         assert call(ldx=7) == 1 and call(ldy=7) == 1 and call(ldx=2**29 + 1) == 3 and call(ldy=2**62) == 3
         assert call(mask=P, mask_rows=0) == 1 and call(q=P) == 1 and call(k=P) == 1
         assert call(y=P, ldy=9) == 1  # in place, but rows elsewhere
-        assert call(r=_rel(table=0)) == 1
+        assert call(r=Packed(table=0)) == 1
         assert call(q=ctypes.c_void_p(264), k=P) == 2
-        assert call(r=_rel(B=0), x=N, y=N) == 0 and call(r=_rel(Lq=0), x=N, y=N) == 0
+        assert call(r=Packed(B=0), x=N, y=N) == 0 and call(r=Packed(Lq=0), x=N, y=N) == 0
     assert lib.ln_last_launch_count() == 0
 
 
 def test_rel_bwd_arguments(lib):
-    rel = _rel()
+    rel = Packed()
     other = ctypes.c_void_p(512)
     for f in (lib.ln_softmax_rel_bwd_f32, lib.ln_softmax_rel_bwd_bf16):
         def call(r=rel, dy=P, ldd=8, y=P, ldy=8, q=N, k=N, dx=other, ldx=8, dt=N, ws=N, n=0):
-            return f(r and ctypes.addressof(r), dy, ldd, y, ldy, q, k, dx, ldx, dt, ws, n, N)
+            return f(r and r.bytes, dy, ldd, y, ldy, q, k, dx, ldx, dt, ws, n, N)
         assert call(r=None) == 1 and call(dy=N) == 1 and call(y=N) == 1 and call(dx=N) == 1
         assert call(ldd=7) == 1 and call(ldy=7) == 1 and call(ldx=7) == 1
         assert call(ldd=2**30) == 3 and call(ldy=2**30) == 3 and call(ldx=2**30) == 3
@@ -142,7 +144,7 @@ def test_rel_bwd_arguments(lib):
         assert call(y=N, q=ctypes.c_void_p(264), k=P) == 2
         assert call(dt=P) == 1 and call(dt=P, ws=ctypes.c_void_p(272), n=1 << 20) == 2
         assert call(dx=P, ldx=9) == 1
-        assert call(r=_rel(B=0), dy=N, y=N, dx=N) == 0
+        assert call(r=Packed(B=0), dy=N, y=N, dx=N) == 0
     assert lib.ln_last_launch_count() == 0
 
 
