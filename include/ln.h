@@ -459,7 +459,8 @@ ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
  * The workspace (the backward with dtable) is the caller's, of ln_softmax_rel_workspace_bytes_* bytes; what it
  * holds before and after a call is of no account, and calls that may overlap need one each.  Nothing is
  * allocated, nothing is atomic, and no kernel waits for another block: results are bitwise repeatable for the same
- * sizes on devices of as many SMs.
+ * sizes, the same outputs asked for and the same addresses modulo 16, on devices of as many SMs (rows are cut at 16
+ * bytes, and split by their number).
  */
 #define LN_REL_MAX_KEYS (1 << 20)
 #define LN_REL_MAX_HEADS 65536

@@ -54,6 +54,7 @@ constexpr int kRelShapeCount = sizeof(kRelShapes) / sizeof(kRelShapes[0]);
 __host__ __device__ constexpr int rel_slot_count(int teams) { return teams > 8 ? teams : 8; }
 __host__ __device__ constexpr int rel_groups(int span, int V) { return (span - 1 + 2 * V - 1 + V - 1) / V + 1; }
 constexpr int kRelSlotBytes = 48 * 1024;  // of all slots at most
+constexpr int kRelShiftedBytes = 64 * 1024;  // in the backward of shifted rows, with slots for each team
 
 constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch uses
 
@@ -61,6 +62,9 @@ constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch u
 void rel_span(const RelArgs& a, int* dlo, int* dhi);
 // The kernel's shape, and whether its window is in slots, for vectors of V elements.
 int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots);
+
+// The shape for shifted rows and the slots that it has, or -1.
+int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies);
 
 // Bytes of partial sums: a row of buckets for each block and head that it works on.
 size_t rel_workspace_bytes(int H, int buckets, int sms);

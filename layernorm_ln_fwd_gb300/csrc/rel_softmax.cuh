@@ -135,6 +135,12 @@ __device__ __forceinline__ T* rel_at(const void* t, unsigned row, unsigned ld) {
     return reinterpret_cast<T*>(static_cast<char*>(const_cast<void*>(t)) + (unsigned long long)row * ld);
 }
 
+// Elements between the last 16-byte boundary and a row's start.
+template <typename T>
+__device__ __forceinline__ int rel_shift(const T* row) {
+    return (int)((unsigned)reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
+}
+
 template <int W, int TEAMS>
 __device__ __forceinline__ void team_sync(int team) {
     if constexpr (TEAMS == 1)
@@ -150,7 +156,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 // Blocks an SM that the registers are to allow.
-constexpr int rel_resident(int threads, int nv, bool whole) {
+constexpr int rel_resident(int threads, int nv) {
     return threads == 256 ? (nv == 4 ? 3 : 4) : 1;
 }
 
@@ -167,6 +173,12 @@ __device__ __forceinline__ float rel_warp_sum(float a) {
     for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFullMask, a, o);
     return a;
 }
+
+// How rows lie.  kRelWhole: at multiples of 16 bytes, of whole vectors.  kRelShifted: the rows of all tensors
+// start at the same place in 16 bytes, and lanes hold the aligned chunks: column c of a row that starts `sh`
+// elements into a chunk is "place" c + sh, and its position p counts as p + sh, so that the distances are the
+// same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else, moved into columns.
+constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
 
 // 1 / s to one unit in the last place (s >= 1 but for what is infinite or NaN).
 __device__ __forceinline__ float rcp_fast(float s) {
@@ -212,8 +224,7 @@ struct RelWindow {
         : win(w), size(SLOTS ? rel_groups(p.dhi - p.dlo + 1, V) : rel_entries(p.dhi - p.dlo + 1, V)), dlo(p.dlo), dhi(p.dhi) {}
     __device__ __forceinline__ int words() const { return SLOTS ? SLOTS * size * V : rel_spread(size - 1, V) + 1; }
 
-    // Position p's slot, the shift of its entries, and the group (entry) of its column 0.
-    __device__ __forceinline__ static int slot(int p) { return p & (SLOTS - 1); }
+    // The shift of a slot's entries, and the group (entry) of column 0 of the row at position p.
     __device__ __forceinline__ int residue(int s) const { return (2 * V - 1 - dlo - s) & (V - 1); }
     __device__ __forceinline__ int first(int p) const {
         return SLOTS ? (2 * V - 1 - dlo - p) >> (V == 8 ? 3 : 2) : V - dlo - p;
@@ -253,9 +264,9 @@ struct RelWindow {
             return t <= 1 ? -1 : t >= size - V ? 1 : 0;
         }
     }
-    __device__ __forceinline__ void read(int at, int first, int col, f2 (&b)[H]) const {
+    __device__ __forceinline__ void read(int slot, int first, int col, f2 (&b)[H]) const {
         if constexpr (SLOTS) {
-            const float4* q = reinterpret_cast<const float4*>(win) + slot(at) * size * (V / 4) +
+            const float4* q = reinterpret_cast<const float4*>(win) + slot * size * (V / 4) +
                               min(max(first + col / V, 0), size - 1);
 #pragma unroll
             for (int j = 0; j < V / 4; ++j) {
@@ -272,9 +283,9 @@ struct RelWindow {
         }
     }
     // Adds a vector that meets the window.
-    __device__ __forceinline__ void add(int at, int first, int col, const f2 (&d)[H]) {
+    __device__ __forceinline__ void add(int slot, int first, int col, const f2 (&d)[H]) {
         if constexpr (SLOTS) {
-            float4* q = reinterpret_cast<float4*>(win) + slot(at) * size * (V / 4) + first + col / V;
+            float4* q = reinterpret_cast<float4*>(win) + slot * size * (V / 4) + first + col / V;
             float4 f[V / 4];
 #pragma unroll
             for (int j = 0; j < V / 4; ++j) f[j] = q[j * size];
@@ -326,16 +337,17 @@ struct RelWindow {
 // ---------------------------------------------------------------------------------------
 
 // LPR lanes (of 1 to 16 warps, or a part of one) hold a row, NV vectors each (lane l: vectors l, l + LPR, ...);
-// TEAMS rows at a time.  WHOLE: rows of whole
-// vectors at vectors' distance, the next row's loads under way during the current one's arithmetic.  LOOP: rows
-// of any length, in tiles of that size, twice.
-template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, bool WHOLE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOLE)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
+// TEAMS rows at a time.  The next row's loads are under way during the current one's arithmetic, but for kRelAny.
+// LOOP: rows of any length, in tiles of that size, twice.
+template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
     constexpr int kTile = LPR * NV * V, kPiece = L * V;
+    constexpr bool SHIFT = MODE == kRelShifted, AHEAD = MODE != kRelAny;
     static_assert(SLOTS || TEAMS == 1, "one window has one team");
+    static_assert(!SHIFT || (SLOTS && !CKPT && L == 32), "shifted rows start in 16 bytes where they do");
     extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][2][W];
@@ -343,7 +355,8 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
     const int team = tid / LPR, wt = (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
-    RelWindow<T, SLOTS ? rel_slot_count(TEAMS) : 0> win(p, smem);
+    constexpr int kSlots = SLOTS ? rel_slot_count(TEAMS) : 0;
+    RelWindow<T, kSlots> win(p, smem);
     const f2 scale = f2_splat(p.scale), l2 = f2_splat(kRelLog2e);
     const int blocks = ckpt_blocks(p.Lk);
     const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
@@ -362,12 +375,15 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
         auto load = [&](const RelRow& r, int base) {
             const T* x = rel_at<const T>(p.a, r.row, p.lda);
             const RowIn<T> in(x, p.Lk, p.ea);
+            const int sh = SHIFT ? rel_shift(x) : 0;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = base + (k * LPR + wt * 32 + lane) * V;
-                if (col < r.n) {
-                    if constexpr (WHOLE)
+                if (col < sh + r.n && (!SHIFT || r.n > 0)) {
+                    if constexpr (MODE == kRelWhole)
                         raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + col));
+                    else if constexpr (SHIFT)
+                        raw[k] = load_chunk<T>(in, col - sh, p.ea);
                     else
                         raw[k] = load_columns<T>(in, col, r.n, p.ea);
                 }
@@ -378,7 +394,8 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
         if (!LOOP) load(r, 0);
         for (int c = 0; c < count; ++c) {
             f2 z[NV][H];
-            const int n = r.n, first = win.first(r.at), at = r.at;
+            const int sh = SHIFT ? rel_shift(rel_at<const T>(p.a, r.row, p.lda)) : 0;
+            const int n = sh + r.n, at = r.at + sh, first = win.first(at), slot = at & (kSlots - 1);
             const int most = L < 32 ? __reduce_max_sync(kFullMask, n) : n;   // of the warp's rows
             const int least = L < 32 ? __reduce_min_sync(kFullMask, n) : n;
             const unsigned row = r.row;
@@ -393,16 +410,16 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                     const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
                     if (from >= most) continue;
                     f2 b[H];
-                    win.read(at, first, col, b);
+                    win.read(slot, first, col, b);
                     Pairs<T>::unpack(raw[k], z[k]);
 #pragma unroll
                     for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_fma(scale, z[k][h2], b[h2]);
                     if (mrow && col < n) {
                         f2 mv[H];
-                        if constexpr (WHOLE)
+                        if constexpr (MODE == kRelWhole)
                             Pairs<T>::unpack(ld_keep(mrow + col), mv);
                         else
-                            Pairs<T>::unpack(load_columns<T>(RowIn<T>(mrow, p.Lk, p.em), col, n, p.em), mv);
+                            Pairs<T>::unpack(load_columns<T>(RowIn<T>(mrow, p.Lk, p.em), col - sh, n - sh, p.em), mv);
 #pragma unroll
                         for (int h2 = 0; h2 < H; ++h2) {  // a mask of -inf removes a key whatever its score is
                             const f2 s = f2_add(z[k][h2], mv[h2]);
@@ -416,6 +433,12 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                         for (int h2 = 0; h2 < H; ++h2)
                             z[k][h2] = f2_make(2 * h2 < left ? f2_lo(z[k][h2]) : -INFINITY,
                                                2 * h2 + 1 < left ? f2_hi(z[k][h2]) : -INFINITY);
+                    }
+                    if (SHIFT && from == 0) {
+#pragma unroll
+                        for (int h2 = 0; h2 < H; ++h2)
+                            z[k][h2] = f2_make(col + 2 * h2 >= sh ? f2_lo(z[k][h2]) : -INFINITY,
+                                               col + 2 * h2 + 1 >= sh ? f2_hi(z[k][h2]) : -INFINITY);
                     }
 #pragma unroll
                     for (int h2 = 0; h2 < H; ++h2) m = max3(m, f2_lo(z[k][h2]), f2_hi(z[k][h2]));
@@ -463,9 +486,9 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                 m = scores(0);
                 walk.next(p);
                 r = c + 1 < count ? rel_row<TEAMS>(p, walk, h, team) : RelRow();
-                if (WHOLE) load(r, 0);
+                if (AHEAD) load(r, 0);
                 if (L == 32 && !ok) {  // (the same in the whole team)
-                    if (!WHOLE) load(r, 0);
+                    if (!AHEAD) load(r, 0);
                     continue;
                 }
                 m = rel_warp_max<L>(m);
@@ -491,7 +514,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
             }
             const f2 c2 = f2_splat(inv);
             T* y = rel_at<T>(p.out, row, p.ldo);
-            const int stored = L == 32 || ok ? p.Lk : 0;
+            const int stored = L == 32 || ok ? sh + p.Lk : 0;
             for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
                 if constexpr (LOOP) {
                     load(r, base);
@@ -501,7 +524,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
-                    if (from >= p.Lk) continue;
+                    if (from >= sh + p.Lk) continue;
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (from < most) {
 #pragma unroll
@@ -509,8 +532,10 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                         u = Pairs<T>::pack(z[k]);
                         if (inv != inv) u = first_of<T>(u, n - col);  // (0 times NaN)
                     }
-                    if constexpr (WHOLE) {
+                    if constexpr (MODE == kRelWhole) {
                         if (col < stored) st_stream(y + col, u);
+                    } else if constexpr (SHIFT) {
+                        store_chunk<T>(y, col, sh, stored, u);
                     } else {
                         store_columns<T, L>(y, col, stored, u);
                     }
@@ -522,7 +547,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
             if constexpr (LOOP) {
                 walk.next(p);
                 if (c + 1 < count) r = rel_row<TEAMS>(p, walk, h, team);
-            } else if (!WHOLE) {
+            } else if (!AHEAD) {
                 load(r, 0);
             }
         }
@@ -554,13 +579,15 @@ __device__ __forceinline__ f2 where_weight(f2 y, f2 g) {
     return f2_make(f2_lo(y) == 0.f ? 0.f : f2_lo(g), f2_hi(y) == 0.f ? 0.f : f2_hi(g));
 }
 
-template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, bool WHOLE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOLE)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
+template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
     constexpr int kTile = LPR * NV * V, kPiece = L * V;
+    constexpr bool SHIFT = MODE == kRelShifted, AHEAD = MODE != kRelAny;
     static_assert(SLOTS || TEAMS == 1, "one window has one team");
+    static_assert(!SHIFT || (SLOTS && !CKPT && L == 32), "shifted rows start in 16 bytes where they do");
     extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][W];
@@ -569,7 +596,9 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
     const int team = tid / LPR, wt = (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
-    RelWindow<T, SLOTS ? rel_slot_count(TEAMS) : 0> win(p, smem);
+    // Shifted rows' residues follow their rows, not their positions: a team has slots of its own.
+    constexpr int kSlots = !SLOTS ? 0 : SHIFT ? TEAMS * V : rel_slot_count(TEAMS);
+    RelWindow<T, kSlots> win(p, smem);
     const bool sums = p.part != nullptr;
     const f2 scale = f2_splat(p.scale);
     const int blocks = ckpt_blocks(p.Lk);
@@ -597,11 +626,13 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
         for (int c = 0; c < count; ++c, walk.next(p)) {
             const RelRow r = rel_row<TEAMS>(p, walk, h, team);
             if (L == 32 && !r.ok) continue;  // (the same in the whole team)
-            const int n = r.n, first = win.first(r.at);
+            const T* dy = rel_at<const T>(p.a, r.row, p.lda);
+            const int sh = SHIFT ? rel_shift(dy) : 0;
+            const int n = sh + r.n, at = r.at + sh, first = win.first(at);
+            const int slot = SHIFT ? team * V + (at & (V - 1)) : at & (kSlots - 1);
             const int most = L < 32 ? __reduce_max_sync(kFullMask, n) : n;   // of the warp's rows
             const int least = L < 32 ? __reduce_min_sync(kFullMask, n) : n;
-            const int stored = L == 32 || r.ok ? p.Lk : 0;
-            const T* dy = rel_at<const T>(p.a, r.row, p.lda);
+            const int stored = L == 32 || r.ok ? sh + p.Lk : 0;
             const T* py = rel_at<const T>(p.y, r.row, p.ldy);
             const int8_t* pq = p.q + (unsigned long long)r.row * (blocks * kCkptBlock);
             const uint8_t* pk = p.k + (unsigned long long)r.row * blocks;
@@ -611,15 +642,19 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int col = base + (k * LPR + wt * 32 + lane) * V;
-                    if (col < n) {
-                        if constexpr (WHOLE)
+                    if (col < n && (!SHIFT || r.n > 0)) {
+                        if constexpr (MODE == kRelWhole)
                             g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + col));
+                        else if constexpr (SHIFT)
+                            g[k] = load_chunk<T>(in, col - sh, p.ea);
                         else
                             g[k] = load_columns<T>(in, col, n, p.ea);
                         if constexpr (CKPT)
                             pr[k].r.load(pq, pk, col);
-                        else if constexpr (WHOLE)
+                        else if constexpr (MODE == kRelWhole)
                             pr[k].u = __ldcs(reinterpret_cast<const uint4*>(py + col));
+                        else if constexpr (SHIFT)
+                            pr[k].u = load_chunk<T>(iy, col - sh, p.ey);
                         else
                             pr[k].u = load_columns<T>(iy, col, n, p.ey);
                     }
@@ -630,6 +665,12 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                     if (from < most && from + kPiece > least) {
                         g[k] = first_of<T>(g[k], n - from - lane * V);
                         pr[k].first(n - from - lane * V);
+                    }
+                    if constexpr (SHIFT) {
+                        if (from == 0) {
+                            g[k] = behind<T>(g[k], sh - lane * V);
+                            pr[k].u = behind<T>(pr[k].u, sh - lane * V);
+                        }
                     }
                 }
             };
@@ -674,7 +715,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
-                    if (from >= p.Lk) continue;
+                    if (from >= sh + p.Lk) continue;
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (from < most) {
                         f2 d[H], y[H], o[H];
@@ -688,6 +729,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                                 d[h2] = where_weight(y[h2], d[h2]);
                                 d[h2] = f2_make(col + 2 * h2 < n ? f2_lo(d[h2]) : 0.f,
                                                 col + 2 * h2 + 1 < n ? f2_hi(d[h2]) : 0.f);
+                                // (before a shifted row's start y is 0)
                             }
                         }
 #pragma unroll
@@ -696,7 +738,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                         if (sums) {
                             const int side = win.side(first, col);
                             if (side == 0) {
-                                win.add(r.at, first, col, d);
+                                win.add(slot, first, col, d);
                             } else {
                                 f2 sum = f2_add(d[0], d[1]);
 #pragma unroll
@@ -708,8 +750,10 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
                             }
                         }
                     }
-                    if constexpr (WHOLE) {
+                    if constexpr (MODE == kRelWhole) {
                         if (col < stored) st_stream(dx + col, u);
+                    } else if constexpr (SHIFT) {
+                        store_chunk<T>(dx, col, sh, stored, u);
                     } else {
                         store_columns<T, L>(dx, col, stored, u);
                     }
@@ -760,36 +804,48 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV, WHOL
 // ---------------------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------------------
-template <typename T, bool BWD, bool CKPT, bool WHOLE, bool SLOTS, int I>
+template <typename T, bool BWD, bool CKPT, int MODE, bool SLOTS, int I>
 const void* rel_kernel_of() {
     constexpr RelShape s = kRelShapes[I];
-    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1))
+    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1) || (MODE == kRelShifted && s.lanes < 32))
         return nullptr;  // rows in tiles have one window, and one window one team
     else if constexpr (BWD)
-        return (const void*)rel_bwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, WHOLE, SLOTS>;
+        return (const void*)rel_bwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, MODE, SLOTS>;
     else
-        return (const void*)rel_fwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, WHOLE, SLOTS>;
+        return (const void*)rel_fwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, MODE, SLOTS>;
 }
 
-template <typename T, bool BWD, bool CKPT, bool WHOLE, bool SLOTS, int... I>
+template <typename T, bool BWD, bool CKPT, int MODE, bool SLOTS, int... I>
 const void* rel_kernel(int shape, std::integer_sequence<int, I...>) {
     const void* found = nullptr;
-    ((void)(shape == I && (found = rel_kernel_of<T, BWD, CKPT, WHOLE, SLOTS, I>())), ...);
+    ((void)(shape == I && (found = rel_kernel_of<T, BWD, CKPT, MODE, SLOTS, I>())), ...);
     return found;
 }
 
-template <typename T, bool BWD, bool CKPT>
-const void* rel_kernel(int shape, bool whole, bool slots) {
+template <typename T, bool BWD>
+const void* rel_kernel(int shape, bool ckpt, int mode, bool slots) {
     constexpr auto all = std::make_integer_sequence<int, kRelShapeCount>();
-    return !slots  ? rel_kernel<T, BWD, CKPT, false, false>(shape, all)
-           : whole ? rel_kernel<T, BWD, CKPT, true, true>(shape, all)
-                   : rel_kernel<T, BWD, CKPT, false, true>(shape, all);
+    if (mode == kRelShifted) return rel_kernel<T, BWD, false, kRelShifted, true>(shape, all);
+    if (ckpt)
+        return !slots               ? rel_kernel<T, BWD, true, kRelAny, false>(shape, all)
+               : mode == kRelWhole ? rel_kernel<T, BWD, true, kRelWhole, true>(shape, all)
+                                   : rel_kernel<T, BWD, true, kRelAny, true>(shape, all);
+    return !slots               ? rel_kernel<T, BWD, false, kRelAny, false>(shape, all)
+           : mode == kRelWhole ? rel_kernel<T, BWD, false, kRelWhole, true>(shape, all)
+                               : rel_kernel<T, BWD, false, kRelAny, true>(shape, all);
 }
 
 // Whether rows of n elements, ld apart, are whole vectors at vectors' distance.
 template <typename T>
 bool rel_whole(const void* t, int64_t ld, int64_t n) {
     return !t || ((reinterpret_cast<uintptr_t>(t) & 15u) == 0 && ld % Io<T>::kVec == 0 && n % Io<T>::kVec == 0);
+}
+
+// Whether rows of both start at the same place in 16 bytes, every one of them.
+template <typename T>
+bool rel_congruent(const void* a, int64_t lda, const void* b, int64_t ldb) {
+    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15u) == 0 &&
+           (lda - ldb) * (int64_t)sizeof(T) % 16 == 0;
 }
 
 template <typename T, bool BWD>
@@ -833,18 +889,28 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
     const bool whole = rel_whole<T>(a.a, a.lda, a.Lk) && rel_whole<T>(a.y, a.ldy, a.Lk) &&
                        rel_whole<T>(a.out, a.ldo, a.Lk) && rel_whole<T>(a.mask, a.Lk, a.Lk);
     bool slots;
-    const int shape = rel_shape(V, rows, a.Lq, a.Lk, span, &slots);
+    int mode = whole ? kRelWhole : kRelAny;
+    int shape = rel_shape(V, rows, a.Lq, a.Lk, span, &slots);
+    int copies = rel_slot_count(kRelShapes[shape].teams);
+    if (!whole && !a.q && slots && rel_congruent<T>(a.a, a.lda, a.out, a.ldo) &&
+        (!a.y || rel_congruent<T>(a.a, a.lda, a.y, a.ldy))) {
+        const int wide = rel_shape_shifted(V, a.Lq, a.Lk, span, BWD, &copies);
+        if (wide >= 0) {
+            mode = kRelShifted;
+            shape = wide;
+        }
+    }
     const RelShape& sh = kRelShapes[shape];
     p.per_matrix = (a.Lq + sh.teams - 1) / sh.teams;
     p.per_head = (int64_t)p.per_matrix * a.B;
     p.units = p.per_head * a.H;
     // The forward's one copy by distance (slots), and the backward's sums by distance.
     const size_t words = BWD && !p.part ? 0
-                         : slots        ? (size_t)rel_slot_count(sh.teams) * rel_groups(span, V) * V + span
+                         : slots        ? (size_t)copies * rel_groups(span, V) * V + span
                                         : (size_t)rel_spread(rel_entries(span, V) - 1, V) + 1;
     const size_t smem = words * sizeof(float);
     const bool ckpt = a.q != nullptr;
-    const void* kern = ckpt ? rel_kernel<T, BWD, true>(shape, whole, slots) : rel_kernel<T, BWD, false>(shape, whole, slots);
+    const void* kern = rel_kernel<T, BWD>(shape, ckpt, mode, slots);
     if (!kern) return cudaErrorInvalidValue;
     cudaError_t e = smem > 40 * 1024 ? allow_smem(kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;

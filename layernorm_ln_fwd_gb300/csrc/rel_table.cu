@@ -66,6 +66,17 @@ int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots) {
     return nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : 4;
 }
 
+int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies) {
+    const int nvec = (Lk + V - 1 + V - 1) / V;  // chunks that a row may lie in
+    int shape = nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : -1;
+    if (Lq < 4 && nvec <= 64) shape = 9;
+    if (Lq >= 4 && nvec <= 256) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : 8;
+    if (shape < 0) return -1;
+    const int teams = kRelShapes[shape].teams;
+    *copies = bwd ? teams * V : rel_slot_count(teams);
+    return *copies * rel_groups(span, V) * V * 4 <= (bwd ? kRelShiftedBytes : kRelSlotBytes) ? shape : -1;
+}
+
 size_t rel_workspace_bytes(int H, int buckets, int sms) {
     return ((size_t)kRelMaxPerSm * sms + (size_t)H) * (size_t)buckets * sizeof(float);
 }

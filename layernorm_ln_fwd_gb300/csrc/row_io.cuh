@@ -59,6 +59,13 @@ __device__ __forceinline__ uint4 first_of(const uint4& u, int count) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A vector without its first `count` elements: zeros in their place.
+template <typename T>
+__device__ __forceinline__ uint4 behind(const uint4& u, int count) {
+    const uint4 f = first_of<T>(u, count);
+    return make_uint4(u.x ^ f.x, u.y ^ f.y, u.z ^ f.z, u.w ^ f.w);
+}
+
 // The aligned chunk at c, of which at least one element is the tensor's; at the tensor's ends the
 // elements inside it alone, zeros elsewhere.
 template <typename T>
@@ -112,6 +119,14 @@ __device__ __forceinline__ uint4 load_columns(const RowIn<T>& r, int col, int n,
     return join_at(a, two ? *reinterpret_cast<const uint4*>(p - s + 16) : make_uint4(0, 0, 0, 0), s);
 }
 
+// The aligned chunk that begins at column col of a row (col may lie before it): the row's elements, others'
+// around them.
+template <typename T>
+__device__ __forceinline__ uint4 load_chunk(const RowIn<T>& r, int col, const Extent& t) {
+    const char* p = reinterpret_cast<const char*>(r.row + col);
+    return r.inside ? __ldcs(reinterpret_cast<const uint4*>(p)) : load_at_end<T>(p, false, t);
+}
+
 // One element of a vector, as it is stored.
 template <typename T>
 __device__ __forceinline__ void store_element(T* p, const uint4& u, int e) {
@@ -120,6 +135,21 @@ __device__ __forceinline__ void store_element(T* p, const uint4& u, int e) {
         *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     else
         *reinterpret_cast<uint32_t*>(p) = w[e];
+}
+
+// Places col .. col + V - 1 of a row that starts `sh` elements into the chunk of place 0 and has its end at
+// place `end`: the chunk whole, or those of its elements that are the row's.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int col, int sh, int end, const uint4& u) {
+    constexpr int V = Io<T>::kVec;
+    T* p = row + (col - sh);
+    if (col >= sh && col + V <= end) {
+        __stcs(reinterpret_cast<uint4*>(p), u);
+    } else if (col < end) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (col + e >= sh && col + e < end) store_element(p + e, u, e);
+    }
 }
 
 // Groups of L lanes store L vectors each that follow one another: lane l of a group has columns col ..
