@@ -539,8 +539,8 @@ ln_status ln_ckpt8_load_bf16(const int8_t* q, const uint8_t* k, int64_t rows, in
  * the forward's own mean and rstd (rrms).  q, k as ln_ckpt8_store_* writes them.  The workspace is the caller's,
  * 256-byte aligned, of ln_bwd_ckpt8_workspace_bytes(rows, cols) bytes (enough for both); what it holds before
  * and after is of no account, and calls that may overlap need one each.  dx may be dy itself.  Two launches; no
- * atomics and no waits between blocks: bitwise repeatable.  rows == 0 writes dgamma = dbeta = 0.  Limits and
- * errors as for ln_bwd_*.
+ * atomics and no waits between blocks: bitwise repeatable for the same sizes and the same addresses modulo 16, on
+ * devices of as many SMs.  rows == 0 writes dgamma = dbeta = 0.  Limits and errors as for ln_bwd_*.
  */
 size_t ln_bwd_ckpt8_workspace_bytes(int64_t rows, int64_t cols);
 

@@ -61,50 +61,48 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_flat_kernel(const CkParams p
     }
 }
 
+// Rows of any kind: a warp takes kCkFlight pieces of 32 vectors of a row that follow one another.
 template <typename T, bool STORE>
 __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
     constexpr int V = Io<T>::kVec, S = 32 * V;
     pdl_enter();
-    const int lane = threadIdx.x & 31, col = lane * V;
+    const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (kCkThreads / 32);
-    const int64_t w0 = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5);
-    for (int64_t base = w0; base < p.total; base += warps * kCkFlight) {
-        uint4 u[kCkFlight];
-        CkptRaw<T> raw[kCkFlight];
-        int64_t row[kCkFlight], first[kCkFlight];
-        int n[kCkFlight];
+    for (int64_t at = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5); at < p.total; at += warps) {
+        const int64_t row = at / p.segs;
+        const int cols = (int)p.cols, from = (int)(at - row * p.segs) * kCkFlight * S + lane * V;
+        int8_t* q = p.q + row * p.ldq;
+        uint8_t* k = p.k + row * p.ldk;
+        if constexpr (STORE) {
+            const RowIn<T> in(static_cast<const T*>(p.x) + row * p.ld, cols, p.ex);
+            uint4 u[kCkFlight];
 #pragma unroll
-        for (int f = 0; f < kCkFlight; ++f) {
-            const int64_t at = base + f * warps;
-            n[f] = 0;
-            if (at >= p.total) continue;
-            row[f] = at / p.segs;
-            first[f] = (at - row[f] * p.segs) * S;
-            n[f] = (int)min((int64_t)S, p.cols - first[f]);
-            if (col < n[f]) {
-                if constexpr (STORE)
-                    u[f] = load_columns<T>(RowIn<T>(static_cast<const T*>(p.x) + row[f] * p.ld + first[f], n[f], p.ex), col, n[f], p.ex);
-                else
-                    raw[f].load(p.q + row[f] * p.ldq + first[f], p.k + row[f] * p.ldk + first[f] / kCkptBlock, col);
+            for (int f = 0; f < kCkFlight; ++f) {
+                const int col = from + f * S;
+                u[f] = col < cols ? load_columns<T>(in, col, cols, p.ex) : make_uint4(0, 0, 0, 0);
             }
-        }
 #pragma unroll
-        for (int f = 0; f < kCkFlight; ++f) {
-            if (n[f] == 0) continue;  // the same in the whole warp
-            if constexpr (STORE) {
-                if (col >= n[f])
-                    u[f] = make_uint4(0, 0, 0, 0);
-                else if (col + V > n[f])
-                    u[f] = first_of<T>(u[f], n[f] - col);
-                ckpt_keep<T>(u[f], col, ckpt_blocks(n[f]) * kCkptBlock, p.q + row[f] * p.ldq + first[f],
-                             p.k + row[f] * p.ldk + first[f] / kCkptBlock);
-            } else {
+            for (int f = 0; f < kCkFlight; ++f) {
+                const int col = from + f * S;
+                if (col - lane * V >= cols) break;  // the same in the whole warp
+                if (col < cols && col + V > cols) u[f] = first_of<T>(u[f], cols - col);
+                ckpt_keep<T>(u[f], col, ckpt_blocks(cols) * kCkptBlock, q, k);
+            }
+        } else {
+            CkptRaw<T> raw[kCkFlight];
+#pragma unroll
+            for (int f = 0; f < kCkFlight; ++f) {
+                raw[f].clear();
+                if (from + f * S < cols) raw[f].load(q, k, from + f * S);
+            }
+            RowOut<T, 32> out;
+#pragma unroll
+            for (int f = 0; f < kCkFlight; ++f) {
+                const int col = from + f * S;
+                if (col - lane * V >= cols) break;  // the same in the whole warp
                 f2 v[Pairs<T>::kPairs];
-                if (col < n[f]) {
-                    raw[f].values(v);
-                    u[f] = Pairs<T>::pack(v);
-                }
-                store_columns<T>(static_cast<T*>(p.out) + row[f] * p.ld + first[f], col, n[f], u[f]);
+                raw[f].values(v);
+                out.put(static_cast<T*>(p.out) + row * p.ld, col, cols, Pairs<T>::pack(v), f == 0, f == kCkFlight - 1);
             }
         }
     }
@@ -123,7 +121,8 @@ cudaError_t launch_t(CkParams p, cudaStream_t stream) {
         p.cols *= p.rows;
         p.rows = 1;
     }
-    p.segs = (p.cols + S - 1) / S;
+    const int64_t per = flat ? S : kCkFlight * S;
+    p.segs = (p.cols + per - 1) / per;
     p.total = p.segs * p.rows;
     const void* kern = flat ? (const void*)ckpt8_flat_kernel<T, STORE> : (const void*)ckpt8_kernel<T, STORE>;
     const int64_t slots = (int64_t)std::max(1, blocks_per_sm(kern, kCkThreads, 0)) * device_info(-1).sms;

@@ -4,9 +4,9 @@
 //   dx = rstd (g - (sum g + xhat sum g xhat) / cols)        (RMSNorm: without the first sum)
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 // ("Accelerating Transformer on GPU (II): Training with LightSeq2", section 2.1; mean and rstd are the
-// forward's, of the input itself).  A row is held in registers by 1 to 32 warps (a team), at 8 to 24 columns a lane,
+// forward's, of the input itself).  A row is held by 1 to 16 warps (a team), at 4 to 32 columns a lane,
 // and each lane keeps the column sums of its columns over all rows that its team takes.  dy and the integers of
-// the next 2 or 3 rows are on their way meanwhile, by asynchronous copies of 16 and 8 (4) bytes into
+// the next 1 to 3 rows are on their way meanwhile, by asynchronous copies of 16 and 8 (4) bytes into
 // shared memory that each lane makes and reads for itself, without barriers.  A block adds its teams' column sums in
 // order and leaves one row of partial sums for each statistic; a second, dependent launch adds those of a column,
 // 32 interleaved groups and then the groups, with their rounding errors carried along.  No atomics: results are the
@@ -22,8 +22,11 @@
 namespace lnk {
 namespace {
 
-// Rows of a team in shared memory or on their way there.
-__host__ __device__ constexpr int cn_stages(int lanes, int nv) { return lanes == 512 && nv == 4 ? 3 : 4; }
+// Rows of a team in shared memory or on their way there: 2 to 4, as many as fit beside gamma.
+__host__ __device__ constexpr int cn_stages(int lanes, int teams, int nv, int V) {
+    const int gamma = lanes * nv * V * 4, row = teams * ((lanes * nv + 1) * 16 + lanes * nv * V);
+    return gamma + 4 * row <= 220 * 1024 ? 4 : gamma + 3 * row <= 220 * 1024 ? 3 : 2;
+}
 
 struct CnParams {
     const void* dy;
@@ -51,6 +54,16 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+template <int LPR, int TEAMS>
+__device__ __forceinline__ void team_meets(int team) {
+    if constexpr (LPR == 32)
+        __syncwarp();
+    else if constexpr (TEAMS == 1)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(LPR) : "memory");
+}
+
 // Loads that stay where they are written, an iteration before their use.
 __device__ __forceinline__ float load_ahead(const float* p) {
     float v;
@@ -63,7 +76,7 @@ __device__ __forceinline__ uint32_t load_ahead(const uint8_t* p) {
     return v;
 }
 
-// The sum of W warps' values in shared memory, in order.
+// The sum of W warps' values in shared memory.
 template <int W>
 __device__ __forceinline__ float warps_sum(const float* v) {
     float s = 0.f;
@@ -71,10 +84,7 @@ __device__ __forceinline__ float warps_sum(const float* v) {
 #pragma unroll
         for (int w = 0; w < W; w += 4) {
             const float4 f = *reinterpret_cast<const float4*>(v + w);
-            s += f.x;
-            s += f.y;
-            s += f.z;
-            s += f.w;
+            s += (f.x + f.y) + (f.z + f.w);
         }
     } else {
 #pragma unroll
@@ -84,12 +94,16 @@ __device__ __forceinline__ float warps_sum(const float* v) {
 }
 
 // LPR lanes hold a row, NV vectors each (lane l: vectors l, l + LPR, ...); TEAMS rows at a time.  WHOLE: rows of
-// whole vectors at vectors' distance; others are loaded when they are needed.
+// whole vectors at vectors' distance.  Others come as the aligned chunks that they lie in, a lane's vector being in two
+// that follow one another, one of them its neighbour's, so that the team meets before it reads them.
 template <typename T, int LPR, int TEAMS, int NV, bool RMS, bool WHOLE>
 __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p) {
-    constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs, W = LPR / 32, S = cn_stages(LPR, NV);
+    constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs, W = LPR / 32, S = cn_stages(LPR, TEAMS, NV, V);
     constexpr int kThreads = LPR * TEAMS;
     constexpr int NS = RMS ? 1 : 2;
+    // xhat stays in registers between a row's two passes where they have room beside the column sums; else the
+    // integers are read again.
+    constexpr bool KEEP = RMS || NV * V <= 24;
     // gamma in fp32 [cols], then dy [S][NV][threads] and the integers behind it; at the end, the teams'
     // column sums [TEAMS][NS][cols] in the place of the two.
     extern __shared__ __align__(16) float smem[];
@@ -99,9 +113,12 @@ __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p)
     const int cols = p.cols, blocks = ckpt_blocks(cols), padded = blocks * kCkptBlock;
     float* gamma = smem;
     float* fold = smem + padded;
-    uint4* sd = reinterpret_cast<uint4*>(fold) + tid;
-    unsigned char* sq = reinterpret_cast<unsigned char*>(fold) + (size_t)S * NV * kThreads * 16 + tid * V;
-    auto column = [&](int v) { return (v * LPR + wt * 32 + lane) * V; };
+    // Rows of dy as chunks, LPR NV and one more each; the integers, each lane's for itself.
+    constexpr int kChunks = LPR * NV + 1;
+    uint4* sd = reinterpret_cast<uint4*>(fold) + team * kChunks;
+    unsigned char* sq = reinterpret_cast<unsigned char*>(fold) + (size_t)S * TEAMS * kChunks * 16 + tid * V;
+    // (Pieces of a warp that follow one another where chunks between them are to be stored whole.)
+    auto column = [&](int v) { return ((WHOLE ? v * LPR + wt * 32 : (wt * NV + v) * 32) + lane) * V; };
     const int step = (int)gridDim.x * TEAMS;  // (row + 2 steps stay below 2^31: LN_MAX_ROWS leaves room for them)
     const int row0 = (int)blockIdx.x * TEAMS + team;
     // Where this lane's first vector is, of the row to copy next and of the row to store next.
@@ -111,17 +128,33 @@ __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p)
     T* dx = static_cast<T*>(p.dx) + (size_t)row0 * cols;
     pdl_enter();
     auto issue = [&](int row, const T* dy, const int8_t* q, int stage) {
-        if constexpr (WHOLE) {
-            if (row < p.rows) {
+        if (row < p.rows) {
+            uint4* to = sd + stage * (TEAMS * kChunks);
+            if constexpr (WHOLE) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
-                    if (column(v) < cols) {
-                        copy_async<16>(sd + (stage * NV + v) * kThreads, dy + v * LPR * V);
-                        copy_async<V>(sq + (stage * NV + v) * (kThreads * V), q + v * LPR * V);
+                    if (column(v) < cols) copy_async<16>(to + column(v) / V, dy + (column(v) - column(0)));
+            } else {
+                const RowIn<T> in(dy - column(0), cols, p.ed);
+                const int sh = (int)((unsigned)reinterpret_cast<uintptr_t>(in.row) & 15u) / (int)sizeof(T);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int col = column(v) - sh;
+                    if (col < cols) {
+                        if (in.inside)
+                            copy_async<16>(to + column(v) / V, in.row + col);
+                        else
+                            to[column(v) / V] = load_chunk<T>(in, col, p.ed);
                     }
+                }
+                if (tid - team * LPR == LPR - 1 && LPR * NV * V - sh < cols)
+                    to[LPR * NV] = load_chunk<T>(in, LPR * NV * V - sh, p.ed);
             }
-            copies_commit();
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (column(v) < cols) copy_async<V>(sq + (stage * NV + v) * (kThreads * V), q + (column(v) - column(0)));
         }
+        copies_commit();
     };
 #pragma unroll
     for (int s = 0; s < S - 1; ++s)
@@ -155,45 +188,65 @@ __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p)
     const float inv = 1.0f / (float)cols;
     int parity = 0, stage = 0;
     for (int row = row0; row < p.rows; row += step, parity ^= 1) {
-        uint4 d[NV];
-        f2 x[NV][H];
+        f2 x[KEEP ? NV : 1][H];
         // (Taken here, not where they were loaded: what is made of them would wait for the loads there.)
         float mean = mean_n, rstd = rstd_n;
+        uint32_t kk[NV];
         asm volatile("" : "+f"(mean), "+f"(rstd));
-        const f2 m2 = f2_splat(-mean), r2 = f2_splat(rstd);
-        copies_wait<S - 2>();
-        f2 a = f2_splat(0.f), b = f2_splat(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            kk[v] = kn[v];
+            asm volatile("" : "+r"(kk[v]));
+        }
+        const f2 m2 = f2_splat(-mean), r2 = f2_splat(rstd);
+        const unsigned s_row = WHOLE ? 0u : (unsigned)reinterpret_cast<uintptr_t>(next_dy - column(0)) & 15u;
+        // A vector of dy, and of xhat.
+        const uint4* chunks = sd + stage * (TEAMS * kChunks);
+        auto load_dy = [&](int v, f2(&dy)[H]) {
             const int col = column(v);
-            if (col >= cols) continue;
-            CkptRaw<T> raw;
-            raw.k = kn[v];
-            asm volatile("" : "+r"(raw.k));
-            if constexpr (WHOLE) {
-                d[v] = sd[(stage * NV + v) * kThreads];
-                raw.take(sq + (stage * NV + v) * (kThreads * V));
-            } else {
-                const T* dy = next_dy - column(0);
-                d[v] = load_columns<T>(RowIn<T>(dy, cols, p.ed), col, cols, p.ed);
-                if (col + V > cols) d[v] = first_of<T>(d[v], cols - col);
-                raw.take(next_q + (col - column(0)));
+            uint4 d = chunks[col / V];
+            if constexpr (!WHOLE) {
+                if (s_row != 0) d = join_at(d, chunks[col / V + 1], s_row);
+                if (col + V > cols) d = first_of<T>(d, cols - col);
             }
-            raw.values(x[v], m2);
-            f2 dy[H];
-            Pairs<T>::unpack(d[v], dy);
-            const float4* gp = reinterpret_cast<const float4*>(gamma) + col / V;
+            Pairs<T>::unpack(d, dy);
+        };
+        auto load_xhat = [&](int v, f2(&xv)[H]) {
+            CkptRaw<T> raw;
+            raw.k = kk[v];
+            raw.take(sq + (stage * NV + v) * (kThreads * V));
+            raw.values(xv, m2);
+#pragma unroll
+            for (int h = 0; h < H; ++h) xv[h] = f2_mul(xv[h], r2);
+        };
+        // gamma dy.
+        auto times_gamma = [&](int v, const f2(&dy)[H], f2(&g)[H]) {
+            const float4* gp = reinterpret_cast<const float4*>(gamma) + column(v) / V;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float4 g4 = gp[h / 2 * (padded / V)];
-                const f2 g = f2_mul(h & 1 ? f2_make(g4.z, g4.w) : f2_make(g4.x, g4.y), dy[h]);
-                x[v][h] = f2_mul(x[v][h], r2);
-                sg[v][h] = f2_fma(dy[h], x[v][h], sg[v][h]);
+                g[h] = f2_mul(h & 1 ? f2_make(g4.z, g4.w) : f2_make(g4.x, g4.y), dy[h]);
+            }
+        };
+        copies_wait<S - 2>();
+        if constexpr (!WHOLE) team_meets<LPR, TEAMS>(team);
+        f2 a = f2_splat(0.f), b = f2_splat(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (column(v) >= cols) continue;
+            f2 dy[H], g[H];
+            f2(&xv)[H] = x[KEEP ? v : 0];
+            load_dy(v, dy);
+            load_xhat(v, xv);
+            times_gamma(v, dy, g);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                sg[v][h] = f2_fma(dy[h], xv[h], sg[v][h]);
                 if constexpr (!RMS) {
                     sb[v][h] = f2_add(sb[v][h], dy[h]);
-                    a = f2_add(a, g);
+                    a = f2_add(a, g[h]);
                 }
-                b = f2_fma(g, x[v][h], b);
+                b = f2_fma(g[h], xv[h], b);
             }
         }
         issue(row + (S - 1) * step, next_dy + lead * cols, next_q + lead * padded, stage == 0 ? S - 1 : stage - 1);
@@ -212,36 +265,33 @@ __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p)
                 red[parity][team][0][wt] = sx;
                 if constexpr (!RMS) red[parity][team][NS - 1][wt] = sa;
             }
-            if constexpr (TEAMS == 1)
-                __syncthreads();
-            else
-                asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(LPR) : "memory");
+            team_meets<LPR, TEAMS>(team);
             sx = warps_sum<W>(red[parity][team][0]);
             if constexpr (!RMS) sa = warps_sum<W>(red[parity][team][NS - 1]);
         }
         const f2 a2 = f2_splat(-sa * inv), b2 = f2_splat(-sx * inv);
+        RowOut<T, 32> out;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int col = column(v);
             if (col - lane * V >= cols) continue;  // the same in the whole warp
             uint4 u = make_uint4(0, 0, 0, 0);
             if (col < cols) {
-                f2 dy[H];
-                Pairs<T>::unpack(d[v], dy);
-                const float4* gp = reinterpret_cast<const float4*>(gamma) + col / V;
+                f2 dy[H], g[H];
+                load_dy(v, dy);
+                times_gamma(v, dy, g);
+                if constexpr (!KEEP) load_xhat(v, x[0]);
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const float4 g4 = gp[h / 2 * (padded / V)];
-                    f2 g = f2_mul(h & 1 ? f2_make(g4.z, g4.w) : f2_make(g4.x, g4.y), dy[h]);
-                    if constexpr (!RMS) g = f2_add(g, a2);
-                    dy[h] = f2_mul(r2, f2_fma(x[v][h], b2, g));
+                    if constexpr (!RMS) g[h] = f2_add(g[h], a2);
+                    dy[h] = f2_mul(r2, f2_fma(x[KEEP ? v : 0][h], b2, g[h]));
                 }
                 u = Pairs<T>::pack(dy);
             }
             if constexpr (WHOLE) {
                 if (col < cols) st_stream(dx + col, u);
             } else {
-                store_columns<T>(dx, col, cols, u);
+                out.put(dx, col, cols, u, v == 0, v == NV - 1);
             }
         }
         dx += (size_t)step * cols;
@@ -320,25 +370,17 @@ __global__ void __launch_bounds__(kCfX * kCfY) ckpt_norm_finish_kernel(const flo
 struct CnShape {
     int lanes, teams, nv;
 };
-// By capacity: lanes * nv vectors a row.  16 warps a block, so that an SM leaves one row of partial sums or two;
-// a lane's sums, x and dy of 24 columns in bf16 fill 128 registers, of 32 where there is one statistic.
-constexpr CnShape kCnShapes[] = {{32, 16, 1}, {32, 16, 2}, {32, 16, 3}, {32, 16, 4}, {64, 8, 2}, {64, 8, 3}, {64, 8, 4},
-                                 {128, 4, 2}, {128, 4, 3}, {128, 4, 4}, {256, 2, 2}, {256, 2, 3}, {256, 2, 4},
-                                 {512, 1, 2}, {512, 1, 3}, {512, 1, 4}, {1024, 1, 4}};
+// By capacity: lanes * nv vectors a row.  16 warps a block, one of which an SM holds: 128 registers a lane, and one
+// row of partial sums an SM.
+constexpr CnShape kCnShapes[] = {{32, 16, 1}, {32, 16, 2}, {32, 16, 3}, {32, 16, 4}, {64, 8, 3}, {64, 8, 4},
+                                 {128, 4, 3}, {128, 4, 4}, {256, 2, 3}, {256, 2, 4}, {512, 1, 3}, {512, 1, 4}, {512, 1, 8}};
 constexpr int kCnCount = sizeof(kCnShapes) / sizeof(kCnShapes[0]);
-
-// Whether a shape is used: of those with 4 vectors a lane, the widest, and any that 128 registers hold.
-constexpr bool cn_fits(const CnShape& s, bool rms, bool f32) {
-    return s.lanes == 256 && s.nv == 4 ? f32 : s.nv < 4 || s.lanes >= 512 || rms || f32;
-}
 
 template <typename T, bool RMS, bool WHOLE, int I>
 const void* cn_kernel_of() {
     constexpr CnShape s = kCnShapes[I];
-    if constexpr (s.lanes == 1024 && (sizeof(T) == 2 || WHOLE))
-        return nullptr;  // 512 lanes hold LN_MAX_COLS in bf16; fp32's rows do not fit the stages
-    else if constexpr (!cn_fits(s, RMS, sizeof(T) == 4))
-        return nullptr;
+    if constexpr (s.nv == 8 && sizeof(T) == 2)
+        return nullptr;  // LN_MAX_COLS in bf16 need no more than 4
     else
         return (const void*)ckpt_norm_kernel<T, s.lanes, s.teams, s.nv, RMS, WHOLE>;
 }
@@ -359,19 +401,18 @@ cudaError_t launch_cn_t(const CkptNormArgs& a, cudaStream_t stream, int* launche
     *launches = 0;
     const int nvec = (a.cols + V - 1) / V;
     int shape = 0;
-    while (shape < kCnCount && (kCnShapes[shape].lanes * kCnShapes[shape].nv < nvec ||
-                                !cn_fits(kCnShapes[shape], RMS, sizeof(T) == 4)))
-        ++shape;
+    while (shape < kCnCount && kCnShapes[shape].lanes * kCnShapes[shape].nv < nvec) ++shape;
     if (shape == kCnCount) return cudaErrorInvalidValue;
     const CnShape& sh = kCnShapes[shape];
     auto aligned = [](const void* t) { return (reinterpret_cast<uintptr_t>(t) & 15u) == 0; };
-    const bool whole = aligned(a.dy) && aligned(a.dx) && a.cols % V == 0 && sh.lanes < 1024;
+    const bool whole = aligned(a.dy) && aligned(a.dx) && a.cols % V == 0;
     constexpr auto all = std::make_integer_sequence<int, kCnCount>();
     const void* kern = whole ? cn_kernel<T, RMS, true>(shape, all) : cn_kernel<T, RMS, false>(shape, all);
     if (!kern) return cudaErrorInvalidValue;
     const int threads = sh.lanes * sh.teams;
     int stats = RMS ? 1 : 2;
-    const size_t staged = whole ? (size_t)cn_stages(sh.lanes, sh.nv) * sh.nv * threads * (16 + V) : 0;
+    const size_t staged = (size_t)cn_stages(sh.lanes, sh.teams, sh.nv, V) *
+                          ((size_t)sh.teams * (sh.lanes * sh.nv + 1) * 16 + (size_t)sh.nv * threads * V);
     const size_t folded = sh.teams > 1 ? (size_t)sh.teams * stats * ckpt_blocks(a.cols) * kCkptBlock * sizeof(float) : 0;
     const size_t smem = (size_t)ckpt_blocks(a.cols) * kCkptBlock * sizeof(float) + std::max(staged, folded);
     cudaError_t e = smem > 40 * 1024 ? allow_smem(kern, smem) : cudaSuccess;

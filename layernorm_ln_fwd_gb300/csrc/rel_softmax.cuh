@@ -320,10 +320,15 @@ struct RelWindow {
         const int span = dhi - dlo + 1;
         float sum = 0.f;
         if constexpr (SLOTS) {
-            for (int s = 0; s < SLOTS; ++s) {
-                const int u = t + 2 * V - 1 - residue(s), last = (size - 1) * V - 1;
-                for (int e = t == 0 ? V : max(u, V); e <= (t == span - 1 ? last : min(u, last)); ++e)
-                    sum += win[place(s, e)];
+            const int last = (size - 1) * V - 1;
+#pragma unroll
+            for (int s = 0; s < V; ++s) {  // slots s, s + V, ... have one residue
+                const int u = t + 2 * V - 1 - residue(s);
+                for (int e = t == 0 ? V : max(u, V); e <= (t == span - 1 ? last : min(u, last)); ++e) {
+                    const float* w = win + place(s, e);
+#pragma unroll
+                    for (int k = 0; k < SLOTS / V; ++k) sum += w[k * V * V * size];
+                }
             }
         } else {
             for (int e = t == 0 ? 0 : t + V; e <= (t == span - 1 ? size - 1 : t + V); ++e) sum += win[rel_spread(e, V)];
@@ -343,7 +348,7 @@ template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE
 __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
-    constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
+    constexpr int kThreads = LPR * TEAMS;
     constexpr int kTile = LPR * NV * V, kPiece = L * V;
     constexpr bool SHIFT = MODE == kRelShifted, AHEAD = MODE != kRelAny;
     static_assert(SLOTS || TEAMS == 1, "one window has one team");
@@ -351,13 +356,16 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
     extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][2][W];
-    const int tid = threadIdx.x, lane = tid & (L - 1), warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & (L - 1);
     const int team = tid / LPR, wt = (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
     constexpr int kSlots = SLOTS ? rel_slot_count(TEAMS) : 0;
     RelWindow<T, kSlots> win(p, smem);
     const f2 scale = f2_splat(p.scale), l2 = f2_splat(kRelLog2e);
+    // A warp's k-th piece of a row, in vectors.  Where vectors are moved into columns a warp's pieces follow one
+    // another, so that it stores the chunks between them whole; else the row's warps take turns.
+    auto place_of = [&](int k) { return MODE == kRelAny ? (wt * NV + k) * L : k * LPR + wt * 32; };
     const int blocks = ckpt_blocks(p.Lk);
     const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
     int parity = 0;
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             const int sh = SHIFT ? rel_shift(x) : 0;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = base + (k * LPR + wt * 32 + lane) * V;
+                const int col = base + (place_of(k) + lane) * V;
                 if (col < sh + r.n && (!SHIFT || r.n > 0)) {
                     if constexpr (MODE == kRelWhole)
                         raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + col));
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 float m = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    const int from = base + place_of(k) * V, col = from + lane * V;
                     if (from >= most) continue;
                     f2 b[H];
                     win.read(slot, first, col, b);
@@ -453,7 +461,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 if (!(fabsf(ref) < 16777216.f)) {
 #pragma unroll
                     for (int k = 0; k < NV; ++k) {
-                        if (base + (k * LPR + wt * 32) * V >= most) continue;
+                        if (base + place_of(k) * V >= most) continue;
 #pragma unroll
                         for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_add(z[k][h2], f2_splat(-ref));
                     }
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 f2 acc = f2_splat(0.f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    if (base + (k * LPR + wt * 32) * V >= most) continue;
+                    if (base + place_of(k) * V >= most) continue;
 #pragma unroll
                     for (int h2 = 0; h2 < H; ++h2) {
                         const f2 t = f2_fma(z[k][h2], l2, nr);
@@ -516,6 +524,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             T* y = rel_at<T>(p.out, row, p.ldo);
             const int stored = L == 32 || ok ? sh + p.Lk : 0;
             for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
+                RowOut<T, L> out;
                 if constexpr (LOOP) {
                     load(r, base);
                     scores(base);
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 }
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    const int from = base + place_of(k) * V, col = from + lane * V;
                     if (from >= sh + p.Lk) continue;
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (from < most) {
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     } else if constexpr (SHIFT) {
                         store_chunk<T>(y, col, sh, stored, u);
                     } else {
-                        store_columns<T, L>(y, col, stored, u);
+                        out.put(y, col, stored, u, k == 0, k == NV - 1);
                     }
                     if constexpr (CKPT)
                         ckpt_keep<T>(u, col, L == 32 || ok ? blocks * kCkptBlock : 0, p.q + (unsigned long long)row * (blocks * kCkptBlock),
@@ -585,7 +594,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
     constexpr int kTile = LPR * NV * V, kPiece = L * V;
-    constexpr bool SHIFT = MODE == kRelShifted, AHEAD = MODE != kRelAny;
+    constexpr bool SHIFT = MODE == kRelShifted;
     static_assert(SLOTS || TEAMS == 1, "one window has one team");
     static_assert(!SHIFT || (SLOTS && !CKPT && L == 32), "shifted rows start in 16 bytes where they do");
     extern __shared__ __align__(16) float smem[];
@@ -601,6 +610,9 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
     RelWindow<T, kSlots> win(p, smem);
     const bool sums = p.part != nullptr;
     const f2 scale = f2_splat(p.scale);
+    // A warp's k-th piece of a row, in vectors.  Where vectors are moved into columns a warp's pieces follow one
+    // another, so that it stores the chunks between them whole; else the row's warps take turns.
+    auto place_of = [&](int k) { return MODE == kRelAny ? (wt * NV + k) * L : k * LPR + wt * 32; };
     const int blocks = ckpt_blocks(p.Lk);
     const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
     int parity = 0;
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 const RowIn<T> in(dy, p.Lk, p.ea), iy(py, p.Lk, p.ey);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int col = base + (k * LPR + wt * 32 + lane) * V;
+                    const int col = base + (place_of(k) + lane) * V;
                     if (col < n && (!SHIFT || r.n > 0)) {
                         if constexpr (MODE == kRelWhole)
                             g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + col));
@@ -661,7 +673,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                 }
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {  // zeros where a key takes no part
-                    const int from = base + (k * LPR + wt * 32) * V;
+                    const int from = base + place_of(k) * V;
                     if (from < most && from + kPiece > least) {
                         g[k] = first_of<T>(g[k], n - from - lane * V);
                         pr[k].first(n - from - lane * V);
@@ -682,7 +694,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     f2 acc = f2_splat(0.f);
 #pragma unroll
                     for (int k = 0; k < NV; ++k) {
-                        if (base + (k * LPR + wt * 32) * V >= most) continue;
+                        if (base + place_of(k) * V >= most) continue;
                         f2 d[H], y[H];
                         Pairs<T>::unpack(g[k], d);
                         pr[k].values(y);
@@ -711,10 +723,11 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             if (careful) s = row_sum(std::true_type{});
             const f2 s2 = f2_splat(s);
             for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
+                RowOut<T, L> out;
                 if constexpr (LOOP) load(base);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int from = base + (k * LPR + wt * 32) * V, col = from + lane * V;
+                    const int from = base + place_of(k) * V, col = from + lane * V;
                     if (from >= sh + p.Lk) continue;
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (from < most) {
@@ -755,7 +768,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     } else if constexpr (SHIFT) {
                         store_chunk<T>(dx, col, sh, stored, u);
                     } else {
-                        store_columns<T, L>(dx, col, stored, u);
+                        out.put(dx, col, stored, u, k == 0, k == NV - 1);
                     }
                 }
             }
@@ -786,17 +799,21 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
         __syncthreads();
         const int total = (p.bk.n + 1) * (p.bk.both ? 2 : 1);
         float* part = p.part + ((int64_t)blockIdx.x + h) * total;
-        for (int k = warp; k < total; k += kWarps) {
-            int a, b;
-            rel_distances(p.bk, edge, k, a, b);
-            // (distances beyond the window have been added to its ends)
-            if (a < p.dlo && b >= p.dlo) a = p.dlo;
-            if (b > p.dhi && a <= p.dhi) b = p.dhi;
+        for (int k0 = 0; k0 < total; k0 += kThreads / 4) {  // four lanes a bucket
+            const int k = k0 + tid / 4;
             float v = 0.f;
-            if (a >= p.dlo && b <= p.dhi)
-                for (int d = a + (tid & 31); d <= b; d += 32) v += SLOTS ? one[d - p.dlo] : win.sum_at(d - p.dlo);
-            v = rel_warp_sum<32>(v);
-            if ((tid & 31) == 0) part[k] = v;
+            if (k < total) {
+                int a, b;
+                rel_distances(p.bk, edge, k, a, b);
+                // (distances beyond the window have been added to its ends)
+                if (a < p.dlo && b >= p.dlo) a = p.dlo;
+                if (b > p.dhi && a <= p.dhi) b = p.dhi;
+                if (a >= p.dlo && b <= p.dhi)
+                    for (int d = a + (tid & 3); d <= b; d += 4) v += SLOTS ? one[d - p.dlo] : win.sum_at(d - p.dlo);
+            }
+            v += __shfl_xor_sync(kFullMask, v, 1);
+            v += __shfl_xor_sync(kFullMask, v, 2);
+            if (k < total && (tid & 3) == 0) part[k] = v;
         }
     }
 }

@@ -152,48 +152,60 @@ __device__ __forceinline__ void store_chunk(T* row, int col, int sh, int end, co
     }
 }
 
-// Groups of L lanes store L vectors each that follow one another: lane l of a group has columns col ..
-// col + V - 1, col = first + l V, of a row of n columns (those of n and more are not stored; rows may differ from
-// group to group).  Called by all lanes of the warp.
-template <typename T, int L = 32>
-__device__ __forceinline__ void store_columns(T* row, int col, int n, const uint4& u) {
-    constexpr int V = Io<T>::kVec;
-    T* p = row + col;
-    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane of a group
-    if (L == 32 ? s == 0 : __all_sync(kFullMask, s == 0)) {
-        if (col + V <= n) {
-            __stcs(reinterpret_cast<uint4*>(p), u);
-        } else {
+// A row's (or a part's) vectors on their way out, by groups of L lanes: pieces of L vectors that follow one another,
+// lane l's of a piece with columns col .. col + V - 1, col = the piece's first + l V, of a row of n columns (those of n
+// and more are not stored; rows may differ from group to group).  `first` and `last`: the first and the last piece,
+// whose outer ends lie in chunks shared with others (a piece that ends at n or behind may be the last unsaid).
+// Called by all lanes of the warp.
+template <typename T, int L>
+struct RowOut {
+    uint4 carry;  // lane 0: the vector before the piece
+
+    __device__ __forceinline__ void put(T* row, int col, int n, const uint4& u, bool first, bool last) {
+        constexpr int V = Io<T>::kVec;
+        T* p = row + col;
+        const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane of a group
+        if (L == 32 ? s == 0 : __all_sync(kFullMask, s == 0)) {
+            if (col + V <= n) {
+                __stcs(reinterpret_cast<uint4*>(p), u);
+            } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (col + e < n) store_element(p + e, u, e);
+                for (int e = 0; e < V; ++e)
+                    if (col + e < n) store_element(p + e, u, e);
+            }
+            return;
         }
-        return;
-    }
-    const int lane = threadIdx.x & (L - 1);
-    const int over = (int)s / (int)sizeof(T);  // elements of mine that belong to the next lane's chunk
-    uint4 before;
-    before.x = __shfl_up_sync(kFullMask, u.x, 1, L);
-    before.y = __shfl_up_sync(kFullMask, u.y, 1, L);
-    before.z = __shfl_up_sync(kFullMask, u.z, 1, L);
-    before.w = __shfl_up_sync(kFullMask, u.w, 1, L);
-    if (lane > 0 || s == 0) {  // the chunk that holds the last `over` elements before mine and my first V - over
-        const uint4 c = s == 0 ? u : join_at(before, u, 16 - s);
-        if (col - over + V <= n) {
-            *reinterpret_cast<uint4*>(p - over) = c;
+        const int lane = threadIdx.x & (L - 1);
+        const int over = (int)s / (int)sizeof(T);  // elements of mine that belong to the next lane's chunk
+        uint4 before;
+        before.x = __shfl_sync(kFullMask, u.x, lane + L - 1, L);
+        before.y = __shfl_sync(kFullMask, u.y, lane + L - 1, L);
+        before.z = __shfl_sync(kFullMask, u.z, lane + L - 1, L);
+        before.w = __shfl_sync(kFullMask, u.w, lane + L - 1, L);
+        const uint4 next = before;  // (lane 0: the piece's last vector)
+        if (lane == 0 && !first) before = carry;
+        carry = next;
+        if (lane > 0 || !first || s == 0) {  // the chunk of the `over` elements before mine and my first V - over
+            const uint4 c = s == 0 ? u : join_at(before, u, 16 - s);
+            if (col - over + V <= n) {
+                *reinterpret_cast<uint4*>(p - over) = c;
+            } else if (col - over < n) {
+                put_some(p - over, c, 0, n - (col - over));
+            }
         } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (col - over + e < n) store_element(p - over + e, c, e);
+            put_some(p, u, 0, min(V - over, n - col));
         }
+        // The last piece's last `over` elements (where the row ends with the piece before, no lane takes them either).
+        if (lane == L - 1 && s != 0 && (last || col + V >= n)) put_some(p, u, V - over, n - col);
     }
-    // The group's first V - over and last `over` elements lie in chunks shared with others.
+
+    // Elements from .. to - 1 of a vector.
+    static __device__ __forceinline__ void put_some(T* p, const uint4& u, int from, int to) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const bool mine = s != 0 && ((lane == 0 && e < V - over) || (lane == L - 1 && e >= V - over));
-        if (mine && col + e < n) store_element(p + e, u, e);
+        for (int e = 0; e < Io<T>::kVec; ++e)
+            if (e >= from && e < to) store_element(p + e, u, e);
     }
-}
+};
 
 }  // namespace
 }  // namespace lnk

@@ -105,9 +105,15 @@ def test_norm_backwards_at_any_address_and_in_place(dtype, rms, cols):
     ck = ln.ckpt8_store(x)
     out = call(rms, dy, ck, gamma, mean, rstd)
     check_norm(dtype, out, dy, to64(ln.ckpt8_load(ck, torch.float32)), gamma, mean, rstd)
-    d = dy.clone()
+    d = dy.clone()  # (at another address: its rows may be cut up elsewhere, and their sums formed in another order)
+    out = call(rms, d, ck, gamma, mean, rstd)
+    check_norm(dtype, out, dy, to64(ln.ckpt8_load(ck, torch.float32)), gamma, mean, rstd)
     again = call(rms, d, ck, gamma, mean, rstd, dx=d)
     assert again[0] is d and all(torch.equal(a, b) for a, b in zip(again, out))
+    d = dy.reshape(-1)  # and in place where it was
+    want = call(rms, d.view(21, cols), ck, gamma, mean, rstd)
+    again = call(rms, d.view(21, cols), ck, gamma, mean, rstd, dx=d.view(21, cols))
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
 
 
 @pytest.mark.parametrize("rms", [False, True])
