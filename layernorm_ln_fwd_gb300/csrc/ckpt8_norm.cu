@@ -41,19 +41,6 @@ struct CnParams {
     Extent ed;
 };
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int LPR, int TEAMS>
 __device__ __forceinline__ void team_meets(int team) {
     if constexpr (LPR == 32)
@@ -62,18 +49,6 @@ __device__ __forceinline__ void team_meets(int team) {
         __syncthreads();
     else
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(LPR) : "memory");
-}
-
-// Loads that stay where they are written, an iteration before their use.
-__device__ __forceinline__ float load_ahead(const float* p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint32_t load_ahead(const uint8_t* p) {
-    uint32_t v;
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
 }
 
 // The sum of W warps' values in shared memory.

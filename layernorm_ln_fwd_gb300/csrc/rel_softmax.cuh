@@ -50,10 +50,11 @@ struct RelParams {
     const int* q_pos;
     int B, H, Lq, Lk, causal;
     int dlo, dhi;        // the window's distances
+    int stage;           // where the next row's values lie in the block's shared memory (backward), bytes
     int per_matrix;      // units of a sequence and head
     int64_t per_head, units;
     float scale;
-    Extent ea, ey, em;
+    Extent ea, ey;
     float* part;
     RelBuckets bk;
 };
@@ -155,9 +156,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// How rows lie.  kRelWhole: at multiples of 16 bytes, of whole vectors.  kRelShifted: the rows of all tensors
+// start at the same place in 16 bytes, and lanes hold the aligned chunks: column c of a row that starts `sh`
+// elements into a chunk is "place" c + sh, and its position p counts as p + sh, so that the distances are the
+// same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else, moved into columns.
+constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
+
 // Blocks an SM that the registers are to allow.
-constexpr int rel_resident(int threads, int nv) {
-    return threads == 256 ? (nv == 4 ? 3 : 4) : 1;
+constexpr int rel_resident(int lanes, int teams, int nv, int mode, int size) {
+    if (lanes * teams != 256) return 1;
+    const int most = nv == 4 ? 3 : 4;
+    return mode != kRelAny ? most : most - 1;
 }
 
 // Over groups of L lanes.
@@ -173,12 +182,6 @@ __device__ __forceinline__ float rel_warp_sum(float a) {
     for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFullMask, a, o);
     return a;
 }
-
-// How rows lie.  kRelWhole: at multiples of 16 bytes, of whole vectors.  kRelShifted: the rows of all tensors
-// start at the same place in 16 bytes, and lanes hold the aligned chunks: column c of a row that starts `sh`
-// elements into a chunk is "place" c + sh, and its position p counts as p + sh, so that the distances are the
-// same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else, moved into columns.
-constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
 
 // 1 / s to one unit in the last place (s >= 1 but for what is infinite or NaN).
 __device__ __forceinline__ float rcp_fast(float s) {
@@ -345,19 +348,19 @@ struct RelWindow {
 // TEAMS rows at a time.  The next row's loads are under way during the current one's arithmetic, but for kRelAny.
 // LOOP: rows of any length, in tiles of that size, twice.
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE, sizeof(T))) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS;
     constexpr int kTile = LPR * NV * V, kPiece = L * V;
     constexpr bool SHIFT = MODE == kRelShifted, AHEAD = MODE != kRelAny;
     static_assert(SLOTS || TEAMS == 1, "one window has one team");
-    static_assert(!SHIFT || (SLOTS && !CKPT && L == 32), "shifted rows start in 16 bytes where they do");
+    static_assert(!SHIFT || (SLOTS && !CKPT), "shifted rows start in 16 bytes where they do");
     extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][2][W];
     const int tid = threadIdx.x, lane = tid & (L - 1);
-    const int team = tid / LPR, wt = (tid - team * LPR) / 32;
+    const int team = tid / LPR, wt = W == 1 ? 0 : (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
     constexpr int kSlots = SLOTS ? rel_slot_count(TEAMS) : 0;
@@ -380,21 +383,28 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
         uint4 raw[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) raw[k] = make_uint4(0, 0, 0, 0);
+        // (shifted rows)
+        auto chunk = [&](const RelRow& r, const T* x, int sh) {
+            const T* mine = x + ((wt * 32 + lane) * V - sh);
+            const int n = r.n > 0 ? sh + r.n - (wt * 32 + lane) * V : 0;
+            return [=](int k, const char*& c) {
+                c = reinterpret_cast<const char*>(mine + k * LPR * V);
+                return k * LPR * V < n;
+            };
+        };
         auto load = [&](const RelRow& r, int base) {
             const T* x = rel_at<const T>(p.a, r.row, p.lda);
             const RowIn<T> in(x, p.Lk, p.ea);
             const int sh = SHIFT ? rel_shift(x) : 0;
+            auto column = [&](int k) { return base + (place_of(k) + lane) * V; };
+            if constexpr (MODE == kRelWhole) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = base + (place_of(k) + lane) * V;
-                if (col < sh + r.n && (!SHIFT || r.n > 0)) {
-                    if constexpr (MODE == kRelWhole)
-                        raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + col));
-                    else if constexpr (SHIFT)
-                        raw[k] = load_chunk<T>(in, col - sh, p.ea);
-                    else
-                        raw[k] = load_columns<T>(in, col, r.n, p.ea);
-                }
+                for (int k = 0; k < NV; ++k)
+                    if (column(k) < r.n) raw[k] = __ldcs(reinterpret_cast<const uint4*>(x + column(k)));
+            } else if constexpr (SHIFT) {
+                load_chunks<T>(raw, in.inside, chunk(r, x, sh));
+            } else {
+                load_vectors<T>(raw, in, r.n, p.ea, column);
             }
         };
         RelWalk walk(p, c0);
@@ -409,6 +419,10 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             const unsigned row = r.row;
             const bool ok = r.ok;
             const T* mrow = p.mask ? rel_at<const T>(p.mask, row % p.mask_rows, p.ldm) : nullptr;
+            if constexpr (SHIFT) {
+                const T* x = rel_at<const T>(p.a, row, p.lda);
+                end_chunks<T>(raw, RowIn<T>(x, p.Lk, p.ea).inside, p.ea, chunk(r, x, sh));
+            }
             // The scores of a tile, where the warp's 32 vectors have keys that take part (elsewhere z is
             // left as it is, and not used): -inf at the others among them.  Returns the largest.
             auto scores = [&](int base) {
@@ -422,12 +436,23 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     Pairs<T>::unpack(raw[k], z[k]);
 #pragma unroll
                     for (int h2 = 0; h2 < H; ++h2) z[k][h2] = f2_fma(scale, z[k][h2], b[h2]);
-                    if (mrow && col < n) {
+                }
+                if (mrow) {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        const int col = base + (place_of(k) + lane) * V;
+                        if (col >= n) continue;
                         f2 mv[H];
-                        if constexpr (MODE == kRelWhole)
+                        if constexpr (MODE == kRelWhole) {
                             Pairs<T>::unpack(ld_keep(mrow + col), mv);
-                        else
-                            Pairs<T>::unpack(load_columns<T>(RowIn<T>(mrow, p.Lk, p.em), col - sh, n - sh, p.em), mv);
+                        } else {  // element by element: few registers, and a mask is small and read again
+#pragma unroll
+                            for (int h2 = 0; h2 < H; ++h2) {
+                                const int c = col - sh + 2 * h2;
+                                mv[h2] = f2_make(c >= 0 && c < n - sh ? Io<T>::to_f(mrow[c]) : 0.f,
+                                                 c >= -1 && c + 1 < n - sh ? Io<T>::to_f(mrow[c + 1]) : 0.f);
+                            }
+                        }
 #pragma unroll
                         for (int h2 = 0; h2 < H; ++h2) {  // a mask of -inf removes a key whatever its score is
                             const f2 s = f2_add(z[k][h2], mv[h2]);
@@ -435,6 +460,11 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                                                f2_hi(mv[h2]) == -INFINITY ? -INFINITY : f2_hi(s));
                         }
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int from = base + place_of(k) * V, col = from + lane * V;
+                    if (from >= most) continue;
                     if (from + kPiece > least) {
                         const int left = n - col;
 #pragma unroll
@@ -544,7 +574,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     if constexpr (MODE == kRelWhole) {
                         if (col < stored) st_stream(y + col, u);
                     } else if constexpr (SHIFT) {
-                        store_chunk<T>(y, col, sh, stored, u);
+                        store_chunks<T, L>(y + (col - sh), from, sh, stored, u);
                     } else {
                         out.put(y, col, stored, u, k == 0, k == NV - 1);
                     }
@@ -589,7 +619,7 @@ __device__ __forceinline__ f2 where_weight(f2 y, f2 g) {
 }
 
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE, sizeof(T))) rel_bwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
@@ -602,13 +632,18 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
     __shared__ float red[2][TEAMS][W];
     __shared__ float far_sums[kWarps][2];
     const int tid = threadIdx.x, lane = tid & (L - 1), warp = tid >> 5;
-    const int team = tid / LPR, wt = (tid - team * LPR) / 32;
+    const int team = tid / LPR, wt = W == 1 ? 0 : (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
     pdl_enter();
     // Shifted rows' residues follow their rows, not their positions: a team has slots of its own.
     constexpr int kSlots = !SLOTS ? 0 : SHIFT ? TEAMS * V : rel_slot_count(TEAMS);
     RelWindow<T, kSlots> win(p, smem);
     const bool sums = p.part != nullptr;
+    // The next row's dy and y (or integers), copied by each lane for itself while it works on the current one.
+    constexpr bool STAGED = MODE == kRelWhole;
+    constexpr int kBytes = CKPT ? V : 16;
+    unsigned char* stage_dy = reinterpret_cast<unsigned char*>(smem) + p.stage + tid * 16;
+    unsigned char* stage_y = reinterpret_cast<unsigned char*>(smem) + p.stage + NV * kThreads * 16 + tid * kBytes;
     const f2 scale = f2_splat(p.scale);
     // A warp's k-th piece of a row, in vectors.  Where vectors are moved into columns a warp's pieces follow one
     // another, so that it stores the chunks between them whole; else the row's warps take turns.
@@ -635,9 +670,37 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             pr[k].clear();
         }
         RelWalk walk(p, c0);
-        for (int c = 0; c < count; ++c, walk.next(p)) {
-            const RelRow r = rel_row<TEAMS>(p, walk, h, team);
-            if (L == 32 && !r.ok) continue;  // (the same in the whole team)
+        uint32_t kn[CKPT ? NV : 1];
+        auto issue = [&](const RelRow& r) {
+            const T* dy = rel_at<const T>(p.a, r.row, p.lda);
+            const T* py = rel_at<const T>(p.y, r.row, p.ldy);
+            const int8_t* pq = p.q + (unsigned long long)r.row * (blocks * kCkptBlock);
+            const uint8_t* pk = p.k + (unsigned long long)r.row * blocks;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (place_of(k) + lane) * V;
+                if (col < r.n) {
+                    copy_async<16>(stage_dy + k * (kThreads * 16), dy + col);
+                    if constexpr (CKPT) {
+                        copy_async<V>(stage_y + k * (kThreads * V), pq + col);
+                        kn[k] = load_ahead(pk + col / kCkptBlock);
+                    } else {
+                        copy_async<16>(stage_y + k * (kThreads * 16), py + col);
+                    }
+                }
+            }
+            copies_commit();
+        };
+        RelRow ahead = rel_row<TEAMS>(p, walk, h, team);
+        if constexpr (STAGED) issue(ahead);
+        for (int c = 0; c < count; ++c) {
+            const RelRow r = ahead;
+            walk.next(p);
+            ahead = c + 1 < count ? rel_row<TEAMS>(p, walk, h, team) : RelRow();
+            if (L == 32 && !r.ok) {  // (the same in the whole team)
+                if constexpr (STAGED) issue(ahead);
+                continue;
+            }
             const T* dy = rel_at<const T>(p.a, r.row, p.lda);
             const int sh = SHIFT ? rel_shift(dy) : 0;
             const int n = sh + r.n, at = r.at + sh, first = win.first(at);
@@ -650,25 +713,47 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             const uint8_t* pk = p.k + (unsigned long long)r.row * blocks;
             T* dx = rel_at<T>(p.out, r.row, p.ldo);
             auto load = [&](int base) {
-                const RowIn<T> in(dy, p.Lk, p.ea), iy(py, p.Lk, p.ey);
+                if constexpr (STAGED) {
+                    copies_wait<0>();
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int col = base + (place_of(k) + lane) * V;
-                    if (col < n && (!SHIFT || r.n > 0)) {
-                        if constexpr (MODE == kRelWhole)
-                            g[k] = __ldcs(reinterpret_cast<const uint4*>(dy + col));
-                        else if constexpr (SHIFT)
-                            g[k] = load_chunk<T>(in, col - sh, p.ea);
-                        else
-                            g[k] = load_columns<T>(in, col, n, p.ea);
-                        if constexpr (CKPT)
-                            pr[k].r.load(pq, pk, col);
-                        else if constexpr (MODE == kRelWhole)
-                            pr[k].u = __ldcs(reinterpret_cast<const uint4*>(py + col));
-                        else if constexpr (SHIFT)
-                            pr[k].u = load_chunk<T>(iy, col - sh, p.ey);
-                        else
-                            pr[k].u = load_columns<T>(iy, col, n, p.ey);
+                    for (int k = 0; k < NV; ++k) {
+                        g[k] = *reinterpret_cast<const uint4*>(stage_dy + k * (kThreads * 16));
+                        if constexpr (CKPT) {
+                            pr[k].r.take(stage_y + k * (kThreads * V));
+                            pr[k].r.k = kn[k];
+                        } else {
+                            pr[k].u = *reinterpret_cast<const uint4*>(stage_y + k * (kThreads * 16));
+                        }
+                    }
+                } else {
+                    const RowIn<T> in(dy, p.Lk, p.ea), iy(py, p.Lk, p.ey);
+                    auto column = [&](int k) { return base + (place_of(k) + lane) * V; };
+                    auto chunk = [&](const T* row) {
+                        const T* mine = row + ((wt * 32 + lane) * V - sh);
+                        const int left = n > sh ? n - (wt * 32 + lane) * V : 0;
+                        return [=](int k, const char*& c) {
+                            c = reinterpret_cast<const char*>(mine + k * LPR * V);
+                            return k * LPR * V < left;
+                        };
+                    };
+                    uint4 y[NV];
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) y[k] = make_uint4(0, 0, 0, 0);
+                    if constexpr (SHIFT) {
+                        load_chunks<T>(g, in.inside, chunk(dy));
+                        load_chunks<T>(y, iy.inside, chunk(py));
+                        end_chunks<T>(g, in.inside, p.ea, chunk(dy));
+                        end_chunks<T>(y, iy.inside, p.ey, chunk(py));
+                    } else {
+                        load_vectors<T>(g, in, n, p.ea, column);
+                        if constexpr (!CKPT) load_vectors<T>(y, iy, n, p.ey, column);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        if constexpr (!CKPT)
+                            pr[k].u = y[k];
+                        else if (column(k) < n)
+                            pr[k].r.load(pq, pk, column(k));
                     }
                 }
 #pragma unroll
@@ -721,6 +806,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
             // not count) is formed again without such keys.
             const bool careful = L < 32 ? __any_sync(kFullMask, !(fabsf(s) < INFINITY)) : !(fabsf(s) < INFINITY);
             if (careful) s = row_sum(std::true_type{});
+            if constexpr (STAGED) issue(ahead);  // (what was there has been used)
             const f2 s2 = f2_splat(s);
             for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
                 RowOut<T, L> out;
@@ -766,7 +852,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
                     if constexpr (MODE == kRelWhole) {
                         if (col < stored) st_stream(dx + col, u);
                     } else if constexpr (SHIFT) {
-                        store_chunk<T>(dx, col, sh, stored, u);
+                        store_chunks<T, L>(dx + (col - sh), from, sh, stored, u);
                     } else {
                         out.put(dx, col, stored, u, k == 0, k == NV - 1);
                     }
@@ -824,7 +910,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR * TEAMS, NV)) rel
 template <typename T, bool BWD, bool CKPT, int MODE, bool SLOTS, int I>
 const void* rel_kernel_of() {
     constexpr RelShape s = kRelShapes[I];
-    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1) || (MODE == kRelShifted && s.lanes < 32))
+    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1) || (BWD && MODE == kRelShifted && s.lanes < 32))
         return nullptr;  // rows in tiles have one window, and one window one team
     else if constexpr (BWD)
         return (const void*)rel_bwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, MODE, SLOTS>;
@@ -898,7 +984,6 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
     p.scale = a.scale;
     p.ea = extent(a.a, rows, a.lda);
     p.ey = extent(a.y, rows, a.ldy);
-    p.em = extent(a.mask, a.mask_rows, a.Lk);
     p.part = BWD && a.dtable ? a.part : nullptr;
     p.bk = *a.buckets;
     rel_span(a, &p.dlo, &p.dhi);
@@ -925,13 +1010,15 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
     const size_t words = BWD && !p.part ? 0
                          : slots        ? (size_t)copies * rel_groups(span, V) * V + span
                                         : (size_t)rel_spread(rel_entries(span, V) - 1, V) + 1;
-    const size_t smem = words * sizeof(float);
+    const int threads = sh.lanes * sh.teams;
+    size_t smem = words * sizeof(float);
+    p.stage = (int)((smem + 15) / 16 * 16);
+    if (BWD && mode == kRelWhole) smem = p.stage + (size_t)sh.nv * threads * (16 + (a.q ? V : 16));
     const bool ckpt = a.q != nullptr;
     const void* kern = rel_kernel<T, BWD>(shape, ckpt, mode, slots);
     if (!kern) return cudaErrorInvalidValue;
     cudaError_t e = smem > 40 * 1024 ? allow_smem(kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    const int threads = sh.lanes * sh.teams;
     const int per_sm = std::min(kRelMaxPerSm, std::max(1, blocks_per_sm(kern, threads, smem)));
     const int grid = (int)std::min<int64_t>(p.units, (int64_t)per_sm * device_info(-1).sms);
     void* args[] = {&p};

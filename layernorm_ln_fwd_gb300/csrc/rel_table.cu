@@ -71,6 +71,10 @@ int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies) {
     int shape = nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : -1;
     if (Lq < 4 && nvec <= 64) shape = 9;
     if (Lq >= 4 && nvec <= 256) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : 8;
+    if (!bwd && Lq >= 4 && nvec <= 64) {  // (in the backward parts of a warp would take too many slots)
+        const int parts = nvec <= 16 ? (nvec <= 8 ? 10 : 11) : nvec <= 32 ? 12 : 13;
+        if (rel_slot_count(kRelShapes[parts].teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes) shape = parts;
+    }
     if (shape < 0) return -1;
     const int teams = kRelShapes[shape].teams;
     *copies = bwd ? teams * V : rel_slot_count(teams);

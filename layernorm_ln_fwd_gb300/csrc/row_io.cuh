@@ -87,6 +87,33 @@ __device__ __forceinline__ uint4 chunk_at(const char* c, const Extent& t) {
     return u;
 }
 
+// Copies of 16, 8 or 4 bytes into shared memory that go on by themselves: each thread commits its own in groups, and
+// waits until all but its last N groups are there (for itself: others see them after a barrier).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Loads that stay where they are written, an iteration before their use.
+__device__ __forceinline__ float load_ahead(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t load_ahead(const uint8_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
 // A row to read: whether the chunks at its ends are the tensor's as well.
 template <typename T>
 struct RowIn {
@@ -97,59 +124,111 @@ struct RowIn {
           inside(reinterpret_cast<const char*>(r) - 15 >= t.lo && reinterpret_cast<const char*>(r + n) + 15 <= t.hi) {}
 };
 
-// The vector of load_columns in a tensor's first or last row (a call: rare, and too large to have in line).
-template <typename T>
-__device__ __noinline__ uint4 load_at_end(const char* p, bool two, Extent t) {
-    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
-    const uint4 a = chunk_at<T>(p - s, t);
-    return s == 0 ? a : join_at(a, two ? chunk_at<T>(p - s + 16, t) : make_uint4(0, 0, 0, 0), s);
+// The chunks that a lane has of a row: `at(k, c)` says whether it has a k-th and sets its address.  Those of a row that
+// is not `inside` (the tensor's first and last) are left to end_chunks, which takes them one after another in one place
+// of the code, and is called where they are needed: in line for each k they would take the registers, and merged with
+// the loads they would make these wait where they are.
+template <typename T, int NV, typename AT>
+__device__ __forceinline__ void load_chunks(uint4 (&raw)[NV], bool inside, AT at) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const char* c;
+        if (at(k, c) && inside) raw[k] = __ldcs(reinterpret_cast<const uint4*>(c));
+    }
 }
 
-// Columns col .. col + V - 1 of a row whose first n > col columns are wanted; those behind them come
-// as anything.
+template <typename T, int NV, typename AT>
+__device__ __forceinline__ void end_chunks(uint4 (&raw)[NV], bool inside, const Extent& t, AT at) {
+    if (inside) return;
+#pragma unroll 1
+    for (int k = 0; k < NV; ++k) {
+        const char* c;
+        if (!at(k, c)) continue;
+        const uint4 u = chunk_at<T>(c, t);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j == k) raw[j] = u;
+    }
+}
+
+// A lane's vectors of a row: columns col(k) .. col(k) + V - 1 of its first n, col(k) a multiple of V, those behind n as
+// anything; a vector without columns below n is left as it is.
+template <typename T, int NV, typename COL>
+__device__ __forceinline__ void load_vectors(uint4 (&raw)[NV], const RowIn<T>& r, int n, const Extent& t, COL col) {
+    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(r.row) & 15u;  // the same in every lane
+    const int sh = (int)s / (int)sizeof(T);
+    auto one = [&](int k, const char*& c) {
+        c = reinterpret_cast<const char*>(r.row + (col(k) - sh));
+        return col(k) < n;
+    };
+    auto two = [&](int k, const char*& c) {
+        c = reinterpret_cast<const char*>(r.row + (col(k) - sh + Io<T>::kVec));
+        return s != 0 && col(k) - sh + Io<T>::kVec < n;
+    };
+    uint4 more[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) more[k] = make_uint4(0, 0, 0, 0);
+    load_chunks<T>(raw, r.inside, one);
+    load_chunks<T>(more, r.inside, two);
+    end_chunks<T>(raw, r.inside, t, one);
+    end_chunks<T>(more, r.inside, t, two);
+    if (s == 0) return;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) raw[k] = join_at(raw[k], more[k], s);
+}
+
+// One of them, col < n, a multiple of V.
 template <typename T>
 __device__ __forceinline__ uint4 load_columns(const RowIn<T>& r, int col, int n, const Extent& t) {
-    constexpr int V = Io<T>::kVec;
-    const char* p = reinterpret_cast<const char*>(r.row + col);
-    const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane
-    const bool two = s != 0 && col + (16 - (int)s) / (int)sizeof(T) < n;  // the second chunk has columns
-    if (!r.inside && (s != 0 || col + V > n)) return load_at_end<T>(p, two, t);
-    const uint4 a = *reinterpret_cast<const uint4*>(p - s);
-    if (s == 0) return a;
-    return join_at(a, two ? *reinterpret_cast<const uint4*>(p - s + 16) : make_uint4(0, 0, 0, 0), s);
+    uint4 u[1] = {make_uint4(0, 0, 0, 0)};
+    load_vectors<T>(u, r, n, t, [&](int) { return col; });
+    return u[0];
 }
 
 // The aligned chunk that begins at column col of a row (col may lie before it): the row's elements, others'
 // around them.
 template <typename T>
 __device__ __forceinline__ uint4 load_chunk(const RowIn<T>& r, int col, const Extent& t) {
-    const char* p = reinterpret_cast<const char*>(r.row + col);
-    return r.inside ? __ldcs(reinterpret_cast<const uint4*>(p)) : load_at_end<T>(p, false, t);
+    uint4 u[1];
+    auto at = [&](int, const char*& c) {
+        c = reinterpret_cast<const char*>(r.row + col);
+        return true;
+    };
+    load_chunks<T>(u, r.inside, at);
+    end_chunks<T>(u, r.inside, t, at);
+    return u[0];
 }
 
-// One element of a vector, as it is stored.
-template <typename T>
-__device__ __forceinline__ void store_element(T* p, const uint4& u, int e) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    else
-        *reinterpret_cast<uint32_t*>(p) = w[e];
-}
-
-// Places col .. col + V - 1 of a row that starts `sh` elements into the chunk of place 0 and has its end at
-// place `end`: the chunk whole, or those of its elements that are the row's.
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int col, int sh, int end, const uint4& u) {
-    constexpr int V = Io<T>::kVec;
-    T* p = row + (col - sh);
-    if (col >= sh && col + V <= end) {
-        __stcs(reinterpret_cast<uint4*>(p), u);
-    } else if (col < end) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (col + e >= sh && col + e < end) store_element(p + e, u, e);
+// Elements from .. to - 1 of lane `src`'s vector, each stored by a lane of its own: element e to p + e (p, src, from
+// and to the same in a group of L lanes; all lanes of the warp call it).
+template <typename T, int L>
+__device__ __forceinline__ void store_some(T* p, const uint4& u, int src, int from, int to) {
+    const uint32_t x = __shfl_sync(kFullMask, u.x, src, L), y = __shfl_sync(kFullMask, u.y, src, L);
+    const uint32_t z = __shfl_sync(kFullMask, u.z, src, L), w = __shfl_sync(kFullMask, u.w, src, L);
+    const int e = threadIdx.x & (L - 1), i = sizeof(T) == 2 ? e >> 1 : e;
+    const uint32_t v = i & 2 ? (i & 1 ? w : z) : (i & 1 ? y : x);
+    if (e >= from && e < to && e < Io<T>::kVec) {
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint16_t*>(p + e) = (uint16_t)(v >> (16 * (e & 1)));
+        else
+            *reinterpret_cast<uint32_t*>(p + e) = v;
     }
+}
+
+// Groups of L lanes store L chunks of a row that starts `sh` elements into the chunk of place 0 and has its end at
+// place `end`: lane l's, at p, at places from + l V .. from + l V + V - 1, whole, or those of its elements that are the
+// row's.  Called by all lanes of the warp, with one `from`.
+template <typename T, int L>
+__device__ __forceinline__ void store_chunks(T* p, int from, int sh, int end, const uint4& u) {
+    constexpr int V = Io<T>::kVec;
+    const int lane = threadIdx.x & (L - 1), col = from + lane * V;
+    if (col >= sh && col + V <= end) __stcs(reinterpret_cast<uint4*>(p), u);
+    if (from == 0 && (L == 32 ? sh > 0 : __any_sync(kFullMask, sh > 0)))
+        store_some<T, L>(p - lane * V, u, 0, sh, sh > 0 ? end : 0);
+    const int left = end - from, last = left / V;  // the chunk with the row's end inside, if it is one of these
+    const bool part = left > 0 && left < L * V && left % V != 0 && !(from == 0 && last == 0 && sh > 0);
+    if (L == 32 ? part : __any_sync(kFullMask, part))
+        store_some<T, L>(p + (last - lane) * V, u, last, 0, part ? left - last * V : 0);
 }
 
 // A row's (or a part's) vectors on their way out, by groups of L lanes: pieces of L vectors that follow one another,
@@ -165,17 +244,14 @@ struct RowOut {
         constexpr int V = Io<T>::kVec;
         T* p = row + col;
         const unsigned s = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;  // the same in every lane of a group
+        const int lane = threadIdx.x & (L - 1), base = col - lane * V;
         if (L == 32 ? s == 0 : __all_sync(kFullMask, s == 0)) {
-            if (col + V <= n) {
-                __stcs(reinterpret_cast<uint4*>(p), u);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (col + e < n) store_element(p + e, u, e);
-            }
+            if (col + V <= n) __stcs(reinterpret_cast<uint4*>(p), u);
+            const int end = n <= base ? 0 : (n - base) / V;  // the vector that the row ends in
+            if (L == 32 ? n % V != 0 : __any_sync(kFullMask, n % V != 0))
+                store_some<T, L>(row + (base + end * V), u, end, 0, n <= base || end >= L ? 0 : n - base - end * V);
             return;
         }
-        const int lane = threadIdx.x & (L - 1);
         const int over = (int)s / (int)sizeof(T);  // elements of mine that belong to the next lane's chunk
         uint4 before;
         before.x = __shfl_sync(kFullMask, u.x, lane + L - 1, L);
@@ -185,25 +261,19 @@ struct RowOut {
         const uint4 next = before;  // (lane 0: the piece's last vector)
         if (lane == 0 && !first) before = carry;
         carry = next;
-        if (lane > 0 || !first || s == 0) {  // the chunk of the `over` elements before mine and my first V - over
-            const uint4 c = s == 0 ? u : join_at(before, u, 16 - s);
-            if (col - over + V <= n) {
-                *reinterpret_cast<uint4*>(p - over) = c;
-            } else if (col - over < n) {
-                put_some(p - over, c, 0, n - (col - over));
-            }
-        } else {
-            put_some(p, u, 0, min(V - over, n - col));
-        }
-        // The last piece's last `over` elements (where the row ends with the piece before, no lane takes them either).
-        if (lane == L - 1 && s != 0 && (last || col + V >= n)) put_some(p, u, V - over, n - col);
-    }
-
-    // Elements from .. to - 1 of a vector.
-    static __device__ __forceinline__ void put_some(T* p, const uint4& u, int from, int to) {
-#pragma unroll
-        for (int e = 0; e < Io<T>::kVec; ++e)
-            if (e >= from && e < to) store_element(p + e, u, e);
+        // The chunk of the `over` elements before mine and my first V - over; the first lane of all has the latter alone.
+        const uint4 c = s == 0 ? u : join_at(before, u, 16 - s);
+        const int at = col - over;
+        if (at + V <= n && (lane > 0 || !first || s == 0)) *reinterpret_cast<uint4*>(p - over) = c;
+        if (first) store_some<T, L>(row + base, u, 0, 0, s == 0 ? 0 : min(V - over, n - base));
+        // The chunk that the row ends in, and the last piece's last `over` elements.
+        const int end = n <= base - over ? L : (n - (base - over)) / V;
+        const bool inner = end < L && !(end == 0 && first && s != 0) && n > base - over + end * V;
+        if (L == 32 ? inner : __any_sync(kFullMask, inner))
+            store_some<T, L>(row + (base - over + end * V), c, min(end, L - 1), 0, inner ? n - (base - over + end * V) : 0);
+        const bool outer = s != 0 && (last || base + L * V >= n);
+        if (L == 32 ? outer : __any_sync(kFullMask, outer))
+            store_some<T, L>(row + (base + (L - 1) * V), u, L - 1, V - over, outer ? n - (base + (L - 1) * V) : 0);
     }
 };
 
