@@ -61,14 +61,18 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_flat_kernel(const CkParams p
     }
 }
 
-// Rows of any kind: a warp takes kCkFlight pieces of 32 vectors of a row that follow one another.
-template <typename T, bool STORE>
+// Rows of any kind: L lanes (fewer than 32 for narrow rows) take kCkFlight pieces of L vectors of a row that follow
+// one another.
+template <typename T, bool STORE, int L>
 __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
-    constexpr int V = Io<T>::kVec, S = 32 * V;
+    constexpr int V = Io<T>::kVec, S = L * V, G = kCkThreads / L;
     pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kCkThreads / 32);
-    for (int64_t at = (int64_t)blockIdx.x * (kCkThreads / 32) + (threadIdx.x >> 5); at < p.total; at += warps) {
+    const int lane = threadIdx.x & (L - 1);
+    const int64_t groups = (int64_t)gridDim.x * G;
+    for (int64_t at0 = (int64_t)blockIdx.x * G + (threadIdx.x & ~31u) / L; at0 < p.total; at0 += groups) {
+        // (A warp's groups together: one past the last takes the last again, and stores nothing.)
+        const int64_t mine = at0 + (threadIdx.x & 31) / L, at = min(mine, p.total - 1);
+        const bool ok = L == 32 || mine < p.total;
         const int64_t row = at / p.segs;
         const int cols = (int)p.cols, from = (int)(at - row * p.segs) * kCkFlight * S + lane * V;
         int8_t* q = p.q + row * p.ldq;
@@ -84,9 +88,9 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
 #pragma unroll
             for (int f = 0; f < kCkFlight; ++f) {
                 const int col = from + f * S;
-                if (col - lane * V >= cols) break;  // the same in the whole warp
+                if (L == 32 && col - lane * V >= cols) break;  // the same in the whole warp
                 if (col < cols && col + V > cols) u[f] = first_of<T>(u[f], cols - col);
-                ckpt_keep<T>(u[f], col, ckpt_blocks(cols) * kCkptBlock, q, k);
+                ckpt_keep<T>(u[f], col, ok ? ckpt_blocks(cols) * kCkptBlock : 0, q, k);
             }
         } else {
             CkptRaw<T> raw[kCkFlight];
@@ -95,14 +99,14 @@ __global__ void __launch_bounds__(kCkThreads) ckpt8_kernel(const CkParams p) {
                 raw[f].clear();
                 if (from + f * S < cols) raw[f].load(q, k, from + f * S);
             }
-            RowOut<T, 32> out;
+            RowOut<T, L> out;
 #pragma unroll
             for (int f = 0; f < kCkFlight; ++f) {
                 const int col = from + f * S;
-                if (col - lane * V >= cols) break;  // the same in the whole warp
+                if (L == 32 && col - lane * V >= cols) break;  // the same in the whole warp
                 f2 v[Pairs<T>::kPairs];
                 raw[f].values(v);
-                out.put(static_cast<T*>(p.out) + row * p.ld, col, cols, Pairs<T>::pack(v), f == 0, f == kCkFlight - 1);
+                out.put(static_cast<T*>(p.out) + row * p.ld, col, ok ? cols : 0, Pairs<T>::pack(v), f == 0, f == kCkFlight - 1);
             }
         }
     }
@@ -121,12 +125,17 @@ cudaError_t launch_t(CkParams p, cudaStream_t stream) {
         p.cols *= p.rows;
         p.rows = 1;
     }
-    const int64_t per = flat ? S : kCkFlight * S;
+    const int64_t vectors = (p.cols + S / 32 - 1) / (S / 32);
+    const int lanes = flat || vectors > 16 * kCkFlight ? 32 : vectors > 8 * kCkFlight ? 16 : 8;
+    const int64_t per = flat ? S : (int64_t)kCkFlight * (S / 32) * lanes;
     p.segs = (p.cols + per - 1) / per;
     p.total = p.segs * p.rows;
-    const void* kern = flat ? (const void*)ckpt8_flat_kernel<T, STORE> : (const void*)ckpt8_kernel<T, STORE>;
+    const void* kern = flat          ? (const void*)ckpt8_flat_kernel<T, STORE>
+                       : lanes == 32 ? (const void*)ckpt8_kernel<T, STORE, 32>
+                       : lanes == 16 ? (const void*)ckpt8_kernel<T, STORE, 16>
+                                     : (const void*)ckpt8_kernel<T, STORE, 8>;
     const int64_t slots = (int64_t)std::max(1, blocks_per_sm(kern, kCkThreads, 0)) * device_info(-1).sms;
-    const int64_t need = (p.total + kCkThreads / 32 - 1) / (kCkThreads / 32);
+    const int64_t each = kCkThreads / lanes, need = (p.total + each - 1) / each;
     void* args[] = {&p};
     return launch_kernel(kern, dim3((unsigned)std::min(slots, need)), dim3(kCkThreads), 0, stream, args, false);
 }

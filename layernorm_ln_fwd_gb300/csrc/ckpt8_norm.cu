@@ -112,18 +112,20 @@ __global__ void __launch_bounds__(LPR* TEAMS) ckpt_norm_kernel(const CnParams p)
             } else {
                 const RowIn<T> in(dy - column(0), cols, p.ed);
                 const int sh = (int)((unsigned)reinterpret_cast<uintptr_t>(in.row) & 15u) / (int)sizeof(T);
+                const T* mine = in.row + (column(0) - sh);
+                uint4* mine_to = to + column(0) / V;
+                if (in.inside) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int col = column(v) - sh;
-                    if (col < cols) {
-                        if (in.inside)
-                            copy_async<16>(to + column(v) / V, in.row + col);
-                        else
-                            to[column(v) / V] = load_chunk<T>(in, col, p.ed);
-                    }
+                    for (int v = 0; v < NV; ++v)
+                        if (column(v) - sh < cols) copy_async<16>(mine_to + v * 32, mine + v * 32 * V);
+                } else {  // the tensor's first and last row
+#pragma unroll 1
+                    for (int v = 0; v < NV; ++v)
+                        if (column(v) - sh < cols)
+                            mine_to[v * 32] = chunk_at<T>(reinterpret_cast<const char*>(mine + v * 32 * V), p.ed);
                 }
                 if (tid - team * LPR == LPR - 1 && LPR * NV * V - sh < cols)
-                    to[LPR * NV] = load_chunk<T>(in, LPR * NV * V - sh, p.ed);
+                    to[LPR * NV] = chunk_at<T>(reinterpret_cast<const char*>(in.row + (LPR * NV * V - sh)), p.ed);
             }
 #pragma unroll
             for (int v = 0; v < NV; ++v)

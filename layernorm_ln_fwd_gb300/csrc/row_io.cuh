@@ -185,20 +185,6 @@ __device__ __forceinline__ uint4 load_columns(const RowIn<T>& r, int col, int n,
     return u[0];
 }
 
-// The aligned chunk that begins at column col of a row (col may lie before it): the row's elements, others'
-// around them.
-template <typename T>
-__device__ __forceinline__ uint4 load_chunk(const RowIn<T>& r, int col, const Extent& t) {
-    uint4 u[1];
-    auto at = [&](int, const char*& c) {
-        c = reinterpret_cast<const char*>(r.row + col);
-        return true;
-    };
-    load_chunks<T>(u, r.inside, at);
-    end_chunks<T>(u, r.inside, t, at);
-    return u[0];
-}
-
 // Elements from .. to - 1 of lane `src`'s vector, each stored by a lane of its own: element e to p + e (p, src, from
 // and to the same in a group of L lanes; all lanes of the warp call it).
 template <typename T, int L>

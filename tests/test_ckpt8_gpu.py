@@ -25,7 +25,8 @@ def values(rows, cols, dtype, seed, pad=0, offset=0):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (5, 32), (4, 33), (700, 64), (64, 768), (9, 1001), (33, 4096),
-                                       (2, 16385), (1, 100003), (3000, 40)])
+                                       (2, 16385), (1, 100003), (3000, 40), (301, 130),
+                                       (77, 249), (301, 310), (77, 511)])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (5, 0), (8, 3)])
 def test_store_and_load(dtype, rows, cols, pad, offset):
     x = values(rows, cols, dtype, cols, pad, offset)
