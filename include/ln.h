@@ -453,16 +453,17 @@ ln_status ln_distill_bf16(const ln_bf16* logits, int64_t ld, const int32_t* ids,
  *
  * y may be x itself, and dx may be dy itself, with the same ld; otherwise outputs overlap nothing.  Columns
  * Lk .. ld of a row are left as they are.  Pointers and ld need no alignment (q: 16 bytes).  Limits: Lk <=
- * LN_REL_MAX_KEYS, ld <= LN_REL_MAX_LD, H <= LN_REL_MAX_HEADS, n_edges <= LN_REL_MAX_EDGES, edges <= LN_REL_MAX_SPAN, B H Lq <=
- * LN_MAX_ROWS.  No rows: the forward does nothing, the backward zeroes dtable.
+ * LN_REL_MAX_KEYS, Lq <= LN_REL_MAX_QUERIES, H <= LN_REL_MAX_HEADS, B H Lq <= LN_MAX_ROWS, ld <= LN_REL_MAX_LD, n_edges <=
+ * LN_REL_MAX_EDGES, edges <= LN_REL_MAX_SPAN.  No rows: the forward does nothing, the backward zeroes dtable.
  *
  * The workspace (the backward with dtable) is the caller's, of ln_softmax_rel_workspace_bytes_* bytes; what it
  * holds before and after a call is of no account, and calls that may overlap need one each.  Nothing is
- * allocated, nothing is atomic, and no kernel waits for another block: results are bitwise repeatable for the same
+ * allocated, nothing is atomic, and no kernel waits for a block outside its cluster: results are bitwise repeatable for the same
  * sizes, the same outputs asked for and the same addresses modulo 16, on devices of as many SMs (rows are cut at 16
  * bytes, and split by their number).
  */
 #define LN_REL_MAX_KEYS (1 << 20)
+#define LN_REL_MAX_QUERIES (1 << 29)
 #define LN_REL_MAX_HEADS 65536
 #define LN_REL_MAX_EDGES 255
 #define LN_REL_MAX_SPAN 16384

@@ -24,6 +24,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 import struct
 import threading
@@ -806,13 +807,14 @@ def ckpt8_workspace_bytes(rows: int, cols: int) -> int:
     return int(lib().ln_bwd_ckpt8_workspace_bytes(rows, cols))
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=256, typed=True)
 def rel_edges(buckets: int, max_distance: int = 128, bidirectional: bool = True) -> tuple:
     """The distances at which buckets 1, 2, ... of a side begin.  A side has ``buckets`` of them, or half
     as many where they are ``bidirectional`` (keys behind a query, then keys ahead of it): the first half
     hold one distance each, the others grow by equal factors up to ``max_distance``, and the last takes
     all beyond.  Exact: bucket m + k begins at the least n with (n / m)^(s - m) >= (max_distance / m)^k, for a
     side of s buckets, m = s // 2."""
+    buckets, max_distance = operator.index(buckets), operator.index(max_distance)
     side = buckets // 2 if bidirectional else buckets
     if bidirectional and buckets % 2:
         raise ValueError("bidirectional buckets come in pairs")
@@ -840,7 +842,7 @@ def rel_edges(buckets: int, max_distance: int = 128, bidirectional: bool = True)
 _REL = struct.Struct("@4q4P4if")
 
 
-@functools.lru_cache(maxsize=256)
+@functools.lru_cache(maxsize=256, typed=True)
 def _edge_array(buckets, max_distance, bidirectional):
     """(array, its address, its length), kept as long as its address is in use: the cache's entries go only when
     others take their place, so the caller holds the array meanwhile."""

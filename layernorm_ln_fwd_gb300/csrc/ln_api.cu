@@ -617,7 +617,7 @@ ln_status check_rel(const ln_rel* r) {
     if (!r || r->B < 0 || r->H <= 0 || r->Lq < 0 || r->Lk <= 0) return LN_EINVAL;
     if (!std::isfinite(r->scale) || r->n_edges < 0 || (r->n_edges > 0 && !r->edges)) return LN_EINVAL;
     if (r->Lk > LN_REL_MAX_KEYS || r->H > LN_REL_MAX_HEADS || r->n_edges > LN_REL_MAX_EDGES ||
-        r->Lq > LN_MAX_ROWS || r->B > LN_MAX_ROWS)
+        r->Lq > LN_REL_MAX_QUERIES || r->B > LN_MAX_ROWS)
         return LN_EUNSUPPORTED;
     if (r->Lq > 0 && r->B > LN_MAX_ROWS / (r->H * r->Lq)) return LN_EUNSUPPORTED;
     for (int i = 0; i < r->n_edges; ++i) {

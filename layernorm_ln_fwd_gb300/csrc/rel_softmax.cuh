@@ -17,7 +17,8 @@
 // contiguous share of the units (one row for each of its teams), which are ordered by head (so that a block fills
 // its window once or twice), then by query from both ends inwards (a causal row's work grows with its query:
 // neighbours average), then by sequence.  Its teams meet only where the head changes.
-// Rows of more columns than 16 warps hold are gone through twice.
+// Rows of more columns than 16 warps hold are gone through twice, in the forward by the blocks of a cluster where
+// there are few of them.
 #pragma once
 
 #include <limits.h>
@@ -29,11 +30,13 @@
 #include "ckpt8.cuh"
 #include "rel_ops.h"
 #include "row_io.cuh"
+#include "vocab.cuh"
 
 namespace lnk {
 namespace {
 
 constexpr float kRelLog2e = 1.4426950408889634f;
+constexpr int kRelMaxCluster = 8;
 
 struct RelParams {
     const void* a;
@@ -163,7 +166,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
 
 // Blocks an SM that the registers are to allow.
-constexpr int rel_resident(int lanes, int teams, int nv, int mode, int size) {
+constexpr int rel_resident(int lanes, int teams, int nv, int mode) {
     if (lanes * teams != 256) return 1;
     const int most = nv == 4 ? 3 : 4;
     return mode != kRelAny ? most : most - 1;
@@ -348,7 +351,7 @@ struct RelWindow {
 // TEAMS rows at a time.  The next row's loads are under way during the current one's arithmetic, but for kRelAny.
 // LOOP: rows of any length, in tiles of that size, twice.
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE, sizeof(T))) rel_fwd_kernel(const __grid_constant__ RelParams p) {
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS;
@@ -359,6 +362,9 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE,
     extern __shared__ __align__(16) float smem[];
     __shared__ int edge[kRelMaxEdges];
     __shared__ float red[2][TEAMS][2][W];
+    __shared__ float2 joint[2][LOOP ? kRelMaxCluster : 1];  // the cluster's (max, sum)
+    const int cluster = LOOP ? (int)cluster_blocks() : 1, rank = LOOP ? (int)cluster_rank() : 0;
+    if (cluster > 1) cluster_arrive();  // "this block's shared memory exists"
     const int tid = threadIdx.x, lane = tid & (L - 1);
     const int team = tid / LPR, wt = W == 1 ? 0 : (tid - team * LPR) / 32;
     for (int i = tid; i < p.bk.n; i += kThreads) edge[i] = p.bk.edge[i];
@@ -370,9 +376,11 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE,
     // another, so that it stores the chunks between them whole; else the row's warps take turns.
     auto place_of = [&](int k) { return MODE == kRelAny ? (wt * NV + k) * L : k * LPR + wt * 32; };
     const int blocks = ckpt_blocks(p.Lk);
-    const int64_t end = p.units * ((int64_t)blockIdx.x + 1) / gridDim.x;
+    const unsigned block = blockIdx.x / cluster, grid = gridDim.x / cluster;
+    const int64_t end = p.units * ((int64_t)block + 1) / grid;
     int parity = 0;
-    for (int64_t unit = p.units * blockIdx.x / gridDim.x; unit < end;) {
+    if (cluster > 1) cluster_wait();
+    for (int64_t unit = p.units * block / grid; unit < end;) {
         const int h = (int)(unit / p.per_head);
         const int64_t c0 = unit - (int64_t)h * p.per_head;
         const int count = (int)(min(p.per_head, c0 + (end - unit)) - c0);
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE,
             };
             float m = -INFINITY, s = 0.f;
             if constexpr (LOOP) {
-                for (int base = 0; base < n; base += kTile) {
+                for (int base = rank * kTile; base < n; base += cluster * kTile) {
                     load(r, base);
                     const float mt = fmaxf(m, rel_warp_max<L>(scores(base)));
                     s *= rel_factor(m, mt);
@@ -547,13 +555,26 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE,
                 for (int w = 0; w < W; ++w) M = fmaxf(M, red[parity][team][0][w]);
 #pragma unroll
                 for (int w = 0; w < W; ++w) S += red[parity][team][1][w] * rel_factor(red[parity][team][0][w], M);
+                if (LOOP && cluster > 1) {  // and the blocks'
+                    if (tid < cluster) {
+                        const uint32_t to = in_block(&joint[parity][rank], (uint32_t)tid);
+                        st_cluster_f32(to, M);
+                        st_cluster_f32(to + 4, S);
+                    }
+                    cluster_arrive();
+                    cluster_wait();
+                    M = -INFINITY;
+                    S = 0.f;
+                    for (int i = 0; i < cluster; ++i) M = fmaxf(M, joint[parity][i].x);
+                    for (int i = 0; i < cluster; ++i) S += joint[parity][i].y * rel_factor(joint[parity][i].x, M);
+                }
                 inv = S == 0.f ? 0.f : rel_factor(m, M) / S;
                 parity ^= 1;
             }
             const f2 c2 = f2_splat(inv);
             T* y = rel_at<T>(p.out, row, p.ldo);
             const int stored = L == 32 || ok ? sh + p.Lk : 0;
-            for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
+            for (int base = LOOP ? rank * kTile : 0; base < (LOOP ? p.Lk : 1); base += cluster * kTile) {
                 RowOut<T, L> out;
                 if constexpr (LOOP) {
                     load(r, base);
@@ -619,7 +640,7 @@ __device__ __forceinline__ f2 where_weight(f2 y, f2 g) {
 }
 
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
-__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE, sizeof(T))) rel_bwd_kernel(const __grid_constant__ RelParams p) {
+__global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
     constexpr int W = LPR > 32 ? LPR / 32 : 1, L = LPR > 32 ? 32 : LPR;  // warps of a row, its lanes in a warp
     constexpr int kThreads = LPR * TEAMS, kWarps = kThreads / 32;
@@ -1013,16 +1034,25 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
     const int threads = sh.lanes * sh.teams;
     size_t smem = words * sizeof(float);
     p.stage = (int)((smem + 15) / 16 * 16);
-    if (BWD && mode == kRelWhole) smem = p.stage + (size_t)sh.nv * threads * (16 + (a.q ? V : 16));
+    if (BWD && mode == kRelWhole && slots) smem = p.stage + (size_t)sh.nv * threads * (16 + (a.q ? V : 16));
     const bool ckpt = a.q != nullptr;
     const void* kern = rel_kernel<T, BWD>(shape, ckpt, mode, slots);
     if (!kern) return cudaErrorInvalidValue;
     cudaError_t e = smem > 40 * 1024 ? allow_smem(kern, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
+    const int sms = device_info(-1).sms;
     const int per_sm = std::min(kRelMaxPerSm, std::max(1, blocks_per_sm(kern, threads, smem)));
-    const int grid = (int)std::min<int64_t>(p.units, (int64_t)per_sm * device_info(-1).sms);
+    int64_t at_once = (int64_t)per_sm * sms;
+    int cluster = 1;  // blocks a row: rows in tiles, of which there are fewer than SMs, share them out
+    if (!BWD && sh.loop) {
+        const int64_t tiles = (a.Lk + (int64_t)threads * sh.nv * V - 1) / ((int64_t)threads * sh.nv * V);
+        while (cluster < kRelMaxCluster && cluster < tiles && p.units * cluster < sms) cluster *= 2;
+        if (cluster > 1) at_once = clusters_at_once(kern, threads, cluster, smem);
+        if (at_once < 1) cluster = 1, at_once = sms;
+    }
+    const int grid = (int)std::min<int64_t>(p.units, at_once);
     void* args[] = {&p};
-    e = launch_kernel(kern, dim3(grid), dim3(threads), smem, stream, args, false);
+    e = launch_cluster(kern, dim3(grid * cluster), dim3(threads), cluster, smem, stream, args);
     if (e != cudaSuccess) return e;
     *launches = 1;
     if (p.part) {

@@ -40,6 +40,13 @@ def test_edges_refuse(args):
         ln.rel_edges(*args)
 
 
+def test_edges_are_of_whole_numbers():
+    for bad in ((32, 200.0), (32.0, 200), (32, "200")):
+        with pytest.raises(TypeError):
+            ln.rel_edges(*bad)
+    assert all(type(e) is int for e in ln.rel_edges(32, 200)) and len(ln.rel_edges(32, 200)) == 15
+
+
 def test_reference_gradients_against_differences():
     rng = np.random.default_rng(1)
     B, H, Lq, Lk = 2, 2, 5, 9
@@ -101,7 +108,7 @@ class Packed:
 BAD = [(dict(B=-1), 1), (dict(H=0), 1), (dict(Lq=-1), 1), (dict(Lk=0), 1), (dict(scale=float("nan")), 1),
        (dict(scale=float("inf")), 1), (dict(n_edges=-1), 1), (dict(edges=0), 1), (dict(edge=(0, 1)), 1),
        (dict(edge=(3, 2)), 1), (dict(edge=(1, 16385)), 3), (dict(Lk=(1 << 20) + 1), 3), (dict(H=65537), 3),
-       (dict(n_edges=256), 3), (dict(Lq=2**31 - 2**16, H=2), 3), (dict(B=2**40), 3)]
+       (dict(n_edges=256), 3), (dict(Lq=2**29 + 1, H=1, B=1), 3), (dict(Lq=2**31 - 2**16, H=2), 3), (dict(B=2**40), 3)]
 
 
 @pytest.mark.parametrize("over,status", BAD)

@@ -109,6 +109,23 @@ def test_rows_longer_than_the_registers_hold(dtype, Lk):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 3, 1, 70001), (2, 1, 1, 140000), (1, 80, 1, 16400), (1, 2, 90, 16600)])
+def test_few_long_rows(dtype, shape):
+    B, H, Lq, Lk = shape
+    g = torch.Generator().manual_seed(1)
+    mask = torch.where(torch.rand(1, Lk, generator=g) < 0.3, -torch.inf, 0.5)
+    case = Case(dtype, shape, both=False, lens=[Lk - 1000, 17][:B], q_pos=[Lk - 1001, 16][:B], mask=mask, seed=10)
+    y, ck = ln.softmax_rel_fwd(case.x, case.table, mask=case.mask, ckpt=True, **case.how)
+    case.check_fwd(y)
+    q, k, _ = relref.quantise(to64(y.view(-1, Lk)))
+    assert (ck.q.cpu().numpy() == q).all() and (ck.k.cpu().numpy() == k).all()
+    again = ln.softmax_rel_fwd(case.x, case.table, mask=case.mask, **case.how)[0]
+    assert torch.equal(y, again)
+    ln.softmax_rel_fwd(case.x, case.table, mask=case.mask, y=case.x, **case.how)
+    assert torch.equal(y, case.x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("buckets,span,both", [(4, 2, True), (2, 5, False), (16, 64, True), (64, 800, False),
                                                (256, 16384, False), (512, 16384, True), (32, 17, True), (3, 2, False)])
 def test_buckets(dtype, buckets, span, both):
@@ -294,7 +311,7 @@ def test_given_streams_and_graphs():
 
 
 def test_rows_past_two_to_the_thirty_two_bytes():
-    """The last rows of a call whose scores end behind 4 GB are those of a call of their own."""
+    """The last rows of a call whose scores end behind 4 GB."""
     B, H, Lq, Lk = 9, 4, 2048, 16384 + 8
     x = torch.empty((B, H, Lq, Lk), dtype=torch.bfloat16, device="cuda")
     x.view(-1)[:1 << 20].normal_()
@@ -302,12 +319,14 @@ def test_rows_past_two_to_the_thirty_two_bytes():
         x[b] = x.view(-1)[:1 << 20].repeat(H * Lq * Lk // (1 << 20) + 1)[:H * Lq * Lk].view(H, Lq, Lk)
     x[-1, -1, -3:].normal_()
     table = torch.randn(32, H).bfloat16().cuda()
-    last = x[-1:, -1:, -3:].clone()
-    at = torch.tensor([Lq - 3], dtype=torch.int32, device="cuda")
-    want, kept = ln.softmax_rel_fwd(last, table[:, -1:].contiguous(), q_pos=at, ckpt=True)
-    wdx, _ = ln.softmax_rel_bwd(last, kept, table[:, -1:].contiguous(), q_pos=at)
+    last = to64(x[-1:, -1:, -3:])
+    y64, tol, bk, kept = relref.fwd(last, to64(table)[:, -1:], relref.edges_of(32, 128, True), True, q_pos=[Lq - 3])
     y, ck = ln.softmax_rel_fwd(x, table, y=x, ckpt=True)
-    assert torch.equal(y[-1:, -1:, -3:], want) and torch.equal(ck.q[-3:], kept.q)
-    y[-1, -1, -3:] = last[0, 0]
+    mine = y[-1:, -1:, -3:].clone()
+    relref.close("y", to64(mine), y64, relref.stored(tol, y64, "bf16"))
+    q, k, values = relref.quantise(to64(mine.view(3, Lk)))
+    assert (ck.q[-3:].cpu().numpy() == q).all() and (ck.k[-3:].cpu().numpy() == k).all()
+    y[-1, -1, -3:] = torch.from_numpy(last[0, 0]).to(torch.bfloat16).cuda()
     dx, _ = ln.softmax_rel_bwd(y, ck, table, dx=y)
-    assert torch.equal(dx[-1:, -1:, -3:], wdx)
+    want, tol = relref.bwd(last, values.reshape(last.shape), bk, kept, 32)[:2]
+    relref.close("dx", to64(dx[-1:, -1:, -3:]), want, relref.stored(tol, want, "bf16"))
