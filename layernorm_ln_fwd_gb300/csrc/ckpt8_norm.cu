@@ -22,10 +22,12 @@
 namespace lnk {
 namespace {
 
-// Rows of a team in shared memory or on their way there: 2 to 4, as many as fit beside gamma.
+// Rows of a team in shared memory or on their way there: 3, in fp32 2, where they fit beside gamma.  More do no
+// good: LayerNorm, bf16 65536 x 768, with 2, 3, 4: 54.5, 53.1, 53.8 us; 65536 x 1001 125, 129, 137; RMSNorm, fp32 4096
+// x 4096 32.4, 38.5, 39.9.
 __host__ __device__ constexpr int cn_stages(int lanes, int teams, int nv, int V) {
     const int gamma = lanes * nv * V * 4, row = teams * ((lanes * nv + 1) * 16 + lanes * nv * V);
-    return gamma + 4 * row <= 220 * 1024 ? 4 : gamma + 3 * row <= 220 * 1024 ? 3 : 2;
+    return V == 8 && gamma + 3 * row <= 220 * 1024 ? 3 : 2;
 }
 
 struct CnParams {

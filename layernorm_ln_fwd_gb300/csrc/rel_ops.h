@@ -47,7 +47,7 @@ struct RelShape {
 constexpr RelShape kRelShapes[] = {{256, 1, 1, false}, {256, 1, 2, false}, {256, 1, 4, false}, {512, 1, 4, false},
                                    {512, 1, 4, true}, {32, 8, 1, false}, {32, 8, 2, false}, {32, 8, 4, false},
                                    {64, 4, 4, false}, {32, 1, 2, false}, {8, 32, 1, false}, {8, 32, 2, false},
-                                   {16, 16, 2, false}, {16, 16, 4, false}};
+                                   {16, 16, 2, false}, {16, 16, 4, false}, {128, 2, 4, false}};
 constexpr int kRelShapeCount = sizeof(kRelShapes) / sizeof(kRelShapes[0]);
 
 // The window in shared memory as slots (rel_softmax.cuh): how many, and groups of V entries of each.
@@ -61,7 +61,7 @@ constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch u
 // The distances a call's window has to hold.
 void rel_span(const RelArgs& a, int* dlo, int* dhi);
 // The kernel's shape, and whether its window is in slots, for vectors of V elements.
-int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots);
+int rel_shape(int V, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots);
 
 // The shape for shifted rows and the slots that it has, or -1.
 int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies);

@@ -159,13 +159,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+
 // How rows lie.  kRelWhole: at multiples of 16 bytes, of whole vectors.  kRelShifted: the rows of all tensors
 // start at the same place in 16 bytes, and lanes hold the aligned chunks: column c of a row that starts `sh`
 // elements into a chunk is "place" c + sh, and its position p counts as p + sh, so that the distances are the
-// same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else, moved into columns.
+// same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else (tensors that lie differently,
+// checkpoints of rows that are not of whole vectors, rows in tiles), moved into columns: two loads a vector and its
+// stores put together from two lanes'.  bf16 16 x 12 x 501 x 501: 46 us shifted, 70 moved; backward 86 and 92.
 constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
 
-// Blocks an SM that the registers are to allow.
+// Blocks an SM that the registers are to allow (rel_shape has figures; rows that are moved hold two chunks a vector).
 constexpr int rel_resident(int lanes, int teams, int nv, int mode) {
     if (lanes * teams != 256) return 1;
     const int most = nv == 4 ? 3 : 4;
@@ -203,11 +206,12 @@ __device__ __forceinline__ float rel_factor(float m, float M) {
 // The window in shared memory.
 //
 // Slots: for windows of up to kRelSlotBytes.  A row at position p meets distance d in column d + p, so that its
-// vectors of V columns start at one residue of V throughout, and rows 8 positions apart at the same.  The window
-// is kept 8 times (a row has slot p % 8), each moved so that its rows' vectors are groups of V consecutive
+// vectors of V columns start at one residue of V throughout, and rows V positions apart at the same.  The window
+// is kept SLOTS times (a row has slot p % SLOTS), each moved so that its rows' vectors are groups of V consecutive
 // entries: a vector is V / 4 loads of 128 bits, one after another over the lanes, at a group held between the
-// first and the last, which are the far ends' throughout.  A team's rows come every TEAMS positions, and TEAMS
-// divides 8: in the backward each slot is added to by one team alone.
+// first and the last, which are the far ends' throughout.  SLOTS is 8, or TEAMS where that is more: a team's rows
+// come every TEAMS positions, and TEAMS divides SLOTS, so that in the backward each slot is added to by one team
+// alone.  The backward's shifted rows (below), whose residue is not their position's, have V slots for each team.
 //
 // Entry t of a slot stands for distance dlo + t + residue - (2 V - 1): group 0 ends before dlo whatever the
 // residue, and the last group begins at dhi or behind.  The groups' first halves come first, then their second
@@ -350,6 +354,11 @@ struct RelWindow {
 // LPR lanes (of 1 to 16 warps, or a part of one) hold a row, NV vectors each (lane l: vectors l, l + LPR, ...);
 // TEAMS rows at a time.  The next row's loads are under way during the current one's arithmetic, but for kRelAny.
 // LOOP: rows of any length, in tiles of that size, twice.
+//
+// One read of the scores, one write of the probabilities: bf16 16 x 12 x 512 x 512 with lengths 34.4 us, 0.81 of the
+// measured copy rate; in full 0.86.  What is left is issue: a vector is unpacked, given its bias (two 128-bit shared loads),
+// 8 exponents, and packed.  A decode step (bf16 64 x 16 x 1 x 4096 with lengths) takes 6.8 us for 2.3 of traffic: a launch,
+// and a row's time from its first load to its last store.
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
 __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)) rel_fwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
@@ -639,6 +648,12 @@ __device__ __forceinline__ f2 where_weight(f2 y, f2 g) {
     return f2_make(f2_lo(y) == 0.f ? 0.f : f2_lo(g), f2_hi(y) == 0.f ? 0.f : f2_hi(g));
 }
 
+// As the forward's.  The next row's dy and y lie in shared memory by the time they are wanted, each lane's copied
+// by itself (cp.async: no registers hold them meanwhile, and no barrier is needed), for rows of whole vectors: bf16
+// 12 x 4096 x 4096 189 us, 235 by loads in time; 16 x 12 x 512 x 512 57 and 126.  Shifted rows measured slower so (the
+// end chunks of their two tensors go by other loads, between the copies) and load in time.  bf16 16 x 12 x 512 x 512
+// with lengths and the table's gradient 54.5 us, 0.75 of the measured copy rate; what is left is issue (the window's load,
+// add and store for the vectors that meet it, and integers to fp32 from a checkpoint).
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
 __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)) rel_bwd_kernel(const __grid_constant__ RelParams p) {
     constexpr int V = Io<T>::kVec, H = Pairs<T>::kPairs;
@@ -1013,7 +1028,7 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
                        rel_whole<T>(a.out, a.ldo, a.Lk) && rel_whole<T>(a.mask, a.Lk, a.Lk);
     bool slots;
     int mode = whole ? kRelWhole : kRelAny;
-    int shape = rel_shape(V, rows, a.Lq, a.Lk, span, &slots);
+    int shape = rel_shape(V, a.Lq, a.Lk, span, BWD, a.causal, &slots);
     int copies = rel_slot_count(kRelShapes[shape].teams);
     if (!whole && !a.q && slots && rel_congruent<T>(a.a, a.lda, a.out, a.ldo) &&
         (!a.y || rel_congruent<T>(a.a, a.lda, a.y, a.ldy))) {

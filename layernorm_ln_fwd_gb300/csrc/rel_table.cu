@@ -53,24 +53,38 @@ void rel_span(const RelArgs& a, int* dlo, int* dhi) {
     }
 }
 
-int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool* slots) {
+// Rows of up to 512 vectors go to teams of 4 vectors a lane, several teams a block, so that a block has several rows on
+// their way and only a row's own warps wait for one another; parts of a warp where a row has no use for one.  bf16,
+// 12 heads, forward / backward with the table's gradient, us, beside another shape's:
+//   128 x 128 (x 256 sequences)        8 lanes x 2 37 / 57      a warp x 1                 109 / 123
+//   256 x 256 (x 64)                   16 lanes x 2 36 / 57     a warp x 1                 51 / 64
+//   512 x 512 (x 16)                   16 lanes x 4 34.5 / 57   a warp x 2                 37 / 57
+//   1024 x 1024 (x 4)                  a warp x 4 35 / 58       8 warps x 1                114 / 103
+//   2048 x 2048 (x 2)                  2 warps x 4 72 / 106     8 warps x 1                135 / 127
+//   4096 x 4096                        4 warps x 4 142 / 204    8 warps x 2                172 / 189
+//   the last, causal                                120 / 148                              152 / 157
+// The backward's full rows beyond 384 vectors alone are better off with 8 warps.  Four vectors a lane take 80
+// registers, three blocks an SM (rel_resident): held to 64 they spill, and the same take 34.5 -> 38, 35 -> 40, 72 -> 80.
+int rel_shape(int V, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots) {
     const int nvec = (Lk + V - 1) / V;
     auto fits = [&](int teams) { return rel_slot_count(teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes; };
     *slots = nvec <= 2048 && fits(8);
     if (*slots && Lq < 4 && nvec <= 64) return 9;  // single queries: no teams to fill
-    if (*slots && Lq >= 4 && nvec <= 256) {
+    if (*slots && Lq >= 4 && nvec <= (bwd && !causal ? 384 : 512)) {
         if (nvec <= 16 && fits(32)) return nvec <= 8 ? 10 : 11;
         if (nvec <= 64 && fits(16)) return nvec <= 32 ? 12 : 13;
-        return nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : 8;
+        return nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : nvec <= 256 ? 8 : 14;
     }
     return nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : 4;
 }
 
+// The same for shifted rows (bf16, 12 heads, 501 x 501 x 16: parts of a warp 46 us forward, a warp 56; 4001 x 4001: 4
+// warps 189 / 210, 8 warps 219 / 242).
 int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies) {
     const int nvec = (Lk + V - 1 + V - 1) / V;  // chunks that a row may lie in
     int shape = nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : -1;
     if (Lq < 4 && nvec <= 64) shape = 9;
-    if (Lq >= 4 && nvec <= 256) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : 8;
+    if (Lq >= 4 && nvec <= 512) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : nvec <= 256 ? 8 : 14;
     if (!bwd && Lq >= 4 && nvec <= 64) {  // (in the backward parts of a warp would take too many slots)
         const int parts = nvec <= 16 ? (nvec <= 8 ? 10 : 11) : nvec <= 32 ? 12 : 13;
         if (rel_slot_count(kRelShapes[parts].teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes) shape = parts;

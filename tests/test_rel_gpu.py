@@ -73,7 +73,7 @@ class Case:
 
 SHAPES = [(1, 1, 1, 1), (2, 3, 1, 77), (2, 2, 5, 8), (1, 2, 33, 33), (2, 3, 17, 100), (1, 2, 40, 256), (1, 2, 24, 333),
           (1, 1, 9, 513), (2, 1, 7, 1000), (1, 2, 5, 1032), (1, 2, 6, 2500), (1, 1, 3, 5001), (1, 1, 5, 8192),
-          (1, 1, 4, 16384), (2, 1, 1, 4099), (1, 3, 130, 40)]
+          (1, 1, 4, 16384), (2, 1, 1, 4099), (1, 3, 130, 40), (1, 2, 7, 3600), (1, 1, 9, 2049)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -85,7 +85,7 @@ def test_shapes(dtype, shape, both):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 2, 1, 1), (2, 2, 37, 37), (1, 2, 128, 128), (1, 1, 65, 301), (1, 1, 4, 1100),
-                                   (1, 1, 300, 520)])
+                                   (1, 1, 300, 520), (1, 2, 9, 4000), (1, 1, 6, 2111)])
 def test_causal(dtype, shape):
     Case(dtype, shape, both=False, causal=True, seed=3).check()
     Case(dtype, shape, both=False, causal=True, q_pos=[shape[3] - shape[2]] * shape[0], seed=4).check()
