@@ -11,6 +11,11 @@
 // order and leaves one row of partial sums for each statistic; a second, dependent launch adds those of a column,
 // 32 interleaved groups and then the groups, with their rounding errors carried along.  No atomics: results are the
 // same from run to run.
+//
+// LayerNorm, bf16 65536 x 768: 53 us, 0.70 of the measured copy rate; RMSNorm 4096 x 8192 38.5 us, 0.65, fp32 4096 x 4096 32
+// us, 0.69.  Small calls (8192 x 768: 12.5 us for 4.7 of traffic) are bound by what comes once: the first rows' way, a
+// block's column sums, the second launch.  LayerNorm beyond 24 columns a lane (bf16 4096 x 8192: 52 us, 0.48) by the second
+// conversion of its integers, for which two column sums leave no registers.
 #include <algorithm>
 #include <utility>
 
@@ -350,7 +355,8 @@ struct CnShape {
     int lanes, teams, nv;
 };
 // By capacity: lanes * nv vectors a row.  16 warps a block, one of which an SM holds: 128 registers a lane, and one
-// row of partial sums an SM.
+// row of partial sums an SM.  (Smaller blocks, by loads in time: bf16 8192 x 768 28 us for 12.5; a wide row
+// by 16 warps, one at a time, for two teams of 8: 4096 x 8192 46 us for 38.)
 constexpr CnShape kCnShapes[] = {{32, 16, 1}, {32, 16, 2}, {32, 16, 3}, {32, 16, 4}, {64, 8, 3}, {64, 8, 4},
                                  {128, 4, 3}, {128, 4, 4}, {256, 2, 3}, {256, 2, 4}, {512, 1, 3}, {512, 1, 4}, {512, 1, 8}};
 constexpr int kCnCount = sizeof(kCnShapes) / sizeof(kCnShapes[0]);

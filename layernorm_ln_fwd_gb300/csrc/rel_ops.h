@@ -61,10 +61,10 @@ constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch u
 // The distances a call's window has to hold.
 void rel_span(const RelArgs& a, int* dlo, int* dhi);
 // The kernel's shape, and whether its window is in slots, for vectors of V elements.
-int rel_shape(int V, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots);
+int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots);
 
 // The shape for shifted rows and the slots that it has, or -1.
-int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies);
+int rel_shape_shifted(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, int* copies);
 
 // Bytes of partial sums: a row of buckets for each block and head that it works on.
 size_t rel_workspace_bytes(int H, int buckets, int sms);

@@ -1028,14 +1028,16 @@ cudaError_t launch_rel_t(const RelArgs& a, cudaStream_t stream, int* launches) {
                        rel_whole<T>(a.out, a.ldo, a.Lk) && rel_whole<T>(a.mask, a.Lk, a.Lk);
     bool slots;
     int mode = whole ? kRelWhole : kRelAny;
-    int shape = rel_shape(V, a.Lq, a.Lk, span, BWD, a.causal, &slots);
+    int shape = rel_shape(V, rows, a.Lq, a.Lk, span, BWD, a.causal, &slots);
     int copies = rel_slot_count(kRelShapes[shape].teams);
     if (!whole && !a.q && slots && rel_congruent<T>(a.a, a.lda, a.out, a.ldo) &&
         (!a.y || rel_congruent<T>(a.a, a.lda, a.y, a.ldy))) {
-        const int wide = rel_shape_shifted(V, a.Lq, a.Lk, span, BWD, &copies);
-        if (wide >= 0) {
+        int shifted_copies;
+        const int shifted = rel_shape_shifted(V, rows, a.Lq, a.Lk, span, BWD, &shifted_copies);
+        if (shifted >= 0) {
             mode = kRelShifted;
-            shape = wide;
+            shape = shifted;
+            copies = shifted_copies;
         }
     }
     const RelShape& sh = kRelShapes[shape];

@@ -53,6 +53,15 @@ void rel_span(const RelArgs& a, int* dlo, int* dhi) {
     }
 }
 
+// Few queries a sequence over short rows: a warp a row, one row a block, where there are rows enough for all SMs and the
+// window is one that a warp fills in time; else a block a row, which fills it 8 times as fast.  bf16, one query, 128
+// distances, a warp and a block a row: 96 rows of 210 keys 4.7 and 3.4 us, 1024 of 502 5.2 and 6.4, 8192 of 502 11 and
+// 28; with 800 distances 96 rows of 210 14.7 and 4.6.
+constexpr int kRelNarrow = 300;
+bool rel_single(int Lq, int nvec, int span, int64_t rows) {
+    return Lq < 4 && nvec <= 64 && span <= kRelNarrow && rows > 4 * (int64_t)device_info(-1).sms;
+}
+
 // Rows of up to 512 vectors go to teams of 4 vectors a lane, several teams a block, so that a block has several rows on
 // their way and only a row's own warps wait for one another; parts of a warp where a row has no use for one.  bf16,
 // 12 heads, forward / backward with the table's gradient, us, beside another shape's:
@@ -65,11 +74,11 @@ void rel_span(const RelArgs& a, int* dlo, int* dhi) {
 //   the last, causal                                120 / 148                              152 / 157
 // The backward's full rows beyond 384 vectors alone are better off with 8 warps.  Four vectors a lane take 80
 // registers, three blocks an SM (rel_resident): held to 64 they spill, and the same take 34.5 -> 38, 35 -> 40, 72 -> 80.
-int rel_shape(int V, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots) {
+int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots) {
     const int nvec = (Lk + V - 1) / V;
     auto fits = [&](int teams) { return rel_slot_count(teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes; };
     *slots = nvec <= 2048 && fits(8);
-    if (*slots && Lq < 4 && nvec <= 64) return 9;  // single queries: no teams to fill
+    if (*slots && rel_single(Lq, nvec, span, rows)) return 9;
     if (*slots && Lq >= 4 && nvec <= (bwd && !causal ? 384 : 512)) {
         if (nvec <= 16 && fits(32)) return nvec <= 8 ? 10 : 11;
         if (nvec <= 64 && fits(16)) return nvec <= 32 ? 12 : 13;
@@ -80,10 +89,10 @@ int rel_shape(int V, int Lq, int Lk, int span, bool bwd, bool causal, bool* slot
 
 // The same for shifted rows (bf16, 12 heads, 501 x 501 x 16: parts of a warp 46 us forward, a warp 56; 4001 x 4001: 4
 // warps 189 / 210, 8 warps 219 / 242).
-int rel_shape_shifted(int V, int Lq, int Lk, int span, bool bwd, int* copies) {
+int rel_shape_shifted(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, int* copies) {
     const int nvec = (Lk + V - 1 + V - 1) / V;  // chunks that a row may lie in
     int shape = nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : -1;
-    if (Lq < 4 && nvec <= 64) shape = 9;
+    if (rel_single(Lq, nvec, span, rows)) shape = 9;
     if (Lq >= 4 && nvec <= 512) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : nvec <= 256 ? 8 : 14;
     if (!bwd && Lq >= 4 && nvec <= 64) {  // (in the backward parts of a warp would take too many slots)
         const int parts = nvec <= 16 ? (nvec <= 8 ? 10 : 11) : nvec <= 32 ? 12 : 13;

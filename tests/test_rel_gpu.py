@@ -109,6 +109,23 @@ def test_rows_longer_than_the_registers_hold(dtype, Lk):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("span", [400, 800, 1200, 2500, 6000, 16384])
+@pytest.mark.parametrize("shape", [(1, 2, 9, 527), (1, 1, 5, 1501), (2, 1, 1, 331), (1, 1, 40, 101), (1, 1, 6, 1504)])
+def test_wide_windows(dtype, span, shape):
+    q_pos = [shape[3] // 2] * shape[0]  # (the whole window, whatever the rows' length)
+    Case(dtype, shape, span=span, q_pos=q_pos, seed=13).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lq,Lk", [(1, 17), (1, 256), (3, 200), (1, 251)])
+@pytest.mark.parametrize("span", [128, 700])
+def test_many_single_queries(dtype, Lq, Lk, span):
+    lens = [(37 * b) % (Lk + 3) for b in range(100)]
+    Case(dtype, (100, 8, Lq, Lk), span=span, both=False, lens=lens, q_pos=[n - Lq for n in lens], seed=11).check()
+    Case(dtype, (100, 8, Lq, Lk), span=span, both=False, causal=True, seed=12, pad=3, offset=1).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 3, 1, 70001), (2, 1, 1, 140000), (1, 80, 1, 16400), (1, 2, 90, 16600)])
 def test_few_long_rows(dtype, shape):
     B, H, Lq, Lk = shape
