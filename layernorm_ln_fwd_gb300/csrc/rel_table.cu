@@ -88,13 +88,17 @@ int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, bool caus
 }
 
 // The same for shifted rows (bf16, 12 heads, 501 x 501 x 16: parts of a warp 46 us forward, a warp 56; 4001 x 4001: 4
-// warps 189 / 210, 8 warps 219 / 242).
+// warps 189 / 210, 8 warps 219 / 242).  In the backward a warp holds a row at least: parts of one would take too many
+// slots.  In bf16 rows of up to 32 vectors are better moved, by parts of a warp (32 heads, shifted and moved: 32 x
+// 65 x 65 49 and 35 us, 16 x 138 x 138 causal 49 and 42, 16 x 201 x 201 66 and 61, 8 x 283 x 283 causal 57 and 56, 8 x 501 x
+// 501 causal 93 and 104; fp32 16 x 101 x 101 28 and 28, 8 x 201 x 201 37 and 46).
 int rel_shape_shifted(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, int* copies) {
+    if (bwd && V == 8 && Lk <= 32 * V) return -1;
     const int nvec = (Lk + V - 1 + V - 1) / V;  // chunks that a row may lie in
     int shape = nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : -1;
     if (rel_single(Lq, nvec, span, rows)) shape = 9;
     if (Lq >= 4 && nvec <= 512) shape = nvec <= 32 ? 5 : nvec <= 64 ? 6 : nvec <= 128 ? 7 : nvec <= 256 ? 8 : 14;
-    if (!bwd && Lq >= 4 && nvec <= 64) {  // (in the backward parts of a warp would take too many slots)
+    if (!bwd && Lq >= 4 && nvec <= 64) {
         const int parts = nvec <= 16 ? (nvec <= 8 ? 10 : 11) : nvec <= 32 ? 12 : 13;
         if (rel_slot_count(kRelShapes[parts].teams) * rel_groups(span, V) * V * 4 <= kRelSlotBytes) shape = parts;
     }
