@@ -583,6 +583,9 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
             const f2 c2 = f2_splat(inv);
             T* y = rel_at<T>(p.out, row, p.ldo);
             const int stored = L == 32 || ok ? sh + p.Lk : 0;
+            // The warp's last place: rows that share a warp start at different places of a chunk, and all lanes take
+            // part in a piece's stores.
+            const int reach = SHIFT && L < 32 ? __reduce_max_sync(kFullMask, sh + p.Lk) : sh + p.Lk;
             for (int base = LOOP ? rank * kTile : 0; base < (LOOP ? p.Lk : 1); base += cluster * kTile) {
                 RowOut<T, L> out;
                 if constexpr (LOOP) {
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int from = base + place_of(k) * V, col = from + lane * V;
-                    if (from >= sh + p.Lk) continue;
+                    if (from >= reach) continue;
                     uint4 u = make_uint4(0, 0, 0, 0);
                     if (from < most) {
 #pragma unroll

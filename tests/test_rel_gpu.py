@@ -347,3 +347,16 @@ def test_rows_past_two_to_the_thirty_two_bytes():
     dx, _ = ln.softmax_rel_bwd(y, ck, table, dx=y)
     want, tol = relref.bwd(last, values.reshape(last.shape), bk, kept, 32)[:2]
     relref.close("dx", to64(dx[-1:, -1:, -3:]), want, relref.stored(tol, want, "bf16"))
+
+
+@pytest.mark.parametrize("dtype,widths", [("bf16", (*range(57, 65), *range(121, 129), *range(249, 257), *range(377, 385))),
+                                          ("f32", (*range(29, 33), *range(61, 65), *range(125, 129), *range(189, 193)))])
+def test_rows_that_end_around_a_piece_and_share_a_warp(dtype, widths):
+    """Rows held by parts of a warp, their ends on either side of a piece by where in 16 bytes they start."""
+    for Lk in widths:
+        for pad, how in ((0, {}), (1, dict(lens=[Lk, Lk - 2])), (3, dict(both=False, causal=True, q_pos=[Lk - 9, Lk - 3]))):
+            c = Case(dtype, (2, 3, 9, Lk), span=24, pad=pad, seed=Lk, **how)
+            whole = torch.full((2, 3, 9, Lk + pad), 7.0, dtype=TYPES[dtype], device="cuda")
+            y, _ = ln.softmax_rel_fwd(c.x, c.table, y=whole[..., :Lk], **c.how)
+            c.check_fwd(y)
+            assert (whole[..., Lk:] == 7).all()
