@@ -189,11 +189,19 @@ __device__ __forceinline__ float rel_warp_sum(float a) {
     return a;
 }
 
-// 1 / s to one unit in the last place (s >= 1 but for what is infinite or NaN).
+// 1 / s to one unit in the last place (s >= 1/2 but for what is infinite or NaN).
 __device__ __forceinline__ float rcp_fast(float s) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     return r;
+}
+
+// The weights of a warp (or tile) whose largest score is m are formed as exp2(z log2 e - p), p = m log2 e as rounded: the
+// factor exp2(p - m log2 e) that all of them lack.  A row of one warp does without it, since it cancels; the sums of
+// several warps, of which each has its own, are given it before they meet.  1 for an m that is subtracted first (`weights`).
+constexpr float kRelLarge = 16777216.f;
+__device__ __forceinline__ float rel_fix(float m) {
+    return fabsf(m) < kRelLarge ? ex2_fast(-__fmaf_rn(m, kRelLog2e, -__fmul_rn(m, kRelLog2e))) : 1.f;
 }
 
 // exp2((m - M) log2 e), the factor from sums taken against m to those against M >= m; 1 for a sum that
@@ -500,12 +508,12 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
                 }
                 return m;
             };
-            // z becomes exp(z - m); returns its sum.  exp2(z log2 e - m log2 e): the last product's rounding
-            // is the same for the whole row and cancels.  For an m whose rounding could pass fp32's exponents,
+            // z becomes exp(z - m), but for the factor rel_fix(m); returns its sum.  exp2(z log2 e - m log2 e): the last
+            // product's rounding is the same for the whole warp.  For an m whose rounding could pass fp32's exponents,
             // z - m first.
             auto weights = [&](float m, int base) {
                 float ref = m == -INFINITY ? 0.f : m;
-                if (!(fabsf(ref) < 16777216.f)) {
+                if (!(fabsf(ref) < kRelLarge)) {
 #pragma unroll
                     for (int k = 0; k < NV; ++k) {
                         if (base + place_of(k) * V >= most) continue;
@@ -514,7 +522,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
                     }
                     ref = 0.f;
                 }
-                const f2 nr = f2_splat(-ref * kRelLog2e);
+                const f2 nr = f2_splat(__fmul_rn(-ref, kRelLog2e));
                 f2 acc = f2_splat(0.f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
@@ -535,7 +543,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
                     const float mt = fmaxf(m, rel_warp_max<L>(scores(base)));
                     s *= rel_factor(m, mt);
                     m = mt;
-                    s += weights(m, base);
+                    s += weights(m, base) * rel_fix(m);
                 }
             } else {
                 m = scores(0);
@@ -554,9 +562,10 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
             if constexpr (W == 1) {
                 inv = s == 0.f ? 0.f : rcp_fast(s);
             } else {  // the warps' (max, sum) meet once
+                const float fix = rel_fix(m);
                 if (lane == 0) {
                     red[parity][team][0][wt] = m;
-                    red[parity][team][1][wt] = s;
+                    red[parity][team][1][wt] = LOOP ? s : s * fix;
                 }
                 team_sync<W, TEAMS>(team);
                 float M = -INFINITY, S = 0.f;
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
                     for (int i = 0; i < cluster; ++i) M = fmaxf(M, joint[parity][i].x);
                     for (int i = 0; i < cluster; ++i) S += joint[parity][i].y * rel_factor(joint[parity][i].x, M);
                 }
-                inv = S == 0.f ? 0.f : rel_factor(m, M) / S;
+                inv = S == 0.f ? 0.f : fix * rel_factor(m, M) / S;
                 parity ^= 1;
             }
             const f2 c2 = f2_splat(inv);

@@ -159,3 +159,18 @@ def close(name, got, want, tol):
         i = np.unravel_index(np.argmax(bad), bad.shape)
         raise AssertionError(f"{name}: {bad.sum()} of {bad.size} out of tolerance; first at {i}: got {got[i]!r}, want "
                              f"{np.broadcast_to(want, got.shape)[i]!r}, tolerance {np.broadcast_to(tol, got.shape)[i]!r}")
+
+
+def exact_scores_tol(y, z, Lk):
+    """fwd's tolerance before the store where the scores z are exact in fp32 (-inf: no key), whatever their magnitude.
+
+    A weight's exponent is z log2 e less the product m log2 e of its warp's largest, as rounded: a rounding of at most
+    1.45 (m - z) + 1 (half a step of a product below 2^25); the factor between two warps, exp2((m - top) log2 e), has two,
+    of 1.45 (top - m) each: together u (2 (top - z) + 0.7) of the weight; log2 e itself is off by 0.23 u: as much of
+    (top - z) again; the approximate exponent 4 u.  From 2^24 on the largest is subtracted first: two roundings of
+    the differences, 2 u (top - z).  The sum's chain as in fwd, the factors of a warp (two exponents, three products) in it."""
+    with np.errstate(all="ignore"):
+        top = z.max(axis=3, keepdims=True)
+        far = np.where(y > 0, np.where(top == -np.inf, 0, top) - z, 0)
+    rel = U * (3 * far + 7)
+    return y * (rel + (y * rel).sum(axis=3, keepdims=True) + U * (192 + Lk / 512)) + np.where(z > -np.inf, 2.0 ** -125, 0)

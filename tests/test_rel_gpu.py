@@ -360,3 +360,35 @@ def test_rows_that_end_around_a_piece_and_share_a_warp(dtype, widths):
             y, _ = ln.softmax_rel_fwd(c.x, c.table, y=whole[..., :Lk], **c.how)
             c.check_fwd(y)
             assert (whole[..., Lk:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 2, 6, 100), (1, 2, 7, 333), (1, 2, 5, 1000), (1, 1, 9, 1501), (1, 1, 4, 2048), (1, 1, 3, 4096),
+                                   (1, 1, 5, 4001), (1, 1, 2, 8192), (1, 1, 2, 20001), (1, 1, 1, 70001)])
+def test_scores_of_large_magnitude(dtype, shape):
+    """Scores a few units apart around a common offset, as an additive mask gives it or the scores themselves have it,
+    exact in fp32: the probabilities are those of the scores without it, at any magnitude and any number of warps."""
+    B, H, Lq, Lk = shape
+    g = torch.Generator().manual_seed(Lk)
+    for offset in (0.0, 1000.0, -9984.0, 99840.0, -999424.0, 8126464.0, 2.0 ** 24, -2.0 ** 24, 2.0 ** 26):
+        step = max(0.125, 2.0 ** -23 * 2.0 ** np.ceil(np.log2(2 * abs(offset) + 1)))
+        units = lambda n, *s: torch.randint(-n, n + 1, s, generator=g) * step  # noqa: E731
+        span = max(2, int(6 / step))
+        x = units(span, *shape).to(TYPES[dtype])
+        x[..., :Lk // 3] -= 4 * step  # (the warps' largest differ)
+        table = units(2, 32, H).to(TYPES[dtype])
+        mask = torch.full((1, Lk), offset)
+        mask[:, 5::11] = -torch.inf
+        z = to64(x) + np.moveaxis(to64(table)[relref.buckets_of(relref.taking_part(B, Lq, Lk, False, None, None)[0],
+                                                                relref.edges_of(32, 128, True), True)], 3, 1)
+        z = z + mask.double().numpy()
+        assert (z == z.astype(np.float32)).all()
+        e = np.exp(z - z.max(axis=3, keepdims=True))
+        want = e / e.sum(axis=3, keepdims=True)
+        tol = relref.stored(relref.exact_scores_tol(want, z, Lk), want, dtype)
+        got = ln.softmax_rel_fwd(x.cuda(), table.cuda(), mask=mask.to(TYPES[dtype]).cuda())[0]
+        relref.close(f"offset {offset}", to64(got), want, tol)
+        if dtype == "f32":
+            moved = (x.double() + mask.double()).float().cuda()
+            got = ln.softmax_rel_fwd(moved, table.cuda())[0]
+            relref.close(f"scores around {offset}", to64(got), want, tol)
