@@ -851,14 +851,35 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
             if constexpr (!LOOP) load(0);
             float s = row_sum(std::false_type{});
             // A sum that is not finite (an infinite or NaN dy, perhaps at a key of weight 0, where it must
-            // not count) is formed again without such keys.
-            const bool careful = L < 32 ? __any_sync(kFullMask, !(fabsf(s) < INFINITY)) : !(fabsf(s) < INFINITY);
-            if (careful) s = row_sum(std::true_type{});
+            // not count) is formed again without such keys.  From 2^103 on its difference from a finite dy may pass fp32's
+            // range: halves are subtracted there.
+            constexpr float kFar = 0x1p103f;
+            const bool careful = L < 32 ? __any_sync(kFullMask, !(fabsf(s) < kFar)) : !(fabsf(s) < kFar);
+            bool far = false;
+            auto halve = [&] {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    f2 d[H];
+                    Pairs<T>::unpack(g[k], d);
+#pragma unroll
+                    for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_mul(d[h2], f2_splat(0.5f));
+                    g[k] = Pairs<T>::pack(d);
+                }
+            };
+            if (careful) {
+                s = row_sum(std::true_type{});
+                far = !(fabsf(s) < kFar);
+                if (far) {
+                    s *= 0.5f;
+                    if (!LOOP) halve();
+                }
+            }
             if constexpr (STAGED) issue(ahead);  // (what was there has been used)
             const f2 s2 = f2_splat(s);
             for (int base = 0; base < (LOOP ? p.Lk : 1); base += kTile) {
                 RowOut<T, L> out;
                 if constexpr (LOOP) load(base);
+                if (LOOP && far) halve();
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int from = base + place_of(k) * V, col = from + lane * V;
@@ -871,6 +892,10 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
 #pragma unroll
                         for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_mul(y[h2], f2_sub(d[h2], s2));
                         if (careful) {
+                            if (far) {
+#pragma unroll
+                                for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_add(d[h2], d[h2]);
+                            }
 #pragma unroll
                             for (int h2 = 0; h2 < H; ++h2) {
                                 d[h2] = where_weight(y[h2], d[h2]);

@@ -392,3 +392,23 @@ def test_scores_of_large_magnitude(dtype, shape):
             moved = (x.double() + mask.double()).float().cuda()
             got = ln.softmax_rel_fwd(moved, table.cuda())[0]
             relref.close(f"scores around {offset}", to64(got), want, tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Lk", [48, 99, 203, 1200, 20001])
+def test_gradients_near_the_types_largest(dtype, Lk):
+    """dy - sum dy y passes fp32's range, at keys of probability 0, where it counts for nothing, and at others, where
+    its product with y does not."""
+    mask = torch.zeros(1, Lk)
+    mask[:, 5::7] = -float("inf")
+    c = Case(dtype, (1, 2, 5, Lk), mask=mask, seed=26)
+    c.dy[..., :3] *= 2.0 ** 100
+    c.dy[:, :, 1:3] = c.dy[:, :, 1:3].abs().clamp(1, 2) * -2.0 ** 126
+    c.dy[..., 5::7] = 3e38
+    c.dy[:, :, 2, 7] = 3e38
+    y, ck = ln.softmax_rel_fwd(c.x, c.table, mask=c.mask, ckpt=True, **c.how)
+    c.check_bwd(ln.softmax_rel_bwd(c.dy, y, c.table, **c.how), to64(y))
+    kept = relref.quantise(to64(y).reshape(-1, Lk))[2].reshape(c.shape)
+    c.check_bwd(ln.softmax_rel_bwd(c.dy, ck, c.table, **c.how), kept, "kept ")
+    dx, dt = ln.softmax_rel_bwd(c.dy, y, c.table, **c.how)
+    assert dx.isfinite().all() and dt.isfinite().all()
