@@ -628,21 +628,38 @@ class Ckpt8(NamedTuple):
 _binding = None
 
 
+class _NoBinding:
+    """In the extension module's place: takes no call, so that each goes the Python way."""
+
+    @staticmethod
+    def _none(*_):
+        return None
+
+    store = load = norm_bwd = rel_fwd = rel_bwd = edges = _none
+
+
 def _load_binding():
-    """The extension module ``_binding.so`` (csrc/binding.cpp) with the library's entry points handed over."""
+    """The extension module (csrc/binding.cpp) of this torch and Python with the library's entry points handed over; where
+    there is none, :class:`_NoBinding` and a warning: the same calls, at two to three times the host's time."""
     global _binding
     import importlib.util
+    import warnings
 
     import torch  # noqa: F401  (the module's symbols are torch's)
+
+    from .build import binding_path
     cdll = lib()
-    path = os.path.join(_HERE, "_binding.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with `python -m layernorm_ln_fwd_gb300.build`")
-    spec = importlib.util.spec_from_file_location("layernorm_ln_fwd_gb300._binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.init({name: ctypes.cast(getattr(cdll, name), _P).value for name in SIGNATURES
-                 if "softmax_rel" in name or "ckpt8" in name})
+    path = binding_path()
+    try:
+        spec = importlib.util.spec_from_file_location("layernorm_ln_fwd_gb300._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init({name: ctypes.cast(getattr(cdll, name), _P).value for name in SIGNATURES
+                     if "softmax_rel" in name or "ckpt8" in name})
+    except (ImportError, OSError) as e:
+        warnings.warn(f"calls go through ctypes ({e}): `python -m layernorm_ln_fwd_gb300.build` makes the extension module",
+                      RuntimeWarning, stacklevel=3)
+        module = _NoBinding
     _binding = module
     return module
 

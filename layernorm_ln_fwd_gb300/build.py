@@ -3,7 +3,8 @@
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then the objects are linked
 into ``layernorm_ln_fwd_gb300/libln.so`` (CUDA runtime linked statically).  Register and
 shared-memory usage reported by ptxas is kept in ``_build/ptxas.log``.  Beside it ``csrc/binding.cpp``
-becomes the extension module ``_binding.so`` (g++, torch's headers).
+becomes the extension module ``_binding_*.so`` of the torch and Python that are here (g++, torch's headers).  The
+library needs neither; without the module the Python binding makes the same calls through ctypes.
 
 Usage: ``python -m layernorm_ln_fwd_gb300.build [--force]``.
 """
@@ -11,7 +12,9 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -22,7 +25,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libln.so")
-BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -45,10 +47,28 @@ def _deps():
         glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "ln.h"), __file__]
 
 
+def binding_path() -> str | None:
+    """Where the extension module for the torch and the Python that are here belongs, or None without a torch.  Its
+    name has both versions: a module built against others is not this one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+    return os.path.join(PKG, "_binding_" + re.sub(r"\W", "_", f"{version}_{sys.implementation.cache_tag}") + ".so")
+
+
+def _built() -> list:
+    """What a build makes here: the library, and the extension module where it can be built."""
+    binding = binding_path() if shutil.which("g++") else None
+    return [LIB] + ([binding] if binding else [])
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+    made = _built()
+    if not all(os.path.exists(m) for m in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -61,7 +81,7 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
-def _compile_binding() -> str:
+def _compile_binding(path: str) -> str:
     """The extension module, against the torch that is here; returns its temporary name."""
     import sysconfig
 
@@ -69,7 +89,7 @@ def _compile_binding() -> str:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
@@ -86,10 +106,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
+    binding = (_built() + [None])[1]
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        binding = ex.submit(_compile_binding)
+        module = ex.submit(_compile_binding, binding) if binding else None
         results = list(ex.map(_compile, srcs))
-        binding = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for (obj, log) in results:
             f.write(f"==== {os.path.basename(obj)}\n{log}\n")
@@ -99,9 +119,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(binding, BINDING)
+    if module:  # (whatever comes of it, the library is there)
+        os.replace(module.result(), binding)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}" + ("" if module else " (no g++ or no torch: without the extension module)"))
     return LIB
 
 

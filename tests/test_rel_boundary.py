@@ -210,3 +210,60 @@ def test_binding_refuses():
                 lambda: ln.softmax_rel_bwd(x, x.bfloat16(), table)):
         with pytest.raises(TypeError):
             bad()
+
+
+@pytest.mark.parametrize("content", [None, b"not a module"])
+def test_calls_without_the_extension_module(monkeypatch, tmp_path, content):
+    """Where it was not built, or for another torch, a call goes through ctypes and says so once."""
+    path = tmp_path / "_binding_other.so"
+    if content:
+        path.write_bytes(content)
+    monkeypatch.setattr(lnbuild, "binding_path", lambda: str(path))
+    monkeypatch.setattr(ln, "_binding", None)
+    x, table = torch.zeros(2, 3, 4, 8), torch.zeros(8, 3)
+    with pytest.warns(RuntimeWarning, match="ctypes"), pytest.raises(ValueError, match="CUDA"):
+        ln.ckpt8_store(x[0, 0])
+    ck = ln.Ckpt8(torch.zeros(24, 32, dtype=torch.int8), torch.zeros(24, 1, dtype=torch.uint8), 8)
+    for call in (lambda: ln.softmax_rel_fwd(x, table), lambda: ln.softmax_rel_bwd(x, ck, table, 40), lambda: ln.ckpt8_load(ck),
+                 lambda: ln.rms_bwd_ckpt8(x.view(24, 8), ck, x[0, 0, 0], torch.zeros(24))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+def test_the_extension_module_is_of_this_torch(lib, monkeypatch, tmp_path):
+    mine = lnbuild.binding_path()
+    assert lnbuild.up_to_date() and lnbuild._built() == [lnbuild.LIB, mine]
+    (tmp_path / "__init__.py").write_text("")
+    (tmp_path / "version.py").write_text("from typing import Optional\n__version__ = '99.1.0+cu999'\n")
+    spec = lnbuild.importlib.util.spec_from_file_location("torch", str(tmp_path / "__init__.py"))
+    with monkeypatch.context() as m:  # another torch
+        m.setattr(lnbuild.importlib.util, "find_spec", lambda name: spec)
+        assert "99_1_0_cu999" in lnbuild.binding_path() and lnbuild.binding_path() != mine and not lnbuild.up_to_date()
+    with monkeypatch.context() as m:  # none, or no compiler of C++: the library alone
+        m.setattr(lnbuild.importlib.util, "find_spec", lambda name: None)
+        assert lnbuild.binding_path() is None and lnbuild._built() == [lnbuild.LIB] and lnbuild.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(lnbuild.shutil, "which", lambda name: None)
+        assert lnbuild._built() == [lnbuild.LIB] and lnbuild.up_to_date()
+
+
+def test_the_library_is_built_whatever_comes_of_the_module(monkeypatch, tmp_path):
+    monkeypatch.setattr(lnbuild, "LIB", str(tmp_path / "libln.so"))
+    monkeypatch.setattr(lnbuild, "BUILD", str(tmp_path))
+    monkeypatch.setattr(lnbuild, "_compile", lambda src: (src + ".o", ""))
+    monkeypatch.setattr(lnbuild, "nvcc", lambda: "nvcc")
+
+    def link(cmd, **_):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return lnbuild.subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(lnbuild.subprocess, "run", link)
+
+    def fails(path):
+        raise RuntimeError("g++ failed")
+    monkeypatch.setattr(lnbuild, "_compile_binding", fails)
+    with pytest.raises(RuntimeError, match=r"g\+\+ failed"):
+        lnbuild.build(force=True)
+    assert (tmp_path / "libln.so").exists()
+    (tmp_path / "libln.so").unlink()
+    monkeypatch.setattr(lnbuild.shutil, "which", lambda name: None)
+    assert lnbuild.build(force=True) == str(tmp_path / "libln.so") and (tmp_path / "libln.so").exists()

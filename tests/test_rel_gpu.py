@@ -412,3 +412,20 @@ def test_gradients_near_the_types_largest(dtype, Lk):
     c.check_bwd(ln.softmax_rel_bwd(c.dy, ck, c.table, **c.how), kept, "kept ")
     dx, dt = ln.softmax_rel_bwd(c.dy, y, c.table, **c.how)
     assert dx.isfinite().all() and dt.isfinite().all()
+
+
+def test_the_same_without_the_extension_module(monkeypatch):
+    c = Case("bf16", (2, 3, 50, 161), lens=[161, 90], seed=27)
+
+    def calls():
+        y, ck = ln.softmax_rel_fwd(c.x, c.table, ckpt=True, **c.how)
+        mean = rstd = torch.ones(300, device="cuda")
+        norm = ln.bwd_ckpt8(c.dy.view(300, 161), ck, c.x[0, 0, 0], mean, rstd)
+        rms = ln.rms_bwd_ckpt8(c.dy.view(300, 161), ck, c.x[0, 0, 0], rstd)
+        return [y, ck.q, ck.k, *ln.softmax_rel_bwd(c.dy, ck, c.table, **c.how), *ln.softmax_rel_bwd(c.dy, y, c.table, **c.how),
+                ln.ckpt8_load(ck), *ln.ckpt8_store(c.x.view(300, 161))[:2], *norm, *rms]
+    want = calls()
+    assert ln._binding is not ln._NoBinding
+    monkeypatch.setattr(ln, "_binding", ln._NoBinding)
+    got = calls()
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
