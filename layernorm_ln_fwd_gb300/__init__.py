@@ -981,8 +981,8 @@ def softmax_rel_bwd(dy, y, table, max_distance: int = 128, bidirectional: bool =
     """Gradients of :func:`softmax_rel_fwd`: dx = scale * dS with dS = y (dy - sum dy y), and dtable, the
     sum of dS over all pairs of a bucket, in the table's type.  y: the forward's, or its :class:`Ckpt8`;
     the other arguments as the forward had them (what ``causal`` and lens removed is not read).  ``dx`` may be
-    dy.  Returns (dx, dtable); dtable is None without ``want_table``.  ``workspace``: as many bytes as
-    ``ln_softmax_rel_workspace_bytes_*`` says, of any content, by default allocated for the call."""
+    dy.  Returns (dx, dtable); dtable is None without ``want_table``.  ``workspace``: at least
+    :func:`softmax_rel_workspace_bytes` bytes of any content, by default allocated for the call."""
     import torch
     if dx is dtable is workspace is stream is None:
         q, k, cols = y if y.__class__ is Ckpt8 else (y, None, None)
@@ -1018,6 +1018,17 @@ def softmax_rel_bwd(dy, y, table, max_distance: int = 128, bidirectional: bool =
         if status:
             _check(name, status)
     return dx, dtable
+
+
+def softmax_rel_workspace_bytes(buckets: int, heads: int, bidirectional: bool = True) -> int:
+    """Bytes of workspace :func:`softmax_rel_bwd` needs on the current device for the gradient of a [buckets,
+    heads] table, whatever the scores' sizes."""
+    if bidirectional and buckets % 2:
+        raise ValueError("bidirectional buckets come in pairs")
+    n = (buckets // 2 if bidirectional else buckets) - 1
+    edges = (ctypes.c_int32 * max(n, 0))(*[1] * max(n, 0))  # (their places do not matter)
+    rel = _REL.pack(1, heads, 1, 1, 0, ctypes.addressof(edges), 0, 0, n, 0, bool(bidirectional), 0, 1.0)
+    return int(lib().ln_softmax_rel_workspace_bytes_f32(rel))
 
 
 def dropout_keep_bytes(rows: int, cols: int) -> int:

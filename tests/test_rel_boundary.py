@@ -267,3 +267,10 @@ def test_the_library_is_built_whatever_comes_of_the_module(monkeypatch, tmp_path
     (tmp_path / "libln.so").unlink()
     monkeypatch.setattr(lnbuild.shutil, "which", lambda name: None)
     assert lnbuild.build(force=True) == str(tmp_path / "libln.so") and (tmp_path / "libln.so").exists()
+
+
+def test_workspace_size_refuses(lib):
+    with pytest.raises(ValueError):
+        ln.softmax_rel_workspace_bytes(31, 4)
+    for buckets, heads, both in ((0, 4, True), (32, 0, True), (514, 4, True), (257, 4, False), (32, 65537, False)):
+        assert ln.softmax_rel_workspace_bytes(buckets, heads, both) == 0

@@ -429,3 +429,15 @@ def test_the_same_without_the_extension_module(monkeypatch):
     monkeypatch.setattr(ln, "_binding", ln._NoBinding)
     got = calls()
     assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("buckets,both", [(32, True), (7, False), (256, False), (512, True)])
+def test_workspace_of_the_size_asked_for(buckets, both):
+    c = Case("f32", (2, 3, 60, 130), buckets, 600, both, seed=28)
+    y, _ = ln.softmax_rel_fwd(c.x, c.table, **c.how)
+    nbytes = ln.softmax_rel_workspace_bytes(buckets, 3, both)
+    guard = torch.full((nbytes + 256,), 171, dtype=torch.uint8, device="cuda")
+    c.check_bwd(ln.softmax_rel_bwd(c.dy, y, c.table, workspace=guard[:nbytes], **c.how), to64(y))
+    assert (guard[nbytes:] == 171).all()
+    with pytest.raises(ln.LnError, match="ENOSPACE"):
+        ln.softmax_rel_bwd(c.dy, y, c.table, workspace=guard[:nbytes - 1], **c.how)
