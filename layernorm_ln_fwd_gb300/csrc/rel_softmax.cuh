@@ -983,8 +983,12 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
 template <typename T, bool BWD, bool CKPT, int MODE, bool SLOTS, int I>
 const void* rel_kernel_of() {
     constexpr RelShape s = kRelShapes[I];
-    if constexpr ((SLOTS && s.loop) || (!SLOTS && s.teams > 1) || (BWD && MODE == kRelShifted && s.lanes < 32))
-        return nullptr;  // rows in tiles have one window, and one window one team
+    // Rows in tiles have one window, and one window blocks of a team of several warps; the backward's shifted rows have a
+    // warp at least, and in bf16 more than 32 vectors.
+    constexpr bool shifted_back = BWD && MODE == kRelShifted;
+    if constexpr ((SLOTS && s.loop) || (!SLOTS && (s.teams > 1 || s.lanes == 32)) || (shifted_back && s.lanes < 32) ||
+                  (shifted_back && Io<T>::kVec == 8 && s.lanes * s.nv <= 32))
+        return nullptr;
     else if constexpr (BWD)
         return (const void*)rel_bwd_kernel<T, s.lanes, s.teams, s.nv, s.loop, CKPT, MODE, SLOTS>;
     else
