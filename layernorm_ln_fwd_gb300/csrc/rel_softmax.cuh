@@ -639,6 +639,16 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
 // Backward.
 // ---------------------------------------------------------------------------------------
 
+// A vector times a power of two.
+template <typename T>
+__device__ __forceinline__ uint4 rel_times(const uint4& u, float f) {
+    f2 v[Pairs<T>::kPairs];
+    Pairs<T>::unpack(u, v);
+#pragma unroll
+    for (int h = 0; h < Pairs<T>::kPairs; ++h) v[h] = f2_mul(v[h], f2_splat(f));
+    return Pairs<T>::pack(v);
+}
+
 // A row's probabilities: stored in T, or in 8 bits.
 template <typename T, bool CKPT>
 struct Probs {
@@ -646,6 +656,7 @@ struct Probs {
     __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void first(int count) { u = first_of<T>(u, count); }
     __device__ __forceinline__ void values(f2 (&v)[Pairs<T>::kPairs]) const { Pairs<T>::unpack(u, v); }
+    __device__ __forceinline__ void twice() { u = rel_times<T>(u, 2.f); }
 };
 template <typename T>
 struct Probs<T, true> {
@@ -653,6 +664,7 @@ struct Probs<T, true> {
     __device__ __forceinline__ void clear() { r.clear(); }
     __device__ __forceinline__ void first(int count) { r.first(count); }
     __device__ __forceinline__ void values(f2 (&v)[Pairs<T>::kPairs]) const { r.values(v); }
+    __device__ __forceinline__ void twice() { r.k += r.k - 1u < 253u; }  // (the step; 0 and 255 have none)
 };
 
 // 0 where y is, whatever g is.
@@ -852,27 +864,22 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
             float s = row_sum(std::false_type{});
             // A sum that is not finite (an infinite or NaN dy, perhaps at a key of weight 0, where it must
             // not count) is formed again without such keys.  From 2^103 on its difference from a finite dy may pass fp32's
-            // range: halves are subtracted there.
+            // range: twice y and halves of dy and of the sum take their places.
             constexpr float kFar = 0x1p103f;
             const bool careful = L < 32 ? __any_sync(kFullMask, !(fabsf(s) < kFar)) : !(fabsf(s) < kFar);
             bool far = false;
             auto halve = [&] {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    f2 d[H];
-                    Pairs<T>::unpack(g[k], d);
-#pragma unroll
-                    for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_mul(d[h2], f2_splat(0.5f));
-                    g[k] = Pairs<T>::pack(d);
+                    g[k] = rel_times<T>(g[k], 0.5f);
+                    pr[k].twice();
                 }
             };
             if (careful) {
                 s = row_sum(std::true_type{});
                 far = !(fabsf(s) < kFar);
-                if (far) {
-                    s *= 0.5f;
-                    if (!LOOP) halve();
-                }
+                if (far) s *= 0.5f;
+                if (!LOOP && far) halve();
             }
             if constexpr (STAGED) issue(ahead);  // (what was there has been used)
             const f2 s2 = f2_splat(s);
@@ -892,10 +899,6 @@ __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)
 #pragma unroll
                         for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_mul(y[h2], f2_sub(d[h2], s2));
                         if (careful) {
-                            if (far) {
-#pragma unroll
-                                for (int h2 = 0; h2 < H; ++h2) d[h2] = f2_add(d[h2], d[h2]);
-                            }
 #pragma unroll
                             for (int h2 = 0; h2 < H; ++h2) {
                                 d[h2] = where_weight(y[h2], d[h2]);
