@@ -12,7 +12,7 @@
 // 32 interleaved groups and then the groups, with their rounding errors carried along.  No atomics: results are the
 // same from run to run.
 //
-// LayerNorm, bf16 65536 x 768: 53 us, 0.70 of the measured copy rate; RMSNorm 4096 x 8192 38.5 us, 0.65, fp32 4096 x 4096 32
+// LayerNorm, bf16 65536 x 768: 53 us, 0.70 of the measured copy rate; RMSNorm 4096 x 8192 38.7 us, 0.64, fp32 4096 x 4096 32
 // us, 0.69.  Small calls (8192 x 768: 12.5 us for 4.7 of traffic) are bound by what comes once: the first rows' way, a
 // block's column sums, the second launch.  LayerNorm beyond 24 columns a lane (bf16 4096 x 8192: 52 us, 0.48) by the second
 // conversion of its integers, for which two column sums leave no registers.
@@ -29,7 +29,7 @@ namespace {
 
 // Rows of a team in shared memory or on their way there: 3, in fp32 2, where they fit beside gamma.  More do no
 // good: LayerNorm, bf16 65536 x 768, with 2, 3, 4: 54.5, 53.1, 53.8 us; 65536 x 1001 125, 129, 137; RMSNorm, fp32 4096
-// x 4096 32.4, 38.5, 39.9.
+// x 4096 32.4, 38.5, 39.9.  (Odd rows alone would do with 2; aligned ones decide.)
 __host__ __device__ constexpr int cn_stages(int lanes, int teams, int nv, int V) {
     const int gamma = lanes * nv * V * 4, row = teams * ((lanes * nv + 1) * 16 + lanes * nv * V);
     return V == 8 && gamma + 3 * row <= 220 * 1024 ? 3 : 2;

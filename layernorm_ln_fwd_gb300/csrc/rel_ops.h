@@ -53,8 +53,14 @@ constexpr int kRelShapeCount = sizeof(kRelShapes) / sizeof(kRelShapes[0]);
 // The window in shared memory as slots (rel_softmax.cuh): how many, and groups of V entries of each.
 __host__ __device__ constexpr int rel_slot_count(int teams) { return teams > 8 ? teams : 8; }
 __host__ __device__ constexpr int rel_groups(int span, int V) { return (span - 1 + 2 * V - 1 + V - 1) / V + 1; }
-constexpr int kRelSlotBytes = 48 * 1024;  // of all slots at most
-constexpr int kRelShiftedBytes = 64 * 1024;  // in the backward of shifted rows, with slots for each team
+// Bytes of all slots at most.  bf16, 12 heads, 16 x 512 x 512 with 400 distances a side, in slots and with what fits in 24 KB:
+// forward 35.7 and 37.8 us, backward 58 and 61; 4 x 1024 x 1024 with 800 36 and 157 (one window), 64 and 170.  64 KB measures
+// the same up to there.
+constexpr int kRelSlotBytes = 48 * 1024;
+// In the backward of shifted rows, with slots for each team: 32, 64, 96 KB (the window that does not fit is moved rows'),
+// 4 x 1001 x 1001 with 150 distances a side 86, 70, 70 us, with 250 92, 92, 79; 16 x 501 x 501 with 150 92, 84, 84, with 250
+// 96, 96, 103.
+constexpr int kRelShiftedBytes = 64 * 1024;
 
 constexpr int kRelMaxPerSm = 8;  // resident blocks of any shape that a launch uses
 

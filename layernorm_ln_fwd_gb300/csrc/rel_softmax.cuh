@@ -165,7 +165,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // elements into a chunk is "place" c + sh, and its position p counts as p + sh, so that the distances are the
 // same.  Only a row's first and last chunk are partly others'.  kRelAny: whatever else (tensors that lie differently,
 // checkpoints of rows that are not of whole vectors, rows in tiles), moved into columns: two loads a vector and its
-// stores put together from two lanes'.  bf16 16 x 12 x 501 x 501: 46 us shifted, 70 moved; backward 86 and 92.
+// stores put together from two lanes'.  bf16 16 x 12 x 501 x 501: 44 us shifted, 70 moved; backward 86 and 92.
 constexpr int kRelAny = 0, kRelWhole = 1, kRelShifted = 2;
 
 // Blocks an SM that the registers are to allow (rel_shape has figures; rows that are moved hold two chunks a vector).
@@ -365,7 +365,7 @@ struct RelWindow {
 //
 // One read of the scores, one write of the probabilities: bf16 16 x 12 x 512 x 512 with lengths 34.4 us, 0.81 of the
 // measured copy rate; in full 0.86.  What is left is issue: a vector is unpacked, given its bias (two 128-bit shared loads),
-// 8 exponents, and packed.  A decode step (bf16 64 x 16 x 1 x 4096 with lengths) takes 6.8 us for 2.3 of traffic: a launch,
+// 8 exponents, and packed.  A decode step (bf16 64 x 16 x 1 x 4096 with lengths) takes 6.9 us for 2.3 of traffic: a launch,
 // and a row's time from its first load to its last store.
 template <typename T, int LPR, int TEAMS, int NV, bool LOOP, bool CKPT, int MODE, bool SLOTS>
 __global__ void __launch_bounds__(LPR* TEAMS, rel_resident(LPR, TEAMS, NV, MODE)) rel_fwd_kernel(const __grid_constant__ RelParams p) {

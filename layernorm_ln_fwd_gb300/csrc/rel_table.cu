@@ -68,11 +68,12 @@ bool rel_single(int Lq, int nvec, int span, int64_t rows) {
 //   128 x 128 (x 256 sequences)        8 lanes x 2 37 / 57      a warp x 1                 109 / 123
 //   256 x 256 (x 64)                   16 lanes x 2 36 / 57     a warp x 1                 51 / 64
 //   512 x 512 (x 16)                   16 lanes x 4 34.5 / 57   a warp x 2                 37 / 57
-//   1024 x 1024 (x 4)                  a warp x 4 35 / 58       8 warps x 1                114 / 103
-//   2048 x 2048 (x 2)                  2 warps x 4 72 / 106     8 warps x 1                135 / 127
-//   4096 x 4096                        4 warps x 4 142 / 204    8 warps x 2                172 / 189
-//   the last, causal                                120 / 148                              152 / 157
-// The backward's full rows beyond 384 vectors alone are better off with 8 warps.  Four vectors a lane take 80
+//   1024 x 1024 (x 4)                  a warp x 4 35 / 59       8 warps x 1                114 / 103
+//   2048 x 2048 (x 2)                  2 warps x 4 72 / 108     8 warps x 1                135 / 127
+//   4096 x 4096                        4 warps x 4 144 / 204    8 warps x 2                172 / 189
+//   the last, causal                                122 / 145                              152 / 157
+// The backward's full rows beyond 384 vectors alone go to 8 warps (8 and 4 warps: 288 vectors 83 and 74 us, 320 94 and 84, 360
+// 112 and 101; 400 131 and 120, 448 152 and 148, so that the border could lie higher; 512 189 and 204).  Four vectors a lane take 80
 // registers, three blocks an SM (rel_resident): held to 64 they spill, and the same take 34.5 -> 38, 35 -> 40, 72 -> 80.
 int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, bool causal, bool* slots) {
     const int nvec = (Lk + V - 1) / V;
@@ -87,8 +88,8 @@ int rel_shape(int V, int64_t rows, int Lq, int Lk, int span, bool bwd, bool caus
     return nvec <= 256 ? 0 : nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 3 : 4;
 }
 
-// The same for shifted rows (bf16, 12 heads, 501 x 501 x 16: parts of a warp 46 us forward, a warp 56; 4001 x 4001: 4
-// warps 189 / 210, 8 warps 219 / 242).  In the backward a warp holds a row at least: parts of one would take too many
+// The same for shifted rows (bf16, 12 heads, 501 x 501 x 16: parts of a warp 44 us forward, a warp 56; 4001 x 4001: 4
+// warps 190 / 212, 8 warps 219 / 242).  In the backward a warp holds a row at least: parts of one would take too many
 // slots.  In bf16 rows of up to 32 vectors are better moved, by parts of a warp (32 heads, shifted and moved: 32 x
 // 65 x 65 49 and 35 us, 16 x 138 x 138 causal 49 and 42, 16 x 201 x 201 66 and 61, 8 x 283 x 283 causal 57 and 56, 8 x 501 x
 // 501 causal 93 and 104; fp32 16 x 101 x 101 28 and 28, 8 x 201 x 201 37 and 46).
