@@ -1,5 +1,10 @@
 """The softmax with a learned relative position bias on the GPU, against 64 bits (relref has the reference and
 where the tolerances come from)."""
+import ctypes
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -441,3 +446,57 @@ def test_workspace_of_the_size_asked_for(buckets, both):
     assert (guard[nbytes:] == 171).all()
     with pytest.raises(ln.LnError, match="ENOSPACE"):
         ln.softmax_rel_bwd(c.dy, y, c.table, workspace=guard[:nbytes - 1], **c.how)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("both", [False, True])
+@pytest.mark.parametrize("edges", [(), (1,), (1, 1, 5, 5, 7), (40, 40), (3, 100, 16384)])
+def test_edges_of_any_kind_through_the_c_abi(dtype, both, edges):
+    """No edges, edges that fall together (buckets without a distance), and ones behind all rows."""
+    B, H, Lq, Lk = 2, 3, 21, 90
+    g = torch.Generator().manual_seed(29)
+    x, dy = (rows_of((B, H, Lq, Lk), dtype, g) for _ in range(2))
+    buckets = (len(edges) + 1) * (2 if both else 1)
+    table = torch.randn(buckets, H, generator=g).to(TYPES[dtype]).cuda()
+    q_pos = torch.tensor([0, 60], dtype=torch.int32).cuda()
+    array = (ctypes.c_int32 * max(1, len(edges)))(*edges)
+    rel = ln._REL.pack(B, H, Lq, Lk, table.data_ptr(), ctypes.addressof(array) if edges else 0, 0, q_pos.data_ptr(),
+                       len(edges), dtype == "f32", both, 0, 0.5)
+    y, dx, dt = torch.empty_like(x), torch.empty_like(dy), torch.empty_like(table)
+    lib, stream = ln.lib(), torch.cuda.current_stream().cuda_stream
+    nbytes = getattr(lib, f"ln_softmax_rel_workspace_bytes_{dtype}")(rel)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    assert getattr(lib, f"ln_softmax_rel_fwd_{dtype}")(rel, x.data_ptr(), Lk, None, 1, y.data_ptr(), Lk, None, None, stream) == 0
+    assert getattr(lib, f"ln_softmax_rel_bwd_{dtype}")(rel, dy.data_ptr(), Lk, y.data_ptr(), Lk, None, None, dx.data_ptr(), Lk,
+                                                       dt.data_ptr(), ws.data_ptr(), nbytes, stream) == 0
+    y64, tol, bk, kept = relref.fwd(to64(x), to64(table), edges, both, 0.5, q_pos=[0, 60])
+    relref.close("y", to64(y), y64, relref.stored(tol, y64, dtype))
+    want = relref.bwd(to64(dy), to64(y), bk, kept, buckets, 0.5)
+    relref.close("dx", to64(dx), want[0], relref.stored(want[1], want[0], dtype))
+    relref.close("dtable", to64(dt), want[2], relref.stored(want[3], want[2], dtype))
+
+
+def test_a_first_call_captured():
+    """A process whose first calls are captured into a graph."""
+    code = """
+import torch, layernorm_ln_fwd_gb300 as ln
+x = torch.randn(2, 3, 40, 300, device="cuda"); table = torch.randn(32, 3, device="cuda")
+long = torch.randn(1, 1, 1, 70001, device="cuda")
+gamma, stats = torch.ones(300, device="cuda"), torch.ones(240, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def step():
+    y, ck = ln.softmax_rel_fwd(x, table, ckpt=True)
+    return (y, *ln.softmax_rel_bwd(x, ck, table), *ln.softmax_rel_bwd(x, y, table), ln.softmax_rel_fwd(long, table[:, :1].contiguous())[0],
+            ln.ckpt8_load(ln.ckpt8_store(x.view(240, 300))), *ln.bwd_ckpt8(x.view(240, 300), ck, gamma, stats, stats),
+            *ln.rms_bwd_ckpt8(x.view(240, 300), ck, gamma, stats))
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0 and done.stdout.strip().endswith("same"), done.stderr[-2000:]
